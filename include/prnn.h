@@ -97,6 +97,7 @@ typedef enum {
 typedef enum {
   PRNN_DATA_FLOAT = 0, /* fp32 */
   PRNN_DATA_HALF = 1,  /* fp16 (IEEE binary16); products and sums are taken in fp32 */
+  PRNN_DATA_BFLOAT = 2, /* bfloat16: linear attention and layer norm only (BAD_PARAM elsewhere) */
   PRNN_DATA_MAX_ENUM = 0x7FFFFFFF  /* not a value: keeps every int in the type's range */
 } prnnDataType_t;
 
@@ -540,6 +541,125 @@ prnnStatus_t prnn_debug_skip_publish(prnnHandle_t handle, int wg, int step);
  * watchdog (prnn_set_watchdog_us) make the run report EXECUTION_FAILED. */
 #define PRNN_DEBUG_JITTER_MAX 1024
 prnnStatus_t prnn_debug_jitter(prnnHandle_t handle, uint32_t seed, int span);
+
+/* Linear attention with a decay for each head: the recurrence of a retentive
+ * layer, whose state is a Dk x Dv matrix per batch row and head.
+ *
+ *     S[t] = exp(log_decay[h]) S[t-1] + k[t] v[t]^T,   S[-1] = S0 or zeros
+ *     o[t] = scale * S[t]^T q[t]
+ *
+ * Head h of q, o, the decay and the state uses head h / (H / Hkv) of k and v.
+ * The decays are constants of the layer (exp(log_decay) <= 1 in use; any fp32
+ * value is taken as it is, -infinity forgets everything before the token);
+ * they have no gradient.  States are fp32 and dense, [B][H][Dk][Dv]; sums are
+ * fp32, and the products of 16-bit operands see every operand whole and the
+ * decayed scores and the state to 2^-16 or better.  A row of o depends on no
+ * later token, whatever that holds (infinities and NaN included). */
+typedef struct {
+  int B;                    /* sequences                                        */
+  int T;                    /* tokens of the longest sequence                   */
+  int H, Hkv;               /* heads; key-value heads, H a multiple of Hkv      */
+  int Dk, Dv;               /* head sizes, 1 .. PRNN_ATTENTION_MAX_D            */
+  prnnDataType_t type;      /* of q, k, v, o and their gradients                */
+  float scale;
+  const float* log_decay;   /* [H], device                                      */
+  /* Sequences of unequal length, one of (both NULL: every sequence has T tokens):
+   *  lengths: int32 [B], device: sequence b is its first lengths[b] tokens
+   *    (below 0 counts as 0, above T as T); rows of the outputs past it are
+   *    written as zeros.
+   *  offsets: int32 [B + 1], device: packed sequences, b the rows offsets[b] ..
+   *    offsets[b + 1] - 1 of the token axis (batch strides are not used);
+   *    `rows` is the length of that axis.  Offsets are clamped to [0, rows]
+   *    and lengths to [0, T]; rows of the outputs that no sequence covers are
+   *    not written. */
+  const int32_t* lengths;
+  const int32_t* offsets;
+  int64_t rows;
+} prnnAttention_t;
+
+#define PRNN_ATTENTION_MAX_D 256
+
+/* One sequence operand: element (t, b, head, d) lies at
+ * data[t * token + b * batch + head * head + d] (strides in elements, not
+ * negative; any order, so time-first, batch-first and slices of one fused
+ * projection all work).  Strides of inputs may be 0; elements of an output
+ * must not coincide.  Base and strides that are multiples of 16 bytes are
+ * loaded in vectors, any others element by element. */
+typedef struct {
+  void* data;
+  int64_t token, batch, head;
+} prnnSequence_t;
+
+/* The whole of a prompt (chunks of tokens on the matrix cores).  S0: initial
+ * states or NULL; S1: receives the states after each sequence's last token, or
+ * NULL; S1 may be S0.  A sequence of no tokens leaves S1 = S0 (zeros).
+ * Few sequences and heads are split along the tokens over more workgroups;
+ * the handle keeps the workspace for that (grown outside stream capture:
+ * NOT_SUPPORTED where it would have to grow while capturing).
+ * BAD_PARAM: NULL handle or descriptor; B, T < 0; H, Hkv, Dk or Dv < 1, Dk or
+ * Dv above PRNN_ATTENTION_MAX_D, H not a multiple of Hkv; unknown type; NULL
+ * or misaligned pointers (elements: their type's size; states: 4 bytes),
+ * negative strides, both lengths and offsets, rows < 0; an output that
+ * overlaps itself, an input or another output (slices of one buffer whose
+ * rows interleave are fine).  NOT_SUPPORTED: a token stride above 2^23
+ * elements; more workgroups than a grid holds.
+ * B == 0 does nothing; T == 0 only passes the states on. */
+prnnStatus_t prnn_linear_attention(prnnHandle_t handle, const prnnAttention_t* attention, const prnnSequence_t* q,
+                                   const prnnSequence_t* k, const prnnSequence_t* v, const float* S0,
+                                   const prnnSequence_t* o, float* S1, hipStream_t stream);
+
+/* Gradients of prnn_linear_attention: do_ the gradient of o, dS1 that of S1
+ * (or NULL), the inputs as they were; writes dq [..][H][Dk], dk [..][Hkv][Dk]
+ * and dv [..][Hkv][Dv] (sums over a shared head's group, added in fp32 in a
+ * fixed order) and, unless NULL, dS0 (which may be dS1).  Each of the three is
+ * itself a linear attention: dq of (do, v, k), and backwards in time dk of (v,
+ * do, q) and dv of (k, q, do).  Errors as prnn_linear_attention. */
+prnnStatus_t prnn_linear_attention_backward(prnnHandle_t handle, const prnnAttention_t* attention,
+                                            const prnnSequence_t* q, const prnnSequence_t* k, const prnnSequence_t* v,
+                                            const float* S0, const prnnSequence_t* do_, const float* dS1,
+                                            const prnnSequence_t* dq, const prnnSequence_t* dk,
+                                            const prnnSequence_t* dv, float* dS0, hipStream_t stream);
+
+/* One new token of every sequence: S1 = exp(log_decay) S0 + k v^T and o =
+ * scale S1^T q.  T, lengths, offsets, rows and the token strides are not used.
+ * S1 may be S0 (the usual form: the state is updated in place).  Errors as
+ * prnn_linear_attention; S0 and S1 must not be NULL. */
+prnnStatus_t prnn_linear_attention_step(prnnHandle_t handle, const prnnAttention_t* attention,
+                                        const prnnSequence_t* q, const prnnSequence_t* k, const prnnSequence_t* v,
+                                        const float* S0, const prnnSequence_t* o, float* S1, hipStream_t stream);
+
+/* Layer norm over the last axis of M rows of N:
+ *
+ *     y[m][n] = (x[m][n] - mean[m]) * rstd[m] * weight[n] + bias[n],
+ *     rstd[m] = 1 / sqrt(var[m] + eps), var the mean of (x - mean)^2
+ *
+ * x and y of `type`, rows ldx and ldy elements apart (>= N); weight and bias
+ * [N] of `param_type` (PRNN_DATA_FLOAT or `type`), either or both NULL (ones,
+ * zeros); mean and rstd [M] fp32, or NULL where they are not wanted.  y may be
+ * x (same ld).  Statistics and sums are fp32 over centred values.
+ * BAD_PARAM: NULL handle, x or y (M > 0); M < 0, N < 1, ld < N; eps < 0 or NaN;
+ * unknown or unsupported types; misaligned pointers; y overlapping x (unless
+ * equal), weight or bias; mean or rstd overlapping any other buffer.
+ * M == 0 does nothing. */
+prnnStatus_t prnn_layer_norm(prnnHandle_t handle, int64_t M, int N, prnnDataType_t type, const void* x, int64_t ldx,
+                             prnnDataType_t param_type, const void* weight, const void* bias, float eps, void* y,
+                             int64_t ldy, float* mean, float* rstd, hipStream_t stream);
+
+/* Gradients of prnn_layer_norm from the statistics it left, with
+ * n = (x - mean) rstd and g = dy weight:
+ *
+ *     dx = rstd (g - mean_n(g) - n mean_n(g n)),  dweight = sum_m dy n,
+ *     dbias = sum_m dy
+ *
+ * dx may be dy or x (same ld), or NULL; dweight and dbias [N] of param_type,
+ * either or both NULL; weight NULL means ones.  The sums over the rows are
+ * fp32 in a fixed order (partial sums in the handle's workspace; see
+ * prnn_linear_attention for its growth).  M == 0 writes zeros to dweight and
+ * dbias.  Errors as prnn_layer_norm, for these buffers. */
+prnnStatus_t prnn_layer_norm_backward(prnnHandle_t handle, int64_t M, int N, prnnDataType_t type, const void* dy,
+                                      int64_t lddy, const void* x, int64_t ldx, const float* mean, const float* rstd,
+                                      prnnDataType_t param_type, const void* weight, void* dx, int64_t lddx,
+                                      void* dweight, void* dbias, hipStream_t stream);
 
 /* For callers that cannot allocate device memory: code under HIP graph
  * capture, tight serving loops, harnesses that forbid allocation.

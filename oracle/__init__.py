@@ -28,3 +28,9 @@ from .layer import (  # noqa: F401
     forward_stack_sparse,
     project,
 )
+from .sequence import (  # noqa: F401
+    layer_norm,
+    layer_norm_backward,
+    linear_attention,
+    linear_attention_backward,
+)

@@ -25,7 +25,7 @@ STATUS_NAMES = {
     5: "PRNN_STATUS_INTERNAL_ERROR",
 }
 SUCCESS, BAD_PARAM, NOT_SUPPORTED, ALLOC_FAILED, EXECUTION_FAILED, INTERNAL_ERROR = range(6)
-DATA_FLOAT, DATA_HALF = 0, 1
+DATA_FLOAT, DATA_HALF, DATA_BFLOAT = 0, 1, 2
 EXCHANGE_AUTO, EXCHANGE_DIRECT, EXCHANGE_RELAY = 0, 1, 2
 LAYOUT_AUTO, LAYOUT_SPREAD, LAYOUT_TEAM = 0, 1, 2
 MATH_AUTO, MATH_EXACT, MATH_SPLIT, MATH_HALF = 0, 1, 2, 3
@@ -37,6 +37,7 @@ TRACE_WORDS = 8  # per-wave trace record: see Handle.get_trace
 _H = ctypes.c_void_p
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 SIGNATURES = {
     "prnn_create": (_I, [ctypes.POINTER(_H)]),
     "prnn_destroy": (_I, [_H]),
@@ -66,7 +67,43 @@ SIGNATURES = {
     "prnn_set_stack_mode": (_I, [_H, _I]),
     "prnn_set_launch": (_I, [_H, _I]),
     "prnn_forward_dense_noalloc": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "prnn_linear_attention": (_I, [_H, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "prnn_linear_attention_backward": (_I, [_H, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "prnn_linear_attention_step": (_I, [_H, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "prnn_layer_norm": (_I, [_H, _L, _I, _I, _P, _L, _I, _P, _P, ctypes.c_float, _P, _L, _P, _P, _P]),
+    "prnn_layer_norm_backward": (_I, [_H, _L, _I, _I, _P, _L, _P, _L, _P, _P, _I, _P, _P, _L, _P, _P, _P]),
 }
+
+ATTENTION_MAX_D = 256  # PRNN_ATTENTION_MAX_D
+SEQUENCE_TYPES = {torch.float32: DATA_FLOAT, torch.float16: DATA_HALF, torch.bfloat16: DATA_BFLOAT}
+
+
+class Attention(ctypes.Structure):
+    """prnnAttention_t."""
+    _fields_ = [
+        ("B", ctypes.c_int),
+        ("T", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("Hkv", ctypes.c_int),
+        ("Dk", ctypes.c_int),
+        ("Dv", ctypes.c_int),
+        ("type", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("log_decay", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("offsets", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+    ]
+
+
+class Sequence(ctypes.Structure):
+    """prnnSequence_t."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("token", ctypes.c_int64),
+        ("batch", ctypes.c_int64),
+        ("head", ctypes.c_int64),
+    ]
 
 
 class PlanInfo(ctypes.Structure):
@@ -135,6 +172,38 @@ def _need(t: torch.Tensor, name: str, dtypes, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _need_strided(t: torch.Tensor, name: str, device: torch.device, dtypes, shape):
+    """_need for a tensor whose rows may lie at any strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+
+
+def _empty(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A new output that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return t.data_ptr() if t is not None else None
+
+
+def _sequence(t: torch.Tensor, axes) -> Sequence:
+    """axes: the tensor's axis of the tokens and of the batch (None: it has none)."""
+    token, batch = (t.stride(a) if a is not None and t.shape[a] > 1 else 0 for a in axes)
+    return Sequence(t.data_ptr(), token, batch, t.stride(-2) if t.shape[-2] > 1 else 0)
 
 
 class Handle:
@@ -445,6 +514,191 @@ class Handle:
                                                  workspace.data_ptr(), Hp, _stream_ptr(stream))
         _check("prnn_forward_stack_sparse", st)
         return outs
+
+    # -- linear attention with a decay for each head -------------------------
+    def _attention(self, q, k, v, log_decay, scale, offsets, lengths, max_len, step):
+        """Checks the inputs; the descriptor, the axes of tokens and batch, the
+        leading shape of q and the shape of the states."""
+        lead = 1 if step or offsets is not None else 2
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor) or t.dim() != lead + 2:
+                raise ValueError(f"{name} must have {lead + 2} axes")
+        H, Dk = q.shape[-2:]
+        Hkv, Dv = v.shape[-2:]
+        rows = tuple(q.shape[:-2])
+        if q.dtype not in SEQUENCE_TYPES:
+            raise TypeError(f"q must have dtype in {tuple(SEQUENCE_TYPES)}, got {q.dtype}")
+        _need_strided(q, "q", self.device, (q.dtype,), rows + (H, Dk))
+        _need_strided(k, "k", self.device, (q.dtype,), rows + (Hkv, Dk))
+        _need_strided(v, "v", self.device, (q.dtype,), rows + (Hkv, Dv))
+        _need(log_decay, "log_decay", (torch.float32,), (H,))
+        if offsets is not None and lengths is not None:
+            raise ValueError("give offsets (packed sequences) or lengths, not both")
+        a = Attention(H=H, Hkv=Hkv, Dk=Dk, Dv=Dv, type=SEQUENCE_TYPES[q.dtype],
+                      scale=Dk ** -0.5 if scale is None else scale, log_decay=log_decay.data_ptr())
+        if step:
+            a.B, a.T, axes = rows[0], 1, (None, 0)
+        elif offsets is not None:
+            if offsets.dim() != 1 or offsets.shape[0] < 1:
+                raise ValueError("offsets must be [B + 1]")
+            _need(offsets, "offsets", (torch.int32,), offsets.shape)
+            a.B, a.T, a.rows = offsets.shape[0] - 1, rows[0] if max_len is None else int(max_len), rows[0]
+            a.offsets, axes = offsets.data_ptr(), (0, None)
+        else:
+            a.T, a.B = rows
+            axes = (0, 1)
+            if lengths is not None:
+                _need(lengths, "lengths", (torch.int32,), (a.B,))
+                a.lengths = lengths.data_ptr()
+        return a, axes, rows, (a.B, H, Dk, Dv)
+
+    def _sequence_out(self, out, name, dtype, shape, stream):
+        if out is None:
+            return _empty(shape, dtype, self.device, stream)
+        _need_strided(out, name, self.device, (dtype,), shape)
+        return out
+
+    def linear_attention(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
+                         scale: Optional[float] = None, initial_state: Optional[torch.Tensor] = None,
+                         final_state: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+                         lengths: Optional[torch.Tensor] = None, max_len: Optional[int] = None,
+                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """S[t] = exp(log_decay) S[t-1] + k[t] v[t]^T, o[t] = scale S[t]^T q[t] for whole sequences.
+
+        q [T, B, H, Dk], k [T, B, Hkv, Dk], v [T, B, Hkv, Dv] (fp32, fp16 or
+        bf16; any strides with a contiguous last axis) give o [T, B, H, Dv];
+        log_decay fp32 [H]; scale None: Dk ** -0.5.  Sequences of unequal length:
+        ``lengths`` int32 [B] (rows of o past them are zeros), or packed
+        sequences, the tensors [rows, heads, D], with ``offsets`` int32 [B + 1]
+        and max_len the longest sequence's tokens (None: rows).
+        initial_state (None: zeros) and final_state (written, may be the
+        initial one) are fp32 [B, H, Dk, Dv]."""
+        a, axes, rows, state = self._attention(q, k, v, log_decay, scale, offsets, lengths, max_len, False)
+        for t, name in ((initial_state, "initial_state"), (final_state, "final_state")):
+            if t is not None:
+                _need(t, name, (torch.float32,), state)
+        out = self._sequence_out(out, "out", q.dtype, rows + (a.H, a.Dv), stream)
+        seqs = [_sequence(t, axes) for t in (q, k, v, out)]
+        r = [ctypes.byref(x) for x in seqs]
+        _check("prnn_linear_attention", self._lib.prnn_linear_attention(
+            self._h, ctypes.byref(a), r[0], r[1], r[2], _ptr(initial_state), r[3], _ptr(final_state),
+            _stream_ptr(stream)))
+        return out
+
+    def linear_attention_backward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                                  grad_out: torch.Tensor, *, scale: Optional[float] = None,
+                                  initial_state: Optional[torch.Tensor] = None,
+                                  grad_final_state: Optional[torch.Tensor] = None,
+                                  grad_initial_state: Optional[torch.Tensor] = None,
+                                  offsets: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                                  max_len: Optional[int] = None, grad_q: Optional[torch.Tensor] = None,
+                                  grad_k: Optional[torch.Tensor] = None, grad_v: Optional[torch.Tensor] = None,
+                                  stream=None):
+        """Gradients of linear_attention: (dq, dk, dv), and into grad_initial_state
+        where it is given.  The inputs are those of the forward call; the decays
+        are constants."""
+        a, axes, rows, state = self._attention(q, k, v, log_decay, scale, offsets, lengths, max_len, False)
+        _need_strided(grad_out, "grad_out", self.device, (q.dtype,), rows + (a.H, a.Dv))
+        for t, name in ((initial_state, "initial_state"), (grad_final_state, "grad_final_state"),
+                        (grad_initial_state, "grad_initial_state")):
+            if t is not None:
+                _need(t, name, (torch.float32,), state)
+        grads = [self._sequence_out(t, name, q.dtype, of.shape, stream)
+                 for t, name, of in ((grad_q, "grad_q", q), (grad_k, "grad_k", k), (grad_v, "grad_v", v))]
+        seqs = [_sequence(t, axes) for t in (q, k, v, grad_out, *grads)]
+        r = [ctypes.byref(x) for x in seqs]
+        _check("prnn_linear_attention_backward", self._lib.prnn_linear_attention_backward(
+            self._h, ctypes.byref(a), r[0], r[1], r[2], _ptr(initial_state), r[3], _ptr(grad_final_state), r[4], r[5],
+            r[6], _ptr(grad_initial_state), _stream_ptr(stream)))
+        return tuple(grads)
+
+    def linear_attention_step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                              state: torch.Tensor, *, scale: Optional[float] = None,
+                              new_state: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+        """One new token of every sequence: q [B, H, Dk], k [B, Hkv, Dk], v [B, Hkv,
+        Dv] give o [B, H, Dv].  state fp32 [B, H, Dk, Dv] is updated in place, or
+        left as it is and the new one written to new_state."""
+        a, axes, rows, shape = self._attention(q, k, v, log_decay, scale, None, None, None, True)
+        _need(state, "state", (torch.float32,), shape)
+        if new_state is None:
+            new_state = state
+        _need(new_state, "new_state", (torch.float32,), shape)
+        out = self._sequence_out(out, "out", q.dtype, rows + (a.H, a.Dv), stream)
+        seqs = [_sequence(t, axes) for t in (q, k, v, out)]
+        r = [ctypes.byref(x) for x in seqs]
+        _check("prnn_linear_attention_step", self._lib.prnn_linear_attention_step(
+            self._h, ctypes.byref(a), r[0], r[1], r[2], state.data_ptr(), r[3], new_state.data_ptr(),
+            _stream_ptr(stream)))
+        return out
+
+    # -- layer norm -------------------------------------------------------------
+    def _norm_rows(self, t, name, dtypes, shape):
+        """The rows of t [..., N]: how many, and the elements from one to the next."""
+        _need_strided(t, name, self.device, dtypes, shape)
+        N = t.shape[-1]
+        M, ld = 1, N
+        for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+            if size == 1:
+                continue
+            if M == 1:
+                ld = stride
+            elif t.numel() > 0 and stride != ld * M:
+                raise ValueError(f"the rows of {name} must lie at one stride")
+            M *= size
+        return M, max(ld, N) if M <= 1 else ld
+
+    def layer_norm(self, x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                   eps: float = 1e-5, *, out: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                   rstd: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """(x - mean) * rstd * weight + bias over the last axis of x (fp32, fp16 or
+        bf16); weight and bias [N], fp32 or x's dtype, or None.  mean and rstd
+        (fp32, x's shape without its last axis) are written where given, for
+        the backward pass; out may be x."""
+        M, ldx = self._norm_rows(x, "x", tuple(SEQUENCE_TYPES), x.shape)
+        N, lead = x.shape[-1], tuple(x.shape[:-1])
+        pdtype = next((p.dtype for p in (weight, bias) if p is not None), torch.float32)
+        for p, name in ((weight, "weight"), (bias, "bias")):
+            if p is not None:
+                _need(p, name, (pdtype,) if pdtype in (torch.float32, x.dtype) else (torch.float32, x.dtype), (N,))
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            if t is not None:
+                _need(t, name, (torch.float32,), lead)
+        if out is None:
+            out = _empty(x.shape, x.dtype, self.device, stream)
+        _, ldy = self._norm_rows(out, "out", (x.dtype,), x.shape)
+        _check("prnn_layer_norm", self._lib.prnn_layer_norm(
+            self._h, M, N, SEQUENCE_TYPES[x.dtype], x.data_ptr(), ldx, SEQUENCE_TYPES[pdtype], _ptr(weight), _ptr(bias),
+            eps, out.data_ptr(), ldy, _ptr(mean), _ptr(rstd), _stream_ptr(stream)))
+        return out
+
+    def layer_norm_backward(self, grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                            weight: Optional[torch.Tensor] = None, *, grad_x: Optional[torch.Tensor] = None,
+                            grad_weight: Optional[torch.Tensor] = None, grad_bias: Optional[torch.Tensor] = None,
+                            stream=None):
+        """Gradients of layer_norm: (dx, dweight, dbias).  dweight and dbias have
+        weight's dtype; without a weight they are computed only into the
+        buffers given, and are None otherwise."""
+        M, ldx = self._norm_rows(x, "x", tuple(SEQUENCE_TYPES), x.shape)
+        N, lead = x.shape[-1], tuple(x.shape[:-1])
+        _, lddy = self._norm_rows(grad_out, "grad_out", (x.dtype,), x.shape)
+        _need(mean, "mean", (torch.float32,), lead)
+        _need(rstd, "rstd", (torch.float32,), lead)
+        pdtype = next((p.dtype for p in (weight, grad_weight, grad_bias) if p is not None), torch.float32)
+        if weight is not None:
+            grad_weight = _empty((N,), pdtype, self.device, stream) if grad_weight is None else grad_weight
+            grad_bias = _empty((N,), pdtype, self.device, stream) if grad_bias is None else grad_bias
+        for p, name in ((weight, "weight"), (grad_weight, "grad_weight"), (grad_bias, "grad_bias")):
+            if p is not None:
+                _need(p, name, (pdtype,) if pdtype in (torch.float32, x.dtype) else (torch.float32, x.dtype), (N,))
+        if grad_x is None:
+            grad_x = _empty(x.shape, x.dtype, self.device, stream)
+        _, lddx = self._norm_rows(grad_x, "grad_x", (x.dtype,), x.shape)
+        _check("prnn_layer_norm_backward", self._lib.prnn_layer_norm_backward(
+            self._h, M, N, SEQUENCE_TYPES[x.dtype], grad_out.data_ptr(), lddy, x.data_ptr(), ldx, mean.data_ptr(),
+            rstd.data_ptr(), SEQUENCE_TYPES[pdtype], _ptr(weight), grad_x.data_ptr(), lddx, _ptr(grad_weight),
+            _ptr(grad_bias), _stream_ptr(stream)))
+        return grad_x, grad_weight, grad_bias
 
     def sync_floor(self, N: int, B: int, T: int, out: Optional[torch.Tensor] = None,
                    stream=None) -> torch.Tensor:

@@ -13,6 +13,7 @@
 
 #include "host_internal.h"
 #include "kernels.h"
+#include "sequence.h"
 
 using prnn::KernelEntry;
 using prnn::StepArgs;
@@ -85,6 +86,17 @@ struct prnnContext {
   int32_t* d_sorted = nullptr;
   size_t sorted_cap = 0;
   int trace_records = 0;  // records written by the last traced call (0: none)
+  // Workspace of the sequence operators (linear attention, layer norm).  A
+  // captured graph keeps its address, so memory that a captured call used is
+  // put aside when the workspace grows and freed with the handle.
+  struct Block {
+    void* mem;
+    Block* next;
+  };
+  void* d_work = nullptr;
+  size_t work_cap = 0;
+  bool work_captured = false;
+  Block* old_work = nullptr;
 };
 
 namespace {
@@ -853,6 +865,44 @@ prnnStatus_t prepare_layer_projection(prnnContext* h, int N, int I, int B, int T
 
 }  // namespace
 
+bool prnn::handle_failed(prnnContext* h) { return take_failure(h); }
+
+int prnn::handle_compute_units(const prnnContext* h) { return h->num_cu; }
+
+bool prnn::handle_logs(const prnnContext* h) { return h->log; }
+
+prnnStatus_t prnn::handle_workspace(prnnContext* h, size_t bytes, hipStream_t stream, void** out) {
+  hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(stream, &cs) != hipSuccess) return PRNN_STATUS_INTERNAL_ERROR;
+  const bool capturing = cs != hipStreamCaptureStatusNone;
+  if (bytes > h->work_cap) {
+    if (capturing) return PRNN_STATUS_NOT_SUPPORTED;
+    prnnContext::Block* old = nullptr;
+    if (h->work_captured) {
+      old = new (std::nothrow) prnnContext::Block{h->d_work, h->old_work};
+      if (old == nullptr) return PRNN_STATUS_ALLOC_FAILED;
+    } else if (h->d_work != nullptr) {
+      if (hipDeviceSynchronize() != hipSuccess) return PRNN_STATUS_INTERNAL_ERROR;
+      (void)hipFree(h->d_work);
+      h->d_work = nullptr;
+      h->work_cap = 0;
+    }
+    void* mem = nullptr;
+    if (hipMalloc(&mem, bytes) != hipSuccess) {
+      (void)hipGetLastError();
+      delete old;
+      return PRNN_STATUS_ALLOC_FAILED;
+    }
+    if (old != nullptr) h->old_work = old;
+    h->d_work = mem;
+    h->work_cap = bytes;
+    h->work_captured = false;
+  }
+  if (capturing) h->work_captured = true;
+  *out = h->d_work;
+  return PRNN_STATUS_SUCCESS;
+}
+
 prnnStatus_t prnn::forward_dense_on(const DeviceFacts& dev, uint32_t* ring, uint32_t* status, int N, int B, int T,
                                     prnnDataType_t w_type, const void* W, const float* X, const float* h0, float* H,
                                     hipStream_t stream) {
@@ -965,6 +1015,13 @@ prnnStatus_t prnn_destroy(prnnHandle_t h) {
   if (h->d_ring != nullptr) (void)hipFree(h->d_ring);
   if (h->d_trace != nullptr) (void)hipFree(h->d_trace);
   if (h->d_sorted != nullptr) (void)hipFree(h->d_sorted);
+  if (h->d_work != nullptr) (void)hipFree(h->d_work);
+  while (h->old_work != nullptr) {
+    prnnContext::Block* b = h->old_work;
+    h->old_work = b->next;
+    (void)hipFree(b->mem);
+    delete b;
+  }
   if (h->d_status != nullptr) (void)hipFree(h->d_status);
   if (h->h_status != nullptr) (void)hipHostFree(const_cast<uint32_t*>(h->h_status));
   delete h;

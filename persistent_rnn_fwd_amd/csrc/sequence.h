@@ -1,0 +1,138 @@
+// Linear attention and layer norm: kernel arguments, launches and the element
+// types they share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "prnn.h"
+
+namespace prnn {
+
+// -- pieces of the handle these calls use (prnn.cpp) -----------------------------
+bool handle_failed(prnnContext* h);  // an earlier run's failure, reported once
+int handle_compute_units(const prnnContext* h);
+bool handle_logs(const prnnContext* h);
+// At least `bytes` of the handle's workspace.  Grown outside stream capture
+// only (NOT_SUPPORTED while capturing); memory that a captured call uses lives
+// until the handle is destroyed.
+prnnStatus_t handle_workspace(prnnContext* h, size_t bytes, hipStream_t stream, void** out);
+
+// -- linear attention (linear_attention.hip) -------------------------------------
+
+// One operand of a linear attention: strides in elements; head h of the state
+// uses head h / group of the operand.
+struct AttnOperand {
+  const void* p;
+  int64_t token, batch, head;
+  int group;
+};
+
+// One linear attention of a launch, in its own roles: the forward pass is one
+// job, the backward pass three.
+//   S <- decay S + kscale k v^T,  o = oscale S^T q
+// `reverse` walks every sequence from its last token to its first, and takes
+// the initial state as decayed already (and leaves the final one decayed).
+// State element (row of Dk, column of Dv) lies at row * s_row + col * s_col of
+// the [B][H] matrices of Dk Dv elements.
+struct AttnJob {
+  AttnOperand q, k, v, o;
+  const float* s_in;   // or nullptr (zeros)
+  float* s_out;        // or nullptr
+  float* segments;     // split sequences: [segments][B][H][Dk][Dv] states, or nullptr
+  int Dk, Dv;
+  int s_row, s_col;
+  float kscale, oscale;
+  int reverse;
+  int o_f32;           // o is fp32 whatever the element type
+};
+
+constexpr int kMaxAttnJobs = 3;
+struct AttnArgs {
+  AttnJob job[kMaxAttnJobs];
+  const float* log_decay;
+  const int32_t* lengths;
+  const int32_t* offsets;
+  int64_t rows;
+  int jobs, B, T, H;
+  int tiles;      // column tiles of the widest job's Dv
+  int segments;   // workgroups along a sequence
+  int seg_tokens; // tokens of a segment
+};
+
+// The attention of every job; a.tiles is set by the launch.
+hipError_t launch_attention(const AttnArgs& a, prnnDataType_t type, hipStream_t stream);
+
+// dst[t][b][g] = sum over the heads of group g of src[t][b][H] (fp32, dense
+// rows of D), in head order.  Rows as the attention's outputs.
+struct AttnReduceArgs {
+  const float* src;
+  AttnOperand dst;
+  const int32_t* lengths;
+  const int32_t* offsets;
+  int64_t rows;
+  int B, T, groups, per_group, D;
+  int blocks;  // workgroups for each sequence (set by the launch)
+};
+hipError_t launch_attention_reduce(const AttnReduceArgs& a, prnnDataType_t type, hipStream_t stream);
+
+struct AttnStepArgs {
+  AttnOperand q, k, v, o;
+  const float* log_decay;
+  const float* s_in;
+  float* s_out;
+  int B, H, Dk, Dv;
+  int tiles;  // tiles of 32 columns (set by the launch)
+  float scale;
+};
+hipError_t launch_attention_step(const AttnStepArgs& a, prnnDataType_t type, hipStream_t stream);
+
+// -- layer norm (layer_norm.hip) ----------------------------------------------------
+struct NormArgs {
+  const void* x;
+  const void* dy;      // backward
+  const void* weight;  // or nullptr
+  const void* bias;    // or nullptr
+  void* y;             // forward: y; backward: dx, or nullptr
+  float* mean;         // forward: or nullptr
+  float* rstd;
+  const float* mean_in;  // backward
+  const float* rstd_in;
+  float* partial;      // backward: [grid][2][N] sums of dy n and dy, or nullptr
+  void* dweight;       // backward: or nullptr
+  void* dbias;
+  int64_t M, ldx, ldy, lddy;
+  int N;
+  float eps;
+};
+hipError_t launch_layer_norm(const NormArgs& a, prnnDataType_t type, prnnDataType_t ptype, hipStream_t stream);
+// Workgroups of the backward pass (each leaves one partial sum).
+int layer_norm_backward_grid(const NormArgs& a, prnnDataType_t type, int compute_units);
+hipError_t launch_layer_norm_backward(const NormArgs& a, prnnDataType_t type, prnnDataType_t ptype, int grid,
+                                      hipStream_t stream);
+
+#ifdef __HIPCC__
+// -- element types ---------------------------------------------------------------------
+struct F32 {
+  typedef float raw;
+  static constexpr int id = PRNN_DATA_FLOAT;
+  __device__ static __forceinline__ float get(raw v) { return v; }
+  __device__ static __forceinline__ raw put(float f) { return f; }
+};
+struct F16 {
+  typedef _Float16 raw;
+  static constexpr int id = PRNN_DATA_HALF;
+  __device__ static __forceinline__ float get(raw v) { return (float)v; }
+  __device__ static __forceinline__ raw put(float f) { return (_Float16)f; }  // nearest, ties to even
+};
+struct BF16 {
+  typedef __bf16 raw;
+  static constexpr int id = PRNN_DATA_BFLOAT;
+  __device__ static __forceinline__ float get(raw v) { return (float)v; }
+  __device__ static __forceinline__ raw put(float f) { return (__bf16)f; }  // nearest, ties to even
+};
+
+#endif
+
+}  // namespace prnn
