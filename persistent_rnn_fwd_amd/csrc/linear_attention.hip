@@ -1,141 +1,18 @@
-// Linear attention with a decay for each head.
+// Linear attention with a decay for each head: the plan of a launch, the sum
+// over shared heads, and one token (the chunks are in attention_chunk.h).
 //
 //   S[t] = d S[t-1] + k[t] v[t]^T,  o[t] = scale S[t]^T q[t],  d = exp(log_decay)
-//
-// attention_token_kernel is the recurrence itself: one wave owns 16 columns of
-// a head's state in registers and walks the tokens, so every column costs one
-// pass over q and k.
-#include "sequence.h"
+#include <algorithm>
+
+#include "attention_chunk.h"
 
 namespace prnn {
 namespace {
 
-// First row and number of tokens of sequence b (see prnnAttention_t).
-struct Span {
-  int64_t first;
-  int len;
-};
-template <class A>
-__device__ __forceinline__ Span span_of(const A& a, int b) {
-  Span s = {0, a.T};
-  if (a.offsets != nullptr) {
-    const int64_t lo = a.offsets[b], hi = a.offsets[b + 1];
-    s.first = lo < 0 ? 0 : (lo > a.rows ? a.rows : lo);
-    int64_t end = hi < s.first ? s.first : (hi > a.rows ? a.rows : hi);
-    if (end - s.first > a.T) end = s.first + a.T;
-    s.len = (int)(end - s.first);
-  } else if (a.lengths != nullptr) {
-    const int n = a.lengths[b];
-    s.len = n < 0 ? 0 : (n > a.T ? a.T : n);
-  }
-  return s;
-}
-
-// Element offset of row `first` of sequence b, head h, of an operand.
-template <class A>
-__device__ __forceinline__ int64_t base_of(const AttnOperand& x, const A& a, const Span& s, int b, int h) {
-  return (a.offsets != nullptr ? s.first * x.token : (int64_t)b * x.batch) + (int64_t)(h / x.group) * x.head;
-}
-
-// exp(log_decay n) to fp32's precision: the product's rounding error re-enters
-// to first order.  n = 0 gives 1 and -infinity 0 for every other n.
-__device__ __forceinline__ float decay_power(float log_decay, int n) {
-  if (n == 0) return 1.f;
-  const float x = log_decay * (float)n;
-  if (x < -104.f) return 0.f;  // below the smallest fp32
-  const float low = __builtin_fmaf(log_decay, (float)n, -x);
-  return x > 89.f ? expf(x) : __builtin_fmaf(expf(x), low, expf(x));
-}
-
-constexpr int kTokenCols = 16;
-
-// grid: (column tiles x B H, jobs), one wave each.  Lane l owns rows l / 4 +
-// 16 j and columns 4 (l % 4) .. + 3 of the tile.
-template <class E, int NR>
-__global__ void __launch_bounds__(64) attention_token_kernel(AttnArgs a) {
-  typedef typename E::raw raw;
-  const AttnJob& job = a.job[blockIdx.y];
-  const int col0 = (int)(blockIdx.x % a.tiles) * kTokenCols;
-  if (col0 >= job.Dv) return;
-  const int bh = blockIdx.x / a.tiles, b = bh / a.H, h = bh % a.H;
-  const int lane = threadIdx.x, rg = lane >> 2, c = col0 + 4 * (lane & 3);
-  const Span s = span_of(a, b);
-  const raw* q = static_cast<const raw*>(job.q.p) + base_of(job.q, a, s, b, h);
-  const raw* k = static_cast<const raw*>(job.k.p) + base_of(job.k, a, s, b, h);
-  const raw* v = static_cast<const raw*>(job.v.p) + base_of(job.v, a, s, b, h);
-  const int64_t o = base_of(job.o, a, s, b, h);
-  const size_t state = ((size_t)b * a.H + h) * job.Dk * job.Dv;
-  const float log_decay = a.log_decay[h];
-  const float d = decay_power(log_decay, 1);
-
-  float S[NR][4];
-#pragma unroll
-  for (int j = 0; j < NR; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = rg + 16 * j;
-      S[j][e] = job.s_in != nullptr && r < job.Dk && c + e < job.Dv
-                    ? job.s_in[state + (size_t)r * job.s_row + (size_t)(c + e) * job.s_col]
-                    : 0.f;
-    }
-  const float before = job.reverse ? 1.f : d;  // decay of the state before a token takes it
-  const float after = job.reverse ? d : 1.f;
-  for (int i = 0; i < s.len; ++i) {
-    const int64_t t = job.reverse ? s.len - 1 - i : i;
-    float kv[NR], qv[NR], vv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NR; ++j) {
-      const int r = rg + 16 * j;
-      kv[j] = r < job.Dk ? E::get(k[t * job.k.token + r]) * job.kscale : 0.f;
-      qv[j] = r < job.Dk ? E::get(q[t * job.q.token + r]) : 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) vv[e] = c + e < job.Dv ? E::get(v[t * job.v.token + c + e]) : 0.f;
-#pragma unroll
-    for (int j = 0; j < NR; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (rg + 16 * j < job.Dk) {
-          S[j][e] = __builtin_fmaf(kv[j], vv[e], S[j][e] * before);
-          acc[e] = __builtin_fmaf(qv[j], S[j][e], acc[e]);
-          S[j][e] *= after;
-        }
-      }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-#pragma unroll
-      for (int m = 4; m < 64; m *= 2) acc[e] += __shfl_xor(acc[e], m);
-      if (rg == 0 && c + e < job.Dv) {
-        const int64_t at = o + t * job.o.token + c + e;
-        if (job.o_f32)
-          static_cast<float*>(const_cast<void*>(job.o.p))[at] = acc[e] * job.oscale;
-        else
-          static_cast<raw*>(const_cast<void*>(job.o.p))[at] = E::put(acc[e] * job.oscale);
-      }
-    }
-  }
-  if (a.lengths != nullptr && rg == 0) {
-    for (int64_t t = s.len; t < a.T; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (c + e < job.Dv) {
-          const int64_t at = o + t * job.o.token + c + e;
-          if (job.o_f32)
-            static_cast<float*>(const_cast<void*>(job.o.p))[at] = 0.f;
-          else
-            static_cast<raw*>(const_cast<void*>(job.o.p))[at] = E::put(0.f);
-        }
-  }
-  if (job.s_out != nullptr) {
-#pragma unroll
-    for (int j = 0; j < NR; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = rg + 16 * j;
-        if (r < job.Dk && c + e < job.Dv) job.s_out[state + (size_t)r * job.s_row + (size_t)(c + e) * job.s_col] = S[j][e];
-      }
-  }
-}
+using attn::base_of;
+using attn::decay_power;
+using attn::Span;
+using attn::span_of;
 
 // grid: `blocks` workgroups for each sequence, one thread per element of dst at a time.
 template <class E>
@@ -240,25 +117,47 @@ hipError_t for_type(prnnDataType_t type, F f) {
 
 }  // namespace
 
-hipError_t launch_attention(const AttnArgs& args, prnnDataType_t type, hipStream_t stream) {
-  AttnArgs a = args;
+size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
   int dk = 0, dv = 0;
-  for (int i = 0; i < a.jobs; ++i) {
-    dk = a.job[i].Dk > dk ? a.job[i].Dk : dk;
-    dv = a.job[i].Dv > dv ? a.job[i].Dv : dv;
+  a->vec = 1;
+  const int e = type == PRNN_DATA_FLOAT ? 4 : 2;
+  // whole 16-byte vectors: the rows' lengths, and every stride that is used
+  auto vectors = [&](const AttnOperand& x, int D, int heads, int size) {
+    const int per = 16 / size;
+    return D % per == 0 && (uintptr_t)x.p % 16 == 0 && (a->T <= 1 || x.token % per == 0) &&
+           (a->offsets != nullptr ? x.token % per == 0 : a->B <= 1 || x.batch % per == 0) &&
+           (heads <= 1 || x.head % per == 0);
+  };
+  for (int i = 0; i < a->jobs; ++i) {
+    AttnJob& j = a->job[i];
+    dk = std::max(dk, j.Dk);
+    dv = std::max(dv, j.Dv);
+    for (const AttnOperand* x : {&j.q, &j.k, &j.v})
+      if (!vectors(*x, x == &j.v ? j.Dv : j.Dk, a->H / x->group, e)) a->vec = 0;
+    // (8 columns at a time also where o is fp32)
+    j.o_vec = j.Dv % 8 == 0 && vectors(j.o, j.Dv, a->H / j.o.group, j.o_f32 ? 4 : e);
   }
-  a.tiles = (dv + kTokenCols - 1) / kTokenCols;
-  const dim3 grid((unsigned)a.tiles * a.B * a.H, a.jobs);
-  return for_type(type, [&](auto e) {
-    typedef decltype(e) E;
-    if (dk <= 64)
-      attention_token_kernel<E, 4><<<grid, 64, 0, stream>>>(a);
-    else if (dk <= 128)
-      attention_token_kernel<E, 8><<<grid, 64, 0, stream>>>(a);
-    else
-      attention_token_kernel<E, 16><<<grid, 64, 0, stream>>>(a);
-    return hipGetLastError();
-  });
+  a->dkp = dk <= 64 ? 64 : dk <= 128 ? 128 : 256;
+  a->waves = dv > 64 ? 8 : 4;
+  const int cols = 16 * a->waves;
+  a->tiles = (dv + cols - 1) / cols;
+  // Segments: enough workgroups for two on each compute unit, of at least 8
+  // chunks of 64 tokens (a segment's state costs k and v a second read).
+  const int64_t groups = (int64_t)a->tiles * a->B * a->H * a->jobs;
+  const int64_t want = std::max<int64_t>(1, 2 * compute_units / std::max<int64_t>(1, groups));
+  const int64_t most = std::max(1, a->T / 512);
+  const int64_t segments = std::min(want, most);
+  a->seg_tokens = std::max(64, (int)(((a->T + segments - 1) / segments + 63) / 64 * 64));
+  a->segments = std::max(1, (a->T + a->seg_tokens - 1) / a->seg_tokens);
+  return a->segments > 1 ? (size_t)a->segments * a->tiles * a->B * a->H * a->dkp * cols : 0;
+}
+
+hipError_t launch_attention(const AttnArgs& a, prnnDataType_t type, hipStream_t stream) {
+  switch (type) {
+    case PRNN_DATA_FLOAT: return launch_attention_f32(a, stream);
+    case PRNN_DATA_HALF: return launch_attention_f16(a, stream);
+    default: return launch_attention_bf16(a, stream);
+  }
 }
 
 hipError_t launch_attention_reduce(const AttnReduceArgs& args, prnnDataType_t type, hipStream_t stream) {

@@ -142,7 +142,6 @@ prnnStatus_t check_attention(prnnContext* h, const prnnAttention_t* d, bool step
   }
   if (d->B == 0) return PRNN_STATUS_SUCCESS;
   if (d->log_decay == nullptr || !aligned(d->log_decay, 4)) return PRNN_STATUS_BAD_PARAM;
-  // workgroups: at most 16 column tiles (or 64 segments) for each state
   if ((int64_t)d->B * d->H > (1ll << 24)) return PRNN_STATUS_NOT_SUPPORTED;
   return PRNN_STATUS_SUCCESS;
 }
@@ -167,6 +166,11 @@ AttnArgs base_args(const Problem& p, int jobs) {
   a.T = p.tokens > 0 ? p.d.T : 0;
   a.H = p.d.H;
   return a;
+}
+
+// Workgroups of the widest launch: elements of a state take up to 256 of them.
+bool grid_fits(const AttnArgs& a) {
+  return (int64_t)a.tiles * a.B * a.H * std::max(a.segments, 256) <= 0x7fffffffll;
 }
 
 uint64_t state_bytes(const prnnAttention_t& d) { return 4ull * d.B * d.H * d.Dk * d.Dv; }
@@ -227,6 +231,14 @@ prnnStatus_t prnn_linear_attention(prnnHandle_t h, const prnnAttention_t* d, con
   j.s_col = 1;
   j.kscale = 1.f;
   j.oscale = d->scale;
+  const size_t floats = plan_attention(&a, d->type, handle_compute_units(h));
+  if (!grid_fits(a)) return PRNN_STATUS_NOT_SUPPORTED;
+  if (floats > 0) {
+    void* mem = nullptr;
+    st = handle_workspace(h, floats * 4, stream, &mem);
+    if (st != PRNN_STATUS_SUCCESS) return st;
+    j.segments = static_cast<float*>(mem);
+  }
   st = launched(launch_attention(a, d->type, stream));
   if (st == PRNN_STATUS_SUCCESS) log_call(h, "linear attention", p);
   return st;
@@ -266,15 +278,8 @@ prnnStatus_t prnn_linear_attention_backward(prnnHandle_t h, const prnnAttention_
   const int group = d->H / d->Hkv;
   const int64_t rows = d->offsets != nullptr ? p.tokens : p.tokens * d->B;
   // A shared head's gradient: every head's own in fp32 first, then their sum.
-  const size_t wide_k = group > 1 ? (size_t)rows * d->H * d->Dk * 4 : 0;
-  const size_t wide_v = group > 1 ? (size_t)rows * d->H * d->Dv * 4 : 0;
-  float* work = nullptr;
-  if (wide_k + wide_v > 0) {
-    void* mem = nullptr;
-    st = handle_workspace(h, wide_k + wide_v, stream, &mem);
-    if (st != PRNN_STATUS_SUCCESS) return st;
-    work = static_cast<float*>(mem);
-  }
+  const size_t wide_k = group > 1 ? ((size_t)rows * d->H * d->Dk * 4 + 255) / 256 * 256 : 0;
+  const size_t wide_v = group > 1 ? ((size_t)rows * d->H * d->Dv * 4 + 255) / 256 * 256 : 0;
   auto dense = [&](float* mem, int D) {
     AttnOperand x = {mem, (int64_t)d->H * D, 0, D, 1};
     if (d->offsets == nullptr) {
@@ -300,7 +305,7 @@ prnnStatus_t prnn_linear_attention_backward(prnnHandle_t h, const prnnAttention_
   jk.q = operand(v, group);
   jk.k = operand(do_, 1);
   jk.v = operand(q, 1);
-  jk.o = group > 1 ? dense(work, d->Dk) : operand(dk, 1);
+  jk.o = group > 1 ? dense(nullptr, d->Dk) : operand(dk, 1);
   jk.o_f32 = group > 1;
   jk.s_in = dS1;
   jk.Dk = d->Dv;
@@ -314,7 +319,7 @@ prnnStatus_t prnn_linear_attention_backward(prnnHandle_t h, const prnnAttention_
   jv.q = operand(k, group);
   jv.k = operand(q, 1);
   jv.v = operand(do_, 1);
-  jv.o = group > 1 ? dense(work + wide_k / 4, d->Dv) : operand(dv, 1);
+  jv.o = group > 1 ? dense(nullptr, d->Dv) : operand(dv, 1);
   jv.o_f32 = group > 1;
   jv.s_in = dS1;
   jv.s_out = dS0;
@@ -325,6 +330,20 @@ prnnStatus_t prnn_linear_attention_backward(prnnHandle_t h, const prnnAttention_
   jv.kscale = d->scale;
   jv.oscale = 1.f;
   jv.reverse = 1;
+  const size_t floats = plan_attention(&a, d->type, handle_compute_units(h));
+  if (!grid_fits(a)) return PRNN_STATUS_NOT_SUPPORTED;
+  float* work = nullptr;  // the heads' gradients, then the segments of the three jobs
+  if (wide_k + wide_v + floats > 0) {
+    void* mem = nullptr;
+    st = handle_workspace(h, wide_k + wide_v + 12 * floats, stream, &mem);
+    if (st != PRNN_STATUS_SUCCESS) return st;
+    work = static_cast<float*>(mem);
+    if (group > 1) {
+      jk.o.p = work;
+      jv.o.p = work + wide_k / 4;
+    }
+    for (int i = 0; i < 3 && floats > 0; ++i) a.job[i].segments = work + (wide_k + wide_v) / 4 + i * floats;
+  }
   st = launched(launch_attention(a, d->type, stream));
   if (st == PRNN_STATUS_SUCCESS && group > 1 && p.tokens > 0) {
     AttnReduceArgs r;

@@ -46,6 +46,7 @@ struct AttnJob {
   float kscale, oscale;
   int reverse;
   int o_f32;           // o is fp32 whatever the element type
+  int o_vec;           // 16-byte stores of o (set by plan_attention)
 };
 
 constexpr int kMaxAttnJobs = 3;
@@ -56,13 +57,22 @@ struct AttnArgs {
   const int32_t* offsets;
   int64_t rows;
   int jobs, B, T, H;
-  int tiles;      // column tiles of the widest job's Dv
+  // set by plan_attention
+  int dkp, waves; // kernel instance: rows of the state; waves, 16 columns of it each
+  int vec;        // 16-byte loads of q, k and v
+  int tiles;      // workgroups along the columns of the widest job's Dv
   int segments;   // workgroups along a sequence
   int seg_tokens; // tokens of a segment
 };
 
-// The attention of every job; a.tiles is set by the launch.
+// Chooses the instance and the split, and returns the floats of workspace
+// that each job needs for AttnJob::segments (0: none).
+size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units);
 hipError_t launch_attention(const AttnArgs& a, prnnDataType_t type, hipStream_t stream);
+// ... of one element type (attention_f32.hip, attention_f16.hip, attention_bf16.hip).
+hipError_t launch_attention_f32(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attention_f16(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attention_bf16(const AttnArgs& a, hipStream_t stream);
 
 // dst[t][b][g] = sum over the heads of group g of src[t][b][H] (fp32, dense
 // rows of D), in head order.  Rows as the attention's outputs.
