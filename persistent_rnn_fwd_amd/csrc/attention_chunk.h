@@ -49,27 +49,29 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// Parts of an input (kIn), of the scores and the state in the output's
-// products (kOut), and of the decayed v in the state's (kState).
+// Parts of an input (kIn), and of the scores and the state in the output's
+// products (kOut).
 template <class E>
 struct Parts;
 template <>
 struct Parts<BF16> {
-  static constexpr int kIn = 1, kOut = 2, kState = 3;
+  static constexpr int kIn = 1, kOut = 2;
 };
 template <>
 struct Parts<F16> {
-  static constexpr int kIn = 2, kOut = 2, kState = 3;
+  static constexpr int kIn = 2, kOut = 2;
 };
 template <>
 struct Parts<F32> {
-  static constexpr int kIn = 3, kOut = 3, kState = 3;
+  static constexpr int kIn = 3, kOut = 3;
 };
 
-// Tokens of a chunk.
+// Tokens of a chunk.  64 halves what a token pays for splitting and scaling
+// the state; the parts of the other types, and 256 rows, leave LDS and
+// registers for 32.
 template <class E, int DKP>
 constexpr int chunk_tokens() {
-  return 32;
+  return E::id == PRNN_DATA_BFLOAT && DKP <= 128 ? 64 : 32;
 }
 
 // First row and number of tokens of sequence b (see prnnAttention_t).
@@ -111,6 +113,11 @@ __device__ __forceinline__ float decay_power(float log_decay, int n) {
   return x > 89.f ? expf(x) : __builtin_fmaf(expf(x), low, expf(x));
 }
 
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
 // -- splitting into bf16 parts -----------------------------------------------------
 
 __device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
@@ -150,15 +157,31 @@ __device__ __forceinline__ b16x8 operand(const uint32_t (&w)[4]) {
   return __builtin_bit_cast(b16x8, v);
 }
 
-// acc += x y over the parts' products that matter: i + j <= L.
-template <int NX, int NY, int L>
-__device__ __forceinline__ void products(f32x4& acc, const b16x8 (&x)[NX], const b16x8 (&y)[NY]) {
+// acc[m] += x y[m] over the parts' products that matter, i + j <= L, the
+// accumulators in turn.
+template <int NX, int NY, int L, int M>
+__device__ __forceinline__ void products(f32x4 (&acc)[M], const b16x8 (&x)[NX], const b16x8 (&y)[M][NY]) {
 #pragma unroll
   for (int s = L; s >= 0; --s)  // small terms first
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const int j = s - i;
-      if (j >= 0 && j < NY) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[j], acc, 0, 0, 0);
+      if (j < 0 || j >= NY) continue;
+#pragma unroll
+      for (int m = 0; m < M; ++m) acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[m][j], acc[m], 0, 0, 0);
+    }
+}
+// ... and acc[m] += x[m] y.
+template <int NX, int NY, int L, int M>
+__device__ __forceinline__ void products(f32x4 (&acc)[M], const b16x8 (&x)[M][NX], const b16x8 (&y)[NY]) {
+#pragma unroll
+  for (int s = L; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int j = s - i;
+      if (j < 0 || j >= NY) continue;
+#pragma unroll
+      for (int m = 0; m < M; ++m) acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m][i], y[j], acc[m], 0, 0, 0);
     }
 }
 
@@ -191,8 +214,10 @@ __device__ __forceinline__ u32x2 read_columns(const char* lds, int at) {
 
 // -- global to LDS -----------------------------------------------------------------------
 
-// Offset past every chunk's buffer: such a load returns zeros.
-constexpr uint32_t kOutside = 0xFFFFFFE0u;
+// An offset past every chunk's buffer, also after a chunk's rows (below 2^30
+// bytes) are added to it or taken from it: loads there return zeros and stores
+// do nothing.
+constexpr uint32_t kOutside = 0x80000000u;
 
 // The rows of one operand of a chunk: C rows of W columns, `cols` of which
 // exist.  Thread t takes 16-byte vectors t, t + THREADS, ... of the tile.
@@ -203,12 +228,34 @@ struct Rows {
   static constexpr int N = C * kPerRow >= THREADS ? C * kPerRow / THREADS : 1;  // (fewer vectors than threads: some idle)
   static constexpr int kStep = THREADS / kPerRow;  // rows from one vector of a thread to its next
   u32x4 v[N];
+  int to;           // bytes of this thread's first vector in the tile
+  uint32_t whole;   // ... and in memory, for a chunk of C tokens
+  uint32_t step;    // from there to the next one's
+
+  __device__ __forceinline__ Rows(uint32_t stride, int cols, bool reverse) {
+    const int c = (int)threadIdx.x % kPerRow, row = (int)threadIdx.x / kPerRow;
+    to = place(row, c);
+    whole = c * kVec < cols && row < C ? (uint32_t)(reverse ? C - 1 - row : row) * stride + 16u * (uint32_t)c : kOutside;
+    step = reverse ? 0u - kStep * stride : kStep * stride;
+  }
+  // 16-byte vectors (fp32: its 8 bytes of each part).
+  static __device__ __forceinline__ int place(int row, int c) {
+    return Parts<E>::kIn == 3 ? (row_at<W>(row) ^ (c / 2 << 4)) + 8 * (c & 1) : row_at<W>(row) ^ (c << 4);
+  }
 
   // Rows [t0, t0 + n) of the sequence in memory order; reversed: token t0 + n
-  // - 1 first.  p: token 0; stride in bytes.
+  // - 1 first; n <= 0: zeros.  p: token 0; stride in bytes.
   __device__ __forceinline__ void load(const void* p, int64_t t0, int n, uint32_t stride, int cols, bool reverse) {
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(static_cast<const char*>(p) + t0 * (int64_t)stride,
-                                               (uint32_t)(n - 1) * stride + (uint32_t)cols * (uint32_t)sizeof(raw));
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(
+        static_cast<const char*>(p) + t0 * (int64_t)stride,
+        n > 0 ? (uint32_t)(n - 1) * stride + (uint32_t)cols * (uint32_t)sizeof(raw) : 0u);
+    if (VEC && n == C) {
+      int at = (int)whole;
+      keep(at);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, (uint32_t)at + i * step, 0, kPlain);
+      return;
+    }
     int c = (int)threadIdx.x % kPerRow * kVec, row = (int)threadIdx.x / kPerRow;
     keep(c);
     keep(row);
@@ -237,14 +284,15 @@ struct Rows {
   // Into the tile's parts, C W bf16 each.
   __device__ __forceinline__ void store(char* lds) const {
     constexpr int P = Parts<E>::kIn;
-    int c = (int)threadIdx.x % kPerRow, row = (int)threadIdx.x / kPerRow;
-    keep(c);
-    keep(row);
-    if (C * kPerRow < THREADS && row >= C) return;
+    if (C * kPerRow < THREADS && (int)threadIdx.x >= C * kPerRow) return;
 #pragma unroll
-    for (int i = 0; i < N; ++i, row += kStep) {
+    for (int i = 0; i < N; ++i) {
+      // 8 rows on, the swizzle's second bit is the other one; 16 rows on it is the same
+      const int at = kStep % 8 == 0 ? (to ^ (kStep * i % 16 == 8 ? 32 : 0)) + i * kStep * (2 * W)
+                                    : place((int)threadIdx.x / kPerRow + i * kStep, (int)threadIdx.x % kPerRow);
+      char* const p0 = lds + at;
       if constexpr (P == 1) {
-        *reinterpret_cast<u32x4*>(lds + (row_at<W>(row) ^ (c << 4))) = v[i];
+        *reinterpret_cast<u32x4*>(p0) = v[i];
       } else if constexpr (P == 2) {
         typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
         const f16x8 h = __builtin_bit_cast(f16x8, v[i]);
@@ -254,9 +302,7 @@ struct Rows {
         uint32_t w[2][4];
         split<2, 8>(x, w);
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-          *reinterpret_cast<u32x4*>(lds + p * (C * W * 2) + (row_at<W>(row) ^ (c << 4))) =
-              u32x4{w[p][0], w[p][1], w[p][2], w[p][3]};
+        for (int p = 0; p < 2; ++p) *reinterpret_cast<u32x4*>(p0 + p * (C * W * 2)) = u32x4{w[p][0], w[p][1], w[p][2], w[p][3]};
       } else {
         float x[4];
         uint32_t w[3][2];
@@ -264,9 +310,7 @@ struct Rows {
         for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(v[i][e]);
         split<3, 4>(x, w);
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
-          *reinterpret_cast<u32x2*>(lds + p * (C * W * 2) + (row_at<W>(row) ^ (c / 2 << 4)) + 8 * (c & 1)) =
-              u32x2{w[p][0], w[p][1]};
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x2*>(p0 + p * (C * W * 2)) = u32x2{w[p][0], w[p][1]};
       }
     }
   }
@@ -274,20 +318,26 @@ struct Rows {
 
 // -- the workgroup's problem -----------------------------------------------------------------
 
-template <class E, int DKP, int WAVES>
+template <class E, int DKP, int NT, int WAVES>
 struct Shape {
   static constexpr int C = chunk_tokens<E, DKP>();
-  static constexpr int DVT = 16 * WAVES;       // columns of a workgroup
+  static constexpr int DVT = 16 * NT * WAVES;       // columns of a workgroup
   static constexpr int KT = DKP / 16;       // 16-row tiles of the state
   static constexpr int kTile = 2 * C * Parts<E>::kIn;  // bytes of a tile's column
   static constexpr int kQ = 0, kK = kTile * DKP, kV = 2 * kTile * DKP, kP = kV + kTile * DVT;
   static constexpr int kPRow = C + 8;       // bf16 of a row of scores: rows 16 bytes apart on the banks
   static constexpr int kPPart = 2 * C * kPRow;
-  static constexpr int kW = kP + Parts<E>::kOut * kPPart;  // kscale d^(C - x), x = 0 .. C
-  static constexpr int kLds = kW + 4 * (C + 4);
+  static constexpr int kW = kP + Parts<E>::kOut * kPPart;  // C weights of the state (state_weight)
+  static constexpr int kD = kW + 4 * C;  // oscale kscale d^(C - x), x = 0 .. C; zeros to C + 15
+  static constexpr int kLds = kD + 4 * (C + 16);
   // without scores: k and v only
-  static constexpr int kLdsState = kTile * (DKP + DVT) + 4 * (C + 4);
+  static constexpr int kLdsState = kTile * (DKP + DVT) + 4 * C;
 };
+
+// The weight of token j of n (at most C, reversed: p = 0) in the state after them.
+__device__ __forceinline__ float state_weight(const AttnJob& job, float log_decay, int n, int p, int j) {
+  return job.kscale * decay_power(log_decay, max(n - p - j, 0));  // (past n: rows of zeros)
+}
 
 // The state of one head in memory, as this lane's elements of it: element r of
 // tile t lies at(t, r) bytes on, past the buffer where it does not exist.
@@ -305,6 +355,21 @@ struct StateAt {
   }
 };
 
+// Keeps a value that is the same in every lane in a scalar register (the
+// compiler would rather load it again inside the loop and wait for it).
+__device__ __forceinline__ int pinned(int x) {
+  x = __builtin_amdgcn_readfirstlane(x);
+  asm volatile("" : "+s"(x));
+  return x;
+}
+
+// Where o goes.
+struct Out {
+  char* p;
+  int token;
+  bool vec, wide;
+};
+
 // What a workgroup works on.
 struct Where {
   int b, h, col0, cols;  // the first of its columns of the state, and how many exist
@@ -312,14 +377,15 @@ struct Where {
   Span s;
   const char *q, *k, *v;  // token 0 (v: of its columns)
   int64_t o;              // element of token 0, first column
-  float log_decay;
-  float* states;          // the segment's states in register order, or nullptr
+  float log_decay;        // (set after the first loads are under way)
+  float* states;          // slot 0 of the segments' states, in register order, or nullptr
+  int64_t slot;           // elements from slot to slot
 };
 
-template <class E, int DKP, int WAVES>
+template <class E, int DKP, int NT, int WAVES>
 __device__ __forceinline__ bool where(const AttnArgs& a, const AttnJob& job, int segments, Where& w) {
   typedef typename E::raw raw;
-  constexpr int DVT = 16 * WAVES;
+  constexpr int DVT = 16 * NT * WAVES;
   int id = blockIdx.x;
   w.col0 = id % a.tiles * DVT;
   const int tile = id % a.tiles;
@@ -335,10 +401,10 @@ __device__ __forceinline__ bool where(const AttnArgs& a, const AttnJob& job, int
   w.k = static_cast<const char*>(job.k.p) + base_of(job.k, a, w.s, w.b, w.h) * (int64_t)sizeof(raw);
   w.v = static_cast<const char*>(job.v.p) + (base_of(job.v, a, w.s, w.b, w.h) + w.col0) * (int64_t)sizeof(raw);
   w.o = base_of(job.o, a, w.s, w.b, w.h) + w.col0;
-  w.log_decay = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(a.log_decay[w.h])));
   w.states = job.segments == nullptr
                  ? nullptr
-                 : job.segments + (((int64_t)w.seg * a.B * a.H + bh) * a.tiles + tile) * (DKP * DVT);
+                 : job.segments + ((int64_t)bh * a.tiles + tile) * (DKP * DVT);
+  w.slot = (int64_t)a.B * a.H * a.tiles * (DKP * DVT);
   if (w.cols > DVT) w.cols = DVT;
   return true;
 }
@@ -348,7 +414,11 @@ __device__ __forceinline__ bool where(const AttnArgs& a, const AttnJob& job, int
 __device__ __forceinline__ int state_row(int t, int r, int lane) {
   return 32 * (t / 2) + 8 * (lane >> 4) + 4 * (t % 2) + r;
 }
-__device__ __forceinline__ int state_col(int wave, int lane) { return 16 * wave + (lane & 15); }
+template <int NT>
+__device__ __forceinline__ int state_col(int m, int wave, int lane) {
+  const int l = lane & 15;
+  return NT == 2 ? 32 * wave + 8 * (l >> 2) + 4 * m + (l & 3) : 16 * wave + l;
+}
 
 template <class E>
 __device__ __forceinline__ void put_out(const AttnJob& job, int64_t at, float x) {
@@ -361,9 +431,9 @@ __device__ __forceinline__ void put_out(const AttnJob& job, int64_t at, float x)
 // The recurrence over tokens [lo, hi) of the job's order for this wave's
 // columns, straight from memory: S is updated and, with OUT, the rows of o
 // written.  Slow; see the file comment.
-template <class E, int DKP, bool OUT>
-__device__ __forceinline__ void attention_tokens(const AttnJob& job, const Where& w, int lo, int hi, int col, int lane,
-                                                 f32x4 (&S)[DKP / 16]) {
+template <class E, int DKP, int NT, bool OUT>
+__device__ __forceinline__ void attention_tokens(const AttnJob& job, const Where& w, int lo, int hi, int wave, int lane,
+                                                 f32x4 (&S)[DKP / 16][NT]) {
   typedef typename E::raw raw;
   const float d = decay_power(w.log_decay, 1);
   const float before = job.reverse ? 1.f : d, after = job.reverse ? d : 1.f;
@@ -374,8 +444,13 @@ __device__ __forceinline__ void attention_tokens(const AttnJob& job, const Where
     const raw* q = reinterpret_cast<const raw*>(w.q) + t * job.q.token + first;
     const raw* k = reinterpret_cast<const raw*>(w.k) + t * job.k.token + first;
     const raw* v = reinterpret_cast<const raw*>(w.v) + t * job.v.token;
-    const float vv = col < w.cols ? E::get(v[col]) : 0.f;
-    float acc = 0.f;
+    float vv[NT], acc[NT];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      const int col = state_col<NT>(m, wave, lane);
+      vv[m] = col < w.cols ? E::get(v[col]) : 0.f;
+      acc[m] = 0.f;
+    }
     int rows = job.Dk - first;  // rows of the state from the lane's first one on
     keep(rows);
 #pragma unroll
@@ -384,218 +459,360 @@ __device__ __forceinline__ void attention_tokens(const AttnJob& job, const Where
       for (int r = 0; r < 4; ++r) {
         const int row = 32 * (x / 2) + 4 * (x % 2) + r;
         if (row < rows) {
-          S[x][r] = __builtin_fmaf(E::get(k[row]) * job.kscale, vv, S[x][r] * before);
-          if (OUT) acc = __builtin_fmaf(E::get(q[row]), S[x][r], acc);
-          S[x][r] *= after;
+          const float kk = E::get(k[row]) * job.kscale, qq = OUT ? E::get(q[row]) : 0.f;
+#pragma unroll
+          for (int m = 0; m < NT; ++m) {
+            S[x][m][r] = __builtin_fmaf(kk, vv[m], S[x][m][r] * before);
+            if (OUT) acc[m] = __builtin_fmaf(qq, S[x][m][r], acc[m]);
+            S[x][m][r] *= after;
+          }
         }
       }
     if constexpr (OUT) {
-      acc += __shfl_xor(acc, 16);
-      acc += __shfl_xor(acc, 32);
-      if (lane < 16 && col < w.cols) put_out<E>(job, w.o + t * job.o.token + col, acc * job.oscale);
-    }
-  }
-}
-
-// S += sum_j (kscale d^(n - p - j) v_j) k_j^T, S having been decayed; V: the
-// chunk's columns of v as operands.  skip = C - n + p, weights from the table
-// kscale d^(C - x).
-template <class E, int DKP, int C>
-__device__ __forceinline__ void update_state(f32x4 (&S)[DKP / 16], const b16x8 (&V)[C / 32][Parts<E>::kIn],
-                                             const char* k, const float* weights, int skip) {
-  constexpr int IN = Parts<E>::kIn, ST = Parts<E>::kState;
-  const int lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  // row 8 g + l / 4, and 4 rows on: 8 W bytes and the swizzle's lowest bit
-  int base = row_at<DKP>(8 * g + (l >> 2)) ^ ((l & 3) << 4);
-  keep(base);
 #pragma unroll
-  for (int j = 0; j < C / 32; ++j) {
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int at = skip + 32 * j + 8 * g + e;
-      x[e] = 0.f;
-#pragma unroll
-      for (int p = IN - 1; p >= 0; --p) x[e] += (float)V[j][p][e];
-      x[e] *= weights[at < C ? at : C];
-    }
-    uint32_t parts[ST][4];
-    split<ST, 8>(x, parts);
-    b16x8 D[ST];
-#pragma unroll
-    for (int p = 0; p < ST; ++p) D[p] = operand(parts[p]);
-#pragma unroll
-    for (int t = 0; t < DKP / 16; ++t) {
-      b16x8 K[IN];
-#pragma unroll
-      for (int p = 0; p < IN; ++p) {
-        u32x2 half[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          half[h] = read_columns(k, (base ^ (64 * (t / 2) + 16 * h)) + p * (C * DKP * 2) + (32 * j + 4 * h) * (2 * DKP) + 8 * (t % 2));
-        const uint32_t words[4] = {half[0][0], half[0][1], half[1][0], half[1][1]};
-        K[p] = operand(words);
+      for (int m = 0; m < NT; ++m) {
+        const int col = state_col<NT>(m, wave, lane);
+        acc[m] += __shfl_xor(acc[m], 16);
+        acc[m] += __shfl_xor(acc[m], 32);
+        if (lane < 16 && col < w.cols) put_out<E>(job, w.o + t * job.o.token + col, acc[m] * job.oscale);
       }
-      products<IN, ST, 2>(S[t], K, D);
     }
   }
 }
 
-// The wave's columns of the chunk's v, as operands.
-template <class E, int W, int C>
-__device__ __forceinline__ void read_values(b16x8 (&V)[C / 32][Parts<E>::kIn], const char* v, int wave) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  int base = (row_at<W>(8 * g + (l >> 2)) ^ ((2 * wave + ((l & 3) >> 1)) << 4)) + 8 * (l & 1);
-  keep(base);
+// Rows 32 j .. + 31 of the wave's columns of the chunk's v, as operands.
+template <class E, int NT, int W, int C>
+__device__ __forceinline__ void read_values(b16x8 (&V)[NT][Parts<E>::kIn], const char* v, int wave, int lane, int j) {
+  const int g = lane >> 4, l = lane & 15;
+  const int base = NT == 2 ? row_at<W>(8 * g + (l >> 2)) ^ ((4 * wave + (l & 3)) << 4)
+                           : (row_at<W>(8 * g + (l >> 2)) ^ ((2 * wave + ((l & 3) >> 1)) << 4)) + 8 * (l & 1);
 #pragma unroll
-  for (int j = 0; j < C / 32; ++j)
+  for (int m = 0; m < NT; ++m)
 #pragma unroll
     for (int p = 0; p < Parts<E>::kIn; ++p) {
       u32x2 half[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        half[h] = read_columns(v, (base ^ (16 * h)) + p * (C * W * 2) + (32 * j + 4 * h) * (2 * W));
+        half[h] = read_columns(v, (base ^ (16 * h)) + p * (C * W * 2) + (32 * j + 4 * h) * (2 * W) + 8 * m);
       const uint32_t words[4] = {half[0][0], half[0][1], half[1][0], half[1][1]};
-      V[j][p] = operand(words);
+      V[m][p] = operand(words);
     }
 }
 
+// Rows 32 j .. + 31 of the wave's columns of weights[j] v_j, as operands.
+template <class E, int NT, int ST, int W, int C>
+__device__ __forceinline__ void decayed_values(b16x8 (&D)[NT][ST], const char* v, const float* weights, int wave,
+                                               int lane, int j) {
+  constexpr int IN = Parts<E>::kIn;
+  b16x8 V[NT][IN];
+  read_values<E, NT, W, C>(V, v, wave, lane, j);
+  float w[8];
+#pragma unroll
+  for (int e = 0; e < 8; e += 4) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(weights + 32 * j + 8 * (lane >> 4) + e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[e + i] = x[i];
+  }
+#pragma unroll
+  for (int m = 0; m < NT; ++m) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = (float)V[m][IN - 1][e];
+#pragma unroll
+      for (int p = IN - 2; p >= 0; --p) x[e] += (float)V[m][p][e];
+      x[e] *= w[e];
+    }
+    uint32_t parts[ST][4];
+    split<ST, 8>(x, parts);
+#pragma unroll
+    for (int p = 0; p < ST; ++p) D[m][p] = operand(parts[p]);
+  }
+}
+
+// Rows 16 t .. + 15 (as the state deals them) of the chunk's k^T, as operands.
+// base: row 8 g + l / 4 of the tile of k, unit l % 4.
+template <class E, int DKP, int C>
+__device__ __forceinline__ void read_keys(b16x8 (&K)[C / 32][Parts<E>::kIn], const char* k, int base, int t) {
+#pragma unroll
+  for (int j = 0; j < C / 32; ++j)
+#pragma unroll
+    for (int p = 0; p < Parts<E>::kIn; ++p) {
+      // 4 rows on: 8 W bytes and the swizzle's lowest bit
+      u32x2 half[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        half[h] = read_columns(k, (base ^ (64 * (t / 2) + 16 * h)) + p * (C * DKP * 2) + (32 * j + 4 * h) * (2 * DKP) + 8 * (t % 2));
+      const uint32_t words[4] = {half[0][0], half[0][1], half[1][0], half[1][1]};
+      K[j][p] = operand(words);
+    }
+}
+
+// S <- decay S + k^T (D of all the chunk's tokens), for 16 rows of the state.
+template <class E, int NT, int ST, int C>
+__device__ __forceinline__ void update_tile(f32x4 (&S)[NT], const b16x8 (&D)[C / 32][NT][ST],
+                                            const b16x8 (&K)[C / 32][Parts<E>::kIn], float decay) {
+#pragma unroll
+  for (int m = 0; m < NT; ++m) S[m] *= decay;
+#pragma unroll
+  for (int j = 0; j < C / 32; ++j) products<Parts<E>::kIn, ST, ST - 1, NT>(S, K[j], D[j]);
+}
+
 // NaN from the first value on that is not finite, 0 until then.
-template <int N>
-__device__ __forceinline__ void watch(float& z, const f32x4 (&x)[N]) {
+template <int N, int M>
+__device__ __forceinline__ void watch(float& z, const f32x4 (&x)[N][M]) {
+  float y[4] = {z, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int t = 0; t < N; ++t)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) z = __builtin_fmaf(x[t][r], 0.f, z);
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(x[t][m][r], 0.f, y[r]);
+  z = (y[0] + y[1]) + (y[2] + y[3]);
 }
 
-// The state a segment starts from.
-template <int DKP>
-__device__ __forceinline__ void first_state(f32x4 (&S)[DKP / 16], const AttnJob& job, const Where& w, size_t head,
-                                            int col, int wave, int lane) {
-  constexpr int KT = DKP / 16;
-  if (w.states != nullptr) {
+// The head's initial state.
+template <int DKP, int NT>
+__device__ __forceinline__ void initial_state(f32x4 (&S)[DKP / 16][NT], const AttnJob& job, const Where& w, size_t head,
+                                              int wave, int lane) {
 #pragma unroll
-    for (int t = 0; t < KT; ++t) S[t] = reinterpret_cast<const f32x4*>(w.states)[(wave * KT + t) * 64 + lane];
-  } else if (job.s_in != nullptr) {
+  for (int m = 0; m < NT; ++m) {
+    if (job.s_in == nullptr) {
+#pragma unroll
+      for (int t = 0; t < DKP / 16; ++t) S[t][m] = f32x4(0.f);
+      continue;
+    }
+    const int col = state_col<NT>(m, wave, lane);
     const StateAt x(job.s_in, job, head, w.col0 + col, col < w.cols, lane);
+#pragma unroll
+    for (int t = 0; t < DKP / 16; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        S[t][m][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(x.rsrc, x.at(t, r), 0, kPlain));
+  }
+}
+
+// Split sequences.  Slot i of the workspace holds the state that segment i
+// leaves by itself (segment 0: from the initial state), or after the scan the
+// sequence's state after segment i; the last slot holds the initial state,
+// which the launch that needs it may overwrite in its own place.
+template <int KT, int NT>
+__device__ __forceinline__ f32x4* slot_at(const Where& w, int slot, int wave, int lane) {
+  return reinterpret_cast<f32x4*>(w.states + slot * w.slot) + wave * (KT * NT * 64) + lane;
+}
+constexpr int kScanFrom = 9;  // segments from which a scan between the launches costs less than every segment's own sum
+
+// The state a segment starts from.
+template <int DKP, int NT>
+__device__ __forceinline__ void first_state(f32x4 (&S)[DKP / 16][NT], const AttnArgs& a, const AttnJob& job,
+                                            const Where& w, size_t head, int wave, int lane) {
+  constexpr int KT = DKP / 16;
+  if (w.states == nullptr) {
+    initial_state<DKP, NT>(S, job, w, head, wave, lane);
+    return;
+  }
+  const bool scanned = a.segments >= kScanFrom;
+  const f32x4* p = slot_at<KT, NT>(w, w.seg == 0 ? a.segments - 1 : scanned ? w.seg - 1 : 0, wave, lane);
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int m = 0; m < NT; ++m) S[t][m] = p[(t * NT + m) * 64];
+  if (scanned) return;
+  const float whole = uniform(decay_power(w.log_decay, a.seg_tokens));
+  for (int i = 1; i < w.seg; ++i) {
+    const f32x4* own = slot_at<KT, NT>(w, i, wave, lane);
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        S[t][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(x.rsrc, x.at(t, r), 0, kPlain));
-  } else {
+      for (int m = 0; m < NT; ++m) {
+        const f32x4 x = own[(t * NT + m) * 64];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) S[t] = f32x4(0.f);
+        for (int r = 0; r < 4; ++r) S[t][m][r] = __builtin_fmaf(S[t][m][r], whole, x[r]);
+      }
   }
 }
-template <int DKP>
-__device__ __forceinline__ void last_state(const f32x4 (&S)[DKP / 16], const AttnJob& job, const Where& w, size_t head,
-                                           int col, int lane) {
-  const StateAt x(job.s_out, job, head, w.col0 + col, col < w.cols, lane);
+template <int DKP, int NT>
+__device__ __forceinline__ void last_state(const f32x4 (&S)[DKP / 16][NT], const AttnJob& job, const Where& w, size_t head,
+                                           int wave, int lane) {
 #pragma unroll
-  for (int t = 0; t < DKP / 16; ++t)
+  for (int m = 0; m < NT; ++m) {
+    const int col = state_col<NT>(m, wave, lane);
+    const StateAt x(job.s_out, job, head, w.col0 + col, col < w.cols, lane);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[t][r]), x.rsrc, x.at(t, r), 0, kPlain);
+    for (int t = 0; t < DKP / 16; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[t][m][r]), x.rsrc, x.at(t, r), 0, kPlain);
+  }
 }
 
-// The state that tokens of each segment but the last leave by themselves:
-// grid tiles x B H x (segments - 1), jobs.
-template <class E, int DKP, int WAVES, bool VEC>
-__global__ void __launch_bounds__(64 * WAVES, DKP == 256 ? 2 : WAVES / 2) attention_state_kernel(AttnArgs a) {
-  typedef Shape<E, DKP, WAVES> Sh;
+// Slots 0 .. segments - 2: grid tiles x B H x (segments - 1), jobs.
+template <class E, int DKP, int NT, int WAVES, bool VEC>
+__global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs a) {
+  typedef Shape<E, DKP, NT, WAVES> Sh;
   constexpr int C = Sh::C;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char *const kt = lds, *const vt = lds + Sh::kTile * DKP;
   float* const weights = reinterpret_cast<float*>(lds + Sh::kTile * (DKP + Sh::DVT));
   const AttnJob& job = a.job[blockIdx.y];
   Where w;
-  if (!where<E, DKP, WAVES>(a, job, a.segments, w)) return;
+  if (!where<E, DKP, NT, WAVES>(a, job, a.segments, w)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lo = w.seg * a.seg_tokens, hi = min(w.s.len, lo + a.seg_tokens);
-  if ((int)threadIdx.x <= C) weights[threadIdx.x] = job.kscale * decay_power(w.log_decay, C - (int)threadIdx.x);
-  const float decay = decay_power(w.log_decay, C);
   const int p = job.reverse ? 0 : 1;
   const uint32_t ks = (uint32_t)job.k.token * (uint32_t)sizeof(typename E::raw),
                  vs = (uint32_t)job.v.token * (uint32_t)sizeof(typename E::raw);
 
-  f32x4 S[Sh::KT];
-#pragma unroll
-  for (int t = 0; t < Sh::KT; ++t) S[t] = f32x4(0.f);
-  Rows<E, C, DKP, 64 * WAVES, VEC> rk;
-  Rows<E, C, Sh::DVT, 64 * WAVES, VEC> rv;
+  Rows<E, C, DKP, 64 * WAVES, VEC> rk(ks, job.Dk, job.reverse);
+  Rows<E, C, Sh::DVT, 64 * WAVES, VEC> rv(vs, w.cols, job.reverse);
   auto fetch = [&](int i) {
-    const int n = min(C, hi - i);
-    const int64_t t0 = job.reverse ? w.s.len - i - n : i;
+    const int n = max(0, min(C, hi - i));
+    const int64_t t0 = n == 0 ? 0 : job.reverse ? w.s.len - i - n : i;
     rk.load(w.k, t0, n, ks, job.Dk, job.reverse);
     rv.load(w.v, t0, n, vs, w.cols, job.reverse);
   };
-  if (lo < hi) fetch(lo);
+  fetch(lo);
+  w.log_decay = uniform(a.log_decay[w.h]);
+  if ((int)threadIdx.x < C) weights[threadIdx.x] = state_weight(job, w.log_decay, C, p, threadIdx.x);
+  const float decay = uniform(decay_power(w.log_decay, C));
+  const size_t head = (size_t)w.b * a.H + w.h;
+  f32x4 S[Sh::KT][NT];
+  auto start = [&]() {
+    if (w.seg == 0) {
+      initial_state<DKP, NT>(S, job, w, head, wave, lane);
+    } else {
+#pragma unroll
+      for (int t = 0; t < Sh::KT; ++t)
+#pragma unroll
+        for (int m = 0; m < NT; ++m) S[t][m] = f32x4(0.f);
+    }
+  };
+  auto put = [&](int slot) {
+    f32x4* to = slot_at<Sh::KT, NT>(w, slot, wave, lane);
+#pragma unroll
+    for (int t = 0; t < Sh::KT; ++t)
+#pragma unroll
+      for (int m = 0; m < NT; ++m) to[(t * NT + m) * 64] = S[t][m];
+  };
+  start();
+  if (w.seg == 0) put(a.segments - 1);
   for (int i = lo; i < hi; i += C) {
     const int n = min(C, hi - i);
+    if (n < C && (int)threadIdx.x < C) weights[threadIdx.x] = state_weight(job, w.log_decay, n, p, threadIdx.x);
     rk.store(kt);
     rv.store(vt);
     __syncthreads();
-    if (i + C < hi) fetch(i + C);
-    b16x8 V[C / 32][Parts<E>::kIn];
-    read_values<E, Sh::DVT, C>(V, vt, wave);
-    const float dn = n == C ? decay : decay_power(w.log_decay, n);
+    fetch(i + C);
+    const float dn = n == C ? decay : uniform(decay_power(w.log_decay, n));
+    b16x8 D[C / 32][NT][3];
 #pragma unroll
-    for (int t = 0; t < Sh::KT; ++t) S[t] *= dn;
-    update_state<E, DKP, C>(S, V, kt, weights, C - n + p);
+    for (int j = 0; j < C / 32; ++j) decayed_values<E, NT, 3, Sh::DVT, C>(D[j], vt, weights, wave, lane, j);
+    const int base = row_at<DKP>(8 * (lane >> 4) + ((lane & 15) >> 2)) ^ ((lane & 3) << 4);
+#pragma unroll
+    for (int t = 0; t < Sh::KT; ++t) {
+      b16x8 K[C / 32][Parts<E>::kIn];
+      read_keys<E, DKP, C>(K, kt, base, t);
+      update_tile<E, NT, 3, C>(S[t], D, K, dn);
+    }
     __syncthreads();
   }
   float z = 0.f;
   watch(z, S);
   if (wave_any(z != 0.f)) {
-#pragma unroll
-    for (int t = 0; t < Sh::KT; ++t) S[t] = f32x4(0.f);
-    attention_tokens<E, DKP, false>(job, w, lo, hi, 16 * wave + (lane & 15), lane, S);
+    start();
+    attention_tokens<E, DKP, NT, false>(job, w, lo, hi, wave, lane, S);
   }
-#pragma unroll
-  for (int t = 0; t < Sh::KT; ++t) reinterpret_cast<f32x4*>(w.states)[(wave * Sh::KT + t) * 64 + lane] = S[t];
+  put(w.seg);
 }
 
-// Turns the segments' own states into the states they start from: one thread
-// per element.  grid: tiles x B H x (DKP DVT / 256) workgroups, jobs.
-template <int DKP, int WAVES>
+// Turns the segments' own states into the sequence's states after them, 4
+// elements a thread, the loads of 8 slots ahead.  grid: tiles x B H x (DKP DVT /
+// 1024) workgroups, jobs.  (Slots that a sequence does not reach hold what no
+// one reads.)
+template <int DKP, int NT, int WAVES>
 __global__ void __launch_bounds__(256) attention_scan_kernel(AttnArgs a) {
-  constexpr int DVT = 16 * WAVES, KT = DKP / 16, kBlocks = DKP * DVT / 256;
+  constexpr int DVT = 16 * NT * WAVES, kBlocks = DKP * DVT / 1024, kAhead = 8;
   const AttnJob& job = a.job[blockIdx.y];
-  const int part = blockIdx.x % kBlocks, id = blockIdx.x / kBlocks, tile = id % a.tiles, bh = id / a.tiles;
-  const int b = bh / a.H, h = bh % a.H;
-  if (tile * DVT >= job.Dv) return;
-  const Span s = span_of(a, b);
-  const int x = part * 256 + (int)threadIdx.x;  // element in register order
-  const int r = x & 3, lane = (x >> 2) & 63, t = (x >> 8) % KT, wave = (x >> 8) / KT;
-  const int row = state_row(t, r, lane), col = tile * DVT + state_col(wave, lane);
-  float S = job.s_in != nullptr && row < job.Dk && col < job.Dv
-                ? job.s_in[(size_t)bh * job.Dk * job.Dv + (size_t)row * job.s_row + (size_t)col * job.s_col]
-                : 0.f;
-  float* p = job.segments + ((int64_t)bh * a.tiles + tile) * (DKP * DVT) + x;
-  const int64_t step = (int64_t)a.B * a.H * a.tiles * (DKP * DVT);
-  for (int seg = 0; seg < a.segments; ++seg, p += step) {
-    const float own = seg + 1 < a.segments ? *p : 0.f;
-    *p = S;
-    const int tokens = max(0, min(s.len - seg * a.seg_tokens, a.seg_tokens));
-    S = tokens > 0 ? __builtin_fmaf(S, decay_power(a.log_decay[h], tokens), own) : S;
+  const int id = blockIdx.x / kBlocks, h = id / a.tiles % a.H;
+  if (id % a.tiles * DVT >= job.Dv) return;
+  const float whole = decay_power(a.log_decay[h], a.seg_tokens);
+  f32x4* p = reinterpret_cast<f32x4*>(job.segments) + (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t step = (int64_t)a.B * a.H * a.tiles * (DKP * DVT / 4);
+  f32x4 S = *p;
+  for (int i0 = 1; i0 < a.segments - 1; i0 += kAhead) {
+    f32x4 own[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) own[i] = i0 + i < a.segments - 1 ? p[(i0 + i) * step] : f32x4(0.f);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= a.segments - 1) break;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[r] = __builtin_fmaf(S[r], whole, own[i][r]);
+      p[(i0 + i) * step] = S;
+    }
   }
+}
+
+// Stores the chunk's rows of o, element type or fp32: a lane has 4 NT
+// neighbouring columns of token 16 t + l.
+template <class E, int IT, int NT, bool WIDE>
+__device__ __forceinline__ void put_rows(const Out& x, const Where& w, const f32x4 (&O)[IT][NT], int64_t t0, int n,
+                                         bool reverse, int wave, int lane) {
+  typedef typename E::raw raw;
+  constexpr int kSize = WIDE ? 4 : 2;
+  const int stride = x.token * kSize, c0 = 16 * NT * wave + 4 * NT * (lane >> 4);
+  const __amdgpu_buffer_rsrc_t out = make_rsrc(x.p + (w.o + t0 * x.token) * kSize,
+                                               (uint32_t)(n - 1) * (uint32_t)stride + (uint32_t)(w.cols * kSize));
+  const int row = lane & 15;
+  const int first = (reverse ? n - 1 - row : row) * stride + c0 * kSize, step = (reverse ? -16 : 16) * stride;
+  if (x.vec) {
+    const int live = c0 < w.cols ? n - row : 0;  // rows from this one on
+#pragma unroll
+    for (int t = 0; t < IT; ++t) {
+      const uint32_t to = 16 * t < live ? (uint32_t)(first + t * step) : kOutside;
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t][m]), out, to + 16 * m, 0, kPlain);
+      } else {
+        typedef raw vec __attribute__((ext_vector_type(4 * NT)));
+        vec y;
+#pragma unroll
+        for (int e = 0; e < 4 * NT; ++e) y[e] = E::put(O[t][e / 4][e % 4]);
+        if constexpr (NT == 2)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), out, to, 0, kPlain);
+        else
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), out, to, 0, kPlain);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int t = 0; t < IT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4 * NT; ++e) {
+      const uint32_t to = row + 16 * t < n && c0 + e < w.cols ? (uint32_t)(first + t * step + e * kSize) : kOutside;
+      const float f = O[t][e / 4][e % 4];
+      if constexpr (WIDE)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), out, to, 0, kPlain);
+      else
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, E::put(f)), out, to, 0, kPlain);
+    }
 }
 
 // The attention: grid tiles x B H x segments, jobs.
-template <class E, int DKP, int WAVES, bool VEC>
-__global__ void __launch_bounds__(64 * WAVES, DKP == 256 ? 2 : WAVES / 2) attention_chunk_kernel(AttnArgs a) {
-  typedef Shape<E, DKP, WAVES> Sh;
+template <class E, int DKP, int NT, int WAVES, bool VEC, int ST>
+__global__ void __launch_bounds__(64 * WAVES, 2) attention_chunk_kernel(AttnArgs a) {
+  typedef Shape<E, DKP, NT, WAVES> Sh;
   typedef typename E::raw raw;
   constexpr int C = Sh::C, IT = C / 16, IN = Parts<E>::kIn, OUT = Parts<E>::kOut;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char *const qt = lds + Sh::kQ, *const kt = lds + Sh::kK, *const vt = lds + Sh::kV, *const pt = lds + Sh::kP;
-  float* const weights = reinterpret_cast<float*>(lds + Sh::kW);
+  float *const weights = reinterpret_cast<float*>(lds + Sh::kW), *const decays = reinterpret_cast<float*>(lds + Sh::kD);
   const AttnJob& job = a.job[blockIdx.y];
   Where w;
-  if (!where<E, DKP, WAVES>(a, job, a.segments, w)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+  if (!where<E, DKP, NT, WAVES>(a, job, a.segments, w)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane & 15;
   const int lo = w.seg * a.seg_tokens, hi = min(w.s.len, lo + a.seg_tokens);
   const int p = job.reverse ? 0 : 1;
   const bool reverse = job.reverse != 0;
@@ -609,168 +826,202 @@ __global__ void __launch_bounds__(64 * WAVES, DKP == 256 ? 2 : WAVES / 2) attent
   const bool last = w.seg == (w.s.len > 0 ? (w.s.len - 1) / a.seg_tokens : 0);
   if (lo >= hi && !(last && job.s_out != nullptr)) return;
 
-  if ((int)threadIdx.x <= C) weights[threadIdx.x] = job.kscale * decay_power(w.log_decay, C - (int)threadIdx.x);
-  // Score tiles above the diagonal that the products read: zero throughout.
-  for (int x = threadIdx.x; x < OUT * Sh::kPPart / 4; x += 64 * WAVES) reinterpret_cast<uint32_t*>(pt)[x] = 0u;
-  const float d16 = decay_power(w.log_decay, 16), decay = decay_power(w.log_decay, C);
-  float from_state = decay_power(w.log_decay, l + p) * job.oscale;  // of i = l
-
-  f32x4 S[Sh::KT];
-  const size_t head = (size_t)w.b * a.H + w.h;
-  const int col = 16 * wave + l;  // of the workgroup's columns: this lane's
-  first_state<DKP>(S, job, w, head, col, wave, lane);
-  float z = 0.f;
-
-  const uint32_t qs = (uint32_t)job.q.token * (uint32_t)sizeof(raw), ks = (uint32_t)job.k.token * (uint32_t)sizeof(raw),
-                 vs = (uint32_t)job.v.token * (uint32_t)sizeof(raw);
-  Rows<E, C, DKP, 64 * WAVES, VEC> rq, rk;
-  Rows<E, C, Sh::DVT, 64 * WAVES, VEC> rv;
+  constexpr int kRaw = (int)sizeof(raw);
+  const uint32_t qs = pinned((int)job.q.token * kRaw), ks = pinned((int)job.k.token * kRaw),
+                 vs = pinned((int)job.v.token * kRaw);
+  const int dk = pinned(job.Dk);
+  const int flags = pinned((job.o_vec ? 1 : 0) | (job.o_f32 ? 2 : 0));
+  const Out out = {static_cast<char*>(const_cast<void*>(job.o.p)), pinned((int)job.o.token), (flags & 1) != 0,
+                   (flags & 2) != 0};
+  Rows<E, C, DKP, 64 * WAVES, VEC> rq(qs, dk, reverse), rk(ks, dk, reverse);
+  Rows<E, C, Sh::DVT, 64 * WAVES, VEC> rv(vs, w.cols, reverse);
   auto fetch = [&](int i) {
-    const int n = min(C, hi - i);
-    const int64_t t0 = reverse ? w.s.len - i - n : i;
-    rq.load(w.q, t0, n, qs, job.Dk, reverse);
-    rk.load(w.k, t0, n, ks, job.Dk, reverse);
+    const int n = max(0, min(C, hi - i));
+    const int64_t t0 = n == 0 ? 0 : reverse ? w.s.len - i - n : i;
+    rq.load(w.q, t0, n, qs, dk, reverse);
+    rk.load(w.k, t0, n, ks, dk, reverse);
+  };
+  auto fetch_v = [&](int i) {
+    const int n = max(0, min(C, hi - i));
+    const int64_t t0 = n == 0 ? 0 : reverse ? w.s.len - i - n : i;
     rv.load(w.v, t0, n, vs, w.cols, reverse);
   };
-  if (lo < hi) fetch(lo);
+  // The next chunk's loads start as soon as the tiles are in LDS where there
+  // are registers for them through the whole chunk, else once the products with
+  // the state are done (v after those with the scores).
+  constexpr bool kEarly = C == 32 && !(DKP == 256 && IN == 3);
+  fetch(lo);
+  fetch_v(lo);
+  w.log_decay = uniform(a.log_decay[w.h]);
+  if ((int)threadIdx.x < C) weights[threadIdx.x] = state_weight(job, w.log_decay, C, p, threadIdx.x);
+  if ((int)threadIdx.x < C + 16) {
+    const int x = threadIdx.x;
+    decays[x] = x <= C ? job.oscale * job.kscale * decay_power(w.log_decay, C - x) : 0.f;
+  }
+  // Score tiles above the diagonal that the products read: zero throughout.
+  for (int x = threadIdx.x; x < OUT * Sh::kPPart / 4; x += 64 * WAVES) reinterpret_cast<uint32_t*>(pt)[x] = 0u;
+  const float d16 = uniform(decay_power(w.log_decay, 16)), decay = uniform(decay_power(w.log_decay, C));
+  const float from_state = job.oscale * decay_power(w.log_decay, l + p);  // of i = l
+
+  f32x4 S[Sh::KT][NT];
+  const size_t head = (size_t)w.b * a.H + w.h;
+  first_state<DKP, NT>(S, a, job, w, head, wave, lane);
+  bool broken = false;  // a value was not finite
+
   for (int i0 = lo; i0 < hi; i0 += C) {
     const int n = min(C, hi - i0);
+    int lane = threadIdx.x & 63;
+    keep(lane);
+    const int g = lane >> 4, l = lane & 15;
+    if (n < C && (int)threadIdx.x < C) weights[threadIdx.x] = state_weight(job, w.log_decay, n, p, threadIdx.x);
     rq.store(qt);
     rk.store(kt);
     rv.store(vt);
     __syncthreads();
-    if (i0 + C < hi) fetch(i0 + C);
+    if (kEarly) {
+      fetch(i0 + C);
+      fetch_v(i0 + C);
+    }
 
-    int rows = row_at<DKP>(l) ^ (g << 4);  // row l of a tile of 16, unit g
-    keep(rows);
+    const int rows = row_at<DKP>(l) ^ (g << 4);  // row l of a tile of 16, unit g
 
-    // Scores, as P^T = k q^T, so that a lane has 4 tokens j of one i: the
-    // tiles on and below the diagonal, dealt to the waves.
-#pragma nounroll
-    for (int x = wave; x < IT * (IT + 1) / 2; x += WAVES) {
-      const int ti = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, tj = x - ti * (ti + 1) / 2;
-      f32x4 acc = f32x4(0.f);
-      const int qa = ti * (32 * DKP), ka = tj * (32 * DKP);
+    // Scores, as P^T = k q^T, so that a lane has 4 tokens j of one i.  C = 64:
+    // a wave takes the tiles of 16 tokens i up to the diagonal; C = 32: one of
+    // the three tiles.  Which ones moves on from chunk to chunk, since they
+    // differ and a wave's number is its SIMD's.
+    const int turn = (wave + i0 / C) % 4, ti = C == 64 ? turn : (turn + 1) / 2, tj0 = C == 64 ? 0 : turn / 2;
+    if (C == 64 || turn < 3) {
+      constexpr int kTiles = C == 64 ? 4 : 1;
+      f32x4 acc[kTiles];
+#pragma unroll
+      for (int x = 0; x < kTiles; ++x) acc[x] = f32x4(0.f);
 #pragma unroll
       for (int s = 0; s < DKP / 32; ++s) {
-        b16x8 Q[IN], K[IN];
+        b16x8 Q[IN], K[kTiles][1][IN];
 #pragma unroll
         for (int c = 0; c < IN; ++c) {
-          Q[c] = read_row(qt, qa + (rows ^ (64 * s)) + c * (C * DKP * 2));
-          K[c] = read_row(kt, ka + (rows ^ (64 * s)) + c * (C * DKP * 2));
+          Q[c] = read_row(qt, ti * (32 * DKP) + (rows ^ (64 * s)) + c * (C * DKP * 2));
+#pragma unroll
+          for (int x = 0; x < kTiles; ++x)
+            if (tj0 + x <= ti) K[x][0][c] = read_row(kt, tj0 * (32 * DKP) + (rows ^ (64 * s)) + c * (C * DKP * 2) + x * (32 * DKP));
         }
-        products<IN, IN, IN - 1>(acc, K, Q);
+#pragma unroll
+        for (int x = 0; x < kTiles; ++x)
+          if (tj0 + x <= ti) {
+            f32x4 y[1] = {acc[x]};
+            products<IN, IN, IN - 1, 1>(y, K[x], Q);
+            acc[x] = y[0];
+          }
       }
-      float f[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int e = 16 * (ti - tj) + l - 4 * g - r;  // i - j
-        f[r] = e >= 0 ? acc[r] * weights[C - max(e, 0)] : 0.f;  // a masked score is 0 whatever the product is
-      }
-      uint32_t words[OUT][2];
-      split<OUT, 4>(f, words);
+      for (int x = 0; x < kTiles; ++x) {
+        const int tj = tj0 + x;
+        if (tj > ti) break;
+        const float* const d = decays + (C - 16 * (ti - tj) - l + 4 * g);  // of i - j; zeros above the diagonal
+        float f[4];
 #pragma unroll
-      for (int c = 0; c < OUT; ++c)
-        *reinterpret_cast<u32x2*>(pt + c * Sh::kPPart + 2 * ((16 * ti + l) * Sh::kPRow + 16 * tj + 4 * g)) =
-            u32x2{words[c][0], words[c][1]};
-    }
-
-    // o^T = S^T q^T, then times d^(i + p)
-    f32x4 O[IT];
-#pragma unroll
-    for (int t = 0; t < IT; ++t) O[t] = f32x4(0.f);
-#pragma unroll
-    for (int s = 0; s < DKP / 32; ++s) {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = S[2 * s + e / 4][e % 4];
-      uint32_t words[OUT][4];
-      split<OUT, 8>(x, words);
-      b16x8 A[OUT];
-#pragma unroll
-      for (int c = 0; c < OUT; ++c) A[c] = operand(words[c]);
-#pragma unroll
-      for (int t = 0; t < IT; ++t) {
-        b16x8 Q[IN];
-#pragma unroll
-        for (int c = 0; c < IN; ++c) Q[c] = read_row(qt, (rows ^ (64 * s)) + c * (C * DKP * 2) + t * (32 * DKP));
-        products<OUT, IN, OUT - 1>(O[t], A, Q);
-      }
-    }
-    float f = from_state;
-#pragma unroll
-    for (int t = 0; t < IT; ++t, f *= d16) O[t] *= f;
-    __syncthreads();  // the scores are in LDS
-
-    // o^T += oscale v^T P^T
-    b16x8 V[C / 32][IN];
-    read_values<E, Sh::DVT, C>(V, vt, wave);
-#pragma unroll
-    for (int t = 0; t < IT; ++t) {
-      f32x4 I = f32x4(0.f);
-#pragma unroll
-      for (int j = 0; j <= t / 2; ++j) {
-        b16x8 P[OUT];
+        for (int r = 0; r < 4; ++r) f[r] = acc[x][r] * d[r];
+        uint32_t words[OUT][2];
+        split<OUT, 4>(f, words);
 #pragma unroll
         for (int c = 0; c < OUT; ++c)
-          P[c] = read_row(pt, c * Sh::kPPart + 2 * ((16 * t + l) * Sh::kPRow + 32 * j + 8 * g));
-        products<IN, OUT, OUT - 1>(I, V[j], P);
+          *reinterpret_cast<u32x2*>(pt + c * Sh::kPPart + 2 * ((16 * ti + l) * Sh::kPRow + 16 * tj + 4 * g)) =
+              u32x2{words[c][0], words[c][1]};
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) O[t][r] = __builtin_fmaf(I[r], job.oscale, O[t][r]);
     }
 
-    watch(z, O);
-    {
-      // A lane has 4 neighbouring columns of token 16 t + l.
-      const bool wide = job.o_f32 || E::id == PRNN_DATA_FLOAT;
-      const int size = wide ? 4 : 2, stride = (int)job.o.token * size;
-      const int64_t t0 = reverse ? w.s.len - i0 - n : i0;
-      const __amdgpu_buffer_rsrc_t out =
-          make_rsrc(static_cast<const char*>(job.o.p) + (w.o + t0 * job.o.token) * size,
-                    (uint32_t)(n - 1) * (uint32_t)stride + (uint32_t)(w.cols * size));
-      int c0 = 16 * wave + 4 * g, row = l;
-      keep(c0);
-      keep(row);
+    // o^T = S^T q^T, 32 rows of the state at a time, which then take the
+    // chunk's tokens.  The reads of a step's operands are issued one product
+    // ahead, and held there: the compiler would move them to their use.
+    const float dn = n == C ? decay : uniform(decay_power(w.log_decay, n));
+    b16x8 D[C / 32][NT][ST];
 #pragma unroll
-      for (int t = 0; t < IT; ++t, row += 16) {
-        const uint32_t at = (uint32_t)(reverse ? n - 1 - row : row) * (uint32_t)stride + (uint32_t)(c0 * size);
-        if (!job.o_vec) {
+    for (int j = 0; j < C / 32; ++j) decayed_values<E, NT, ST, Sh::DVT, C>(D[j], vt, weights, wave, lane, j);
+    const int columns = row_at<DKP>(8 * g + (l >> 2)) ^ ((l & 3) << 4);
+    f32x4 O[IT][NT];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint32_t to = row < n && c0 + r < w.cols ? at + r * size : kOutside;
-            if (wide)
-              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(O[t][r]), out, to, 0, kPlain);
-            else if constexpr (sizeof(raw) == 2)
-              __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, E::put(O[t][r])), out, to, 0, kPlain);
-          }
-        } else {
-          const uint32_t to = row < n && c0 < w.cols ? at : kOutside;
-          if (wide) {
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t]), out, to, 0, kPlain);
-          } else {
-            typedef raw vec __attribute__((ext_vector_type(4)));
-            const vec x = {E::put(O[t][0]), E::put(O[t][1]), E::put(O[t][2]), E::put(O[t][3])};
-            if constexpr (sizeof(raw) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), out, to, 0, kPlain);
-          }
-        }
+    for (int t = 0; t < IT; ++t)
+#pragma unroll
+      for (int m = 0; m < NT; ++m) O[t][m] = f32x4(0.f);
+    b16x8 Q[2][IT][IN];
+    auto read_queries = [&](int s) {
+#pragma unroll
+      for (int t = 0; t < IT; ++t)
+#pragma unroll
+        for (int c = 0; c < IN; ++c) Q[s % 2][t][c] = read_row(qt, (rows ^ (64 * s)) + c * (C * DKP * 2) + t * (32 * DKP));
+    };
+    read_queries(0);
+#pragma unroll
+    for (int s = 0; s < DKP / 32; ++s) {
+      b16x8 K[2][C / 32][IN];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) read_keys<E, DKP, C>(K[y], kt, columns, 2 * s + y);
+      if (s + 1 < DKP / 32) read_queries(s + 1);
+      if (C == 64 && ST == 2 && VEC) __builtin_amdgcn_sched_barrier(0);
+      b16x8 A[NT][OUT];
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = S[2 * s + e / 4][m][e % 4];
+        uint32_t words[OUT][4];
+        split<OUT, 8>(x, words);
+#pragma unroll
+        for (int c = 0; c < OUT; ++c) A[m][c] = operand(words[c]);
       }
-      const float dn = n == C ? decay : decay_power(w.log_decay, n);
 #pragma unroll
-      for (int t = 0; t < Sh::KT; ++t) S[t] *= dn;
-      update_state<E, DKP, C>(S, V, kt, weights, C - n + p);
+      for (int t = 0; t < IT; ++t) products<OUT, IN, OUT - 1, NT>(O[t], A, Q[s % 2][t]);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) update_tile<E, NT, ST, C>(S[2 * s + y], D, K[y], dn);
     }
+    // times d^(i + p)
+    float f = from_state;
+#pragma unroll
+    for (int t = 0; t < IT; ++t, f *= d16)
+#pragma unroll
+      for (int m = 0; m < NT; ++m) O[t][m] *= f;
+    __syncthreads();  // the scores are in LDS
+    if (!kEarly) fetch(i0 + C);
+
+    // o^T += v^T P^T
+#pragma unroll
+    for (int j = 0; j < C / 32; ++j) {
+      b16x8 V[NT][IN], P[IT][OUT];
+      read_values<E, NT, Sh::DVT, C>(V, vt, wave, lane, j);
+#pragma unroll
+      for (int t = 2 * j; t < IT; ++t)
+#pragma unroll
+        for (int c = 0; c < OUT; ++c)
+          P[t][c] = read_row(pt, c * Sh::kPPart + 2 * ((16 * t + l) * Sh::kPRow + 32 * j + 8 * g));
+#pragma unroll
+      for (int t = 2 * j; t < IT; ++t) products<IN, OUT, OUT - 1, NT>(O[t], V, P[t]);
+    }
+    if (!kEarly) fetch_v(i0 + C);
+    float z = 0.f;
+    watch(z, O);
+    broken = broken || wave_any(z != 0.f);
+    const int64_t t0 = reverse ? w.s.len - i0 - n : i0;
+    if constexpr (sizeof(raw) == 2) {
+      if (!out.wide)
+        put_rows<E, IT, NT, false>(out, w, O, t0, n, reverse, wave, lane);
+      else
+        put_rows<E, IT, NT, true>(out, w, O, t0, n, reverse, wave, lane);
+    } else {
+      put_rows<E, IT, NT, true>(out, w, O, t0, n, reverse, wave, lane);
+    }
+
     __syncthreads();  // before the next chunk's tiles
   }
+  float z = 0.f;
   watch(z, S);
   const bool ends = last && job.s_out != nullptr;
-  if (!wave_any(z != 0.f)) {
-    if (ends) last_state<DKP>(S, job, w, head, col, lane);
-    return;
+  int after = threadIdx.x & 63;  // (its products would else be held through the loop)
+  keep(after);
+  if (broken || wave_any(z != 0.f)) {
+    first_state<DKP, NT>(S, a, job, w, head, wave, after);
+    attention_tokens<E, DKP, NT, true>(job, w, lo, hi, wave, after, S);
   }
-  first_state<DKP>(S, job, w, head, col, wave, lane);
-  attention_tokens<E, DKP, true>(job, w, lo, hi, col, lane, S);
-  if (ends) last_state<DKP>(S, job, w, head, col, lane);
+  if (ends) last_state<DKP, NT>(S, job, w, head, wave, after);
 }
 
 // -- launches of one element type --------------------------------------------------------------
@@ -788,26 +1039,33 @@ hipError_t launch_wide(K kernel, dim3 grid, int threads, int lds, const AttnArgs
   return hipLaunchKernel(fn, grid, dim3(threads), list, (size_t)lds, stream);
 }
 
-template <class E, int DKP, int WAVES, bool VEC>
+template <class E, int DKP, int NT, int WAVES, bool VEC>
 hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
-  typedef Shape<E, DKP, WAVES> Sh;
+  typedef Shape<E, DKP, NT, WAVES> Sh;
   const unsigned states = (unsigned)a.tiles * a.B * a.H;
   if (a.segments > 1) {
-    hipError_t e = launch_wide(attention_state_kernel<E, DKP, WAVES, VEC>, dim3(states * (a.segments - 1), a.jobs),
+    hipError_t e = launch_wide(attention_state_kernel<E, DKP, NT, WAVES, VEC>, dim3(states * (a.segments - 1), a.jobs),
                                64 * WAVES, Sh::kLdsState, a, stream);
     if (e != hipSuccess) return e;
-    e = launch_wide(attention_scan_kernel<DKP, WAVES>, dim3(states * (DKP * Sh::DVT / 256), a.jobs), 256, 0, a, stream);
-    if (e != hipSuccess) return e;
+    if (a.segments >= kScanFrom) {
+      e = launch_wide(attention_scan_kernel<DKP, NT, WAVES>, dim3(states * (DKP * Sh::DVT / 1024), a.jobs), 256, 0, a, stream);
+      if (e != hipSuccess) return e;
+    }
   }
-  return launch_wide(attention_chunk_kernel<E, DKP, WAVES, VEC>, dim3(states * a.segments, a.jobs), 64 * WAVES, Sh::kLds,
-                     a, stream);
+  const dim3 grid(states * a.segments, a.jobs);
+  bool whole = Parts<E>::kOut == 3;  // the state in fp32's precision: where it is fp32's output, or a state is handed on
+  for (int i = 0; i < a.jobs; ++i) whole = whole || a.job[i].s_out != nullptr;
+  if constexpr (Parts<E>::kOut < 3)
+    if (!whole)
+      return launch_wide(attention_chunk_kernel<E, DKP, NT, WAVES, VEC, 2>, grid, 64 * WAVES, Sh::kLds, a, stream);
+  return launch_wide(attention_chunk_kernel<E, DKP, NT, WAVES, VEC, 3>, grid, 64 * WAVES, Sh::kLds, a, stream);
 }
 
 template <class E, bool VEC>
 hipError_t launch_vec(const AttnArgs& a, hipStream_t stream) {
-  if (a.dkp == 64) return a.waves == 4 ? launch_shape<E, 64, 4, VEC>(a, stream) : launch_shape<E, 64, 8, VEC>(a, stream);
-  if (a.dkp == 128) return a.waves == 4 ? launch_shape<E, 128, 4, VEC>(a, stream) : launch_shape<E, 128, 8, VEC>(a, stream);
-  return a.waves == 4 ? launch_shape<E, 256, 4, VEC>(a, stream) : launch_shape<E, 256, 8, VEC>(a, stream);
+  if (a.dkp == 64) return a.nt == 1 ? launch_shape<E, 64, 1, 4, VEC>(a, stream) : launch_shape<E, 64, 2, 4, VEC>(a, stream);
+  if (a.dkp == 128) return a.nt == 1 ? launch_shape<E, 128, 1, 4, VEC>(a, stream) : launch_shape<E, 128, 2, 4, VEC>(a, stream);
+  return launch_shape<E, 256, 1, 4, VEC>(a, stream);
 }
 
 template <class E>

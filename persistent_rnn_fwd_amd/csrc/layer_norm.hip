@@ -314,8 +314,19 @@ __global__ void __launch_bounds__(1024) norm_params_kernel(const float* partial,
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.f;
-  if (c < 2ll * N)
-    for (int g = w; g < count; g += 16) s += partial[(size_t)g * 2 * N + c];
+  if (c < 2ll * N) {
+    constexpr int kAhead = 8;
+    for (int g0 = w; g0 < count; g0 += 16 * kAhead) {
+      float x[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int g = g0 + 16 * i;
+        x[i] = g < count ? partial[(size_t)g * 2 * N + c] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) s += x[i];
+    }
+  }
   part[w][lane] = s;
   __syncthreads();
   if (w != 0 || c >= 2ll * N) return;

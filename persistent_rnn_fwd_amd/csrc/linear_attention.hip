@@ -14,27 +14,27 @@ using attn::decay_power;
 using attn::Span;
 using attn::span_of;
 
-// grid: `blocks` workgroups for each sequence, one thread per element of dst at a time.
+// The heads' gradients of k and of v, summed over each group in head order.
+// grid: `blocks` workgroups for each sequence, 2; a thread one element at a time.
 template <class E>
 __global__ void __launch_bounds__(256) attention_reduce_kernel(AttnReduceArgs a) {
-  const int64_t n = (int64_t)a.T * a.groups * a.D;
-  const int b = blockIdx.x / a.blocks;
-  const Span s = span_of(a, b);
   typedef typename E::raw raw;
-  raw* dst = static_cast<raw*>(const_cast<void*>(a.dst.p));
-  const int H = a.groups * a.per_group;
+  const auto& x = a.grad[blockIdx.y];
+  const int64_t n = (int64_t)a.T * a.groups * x.D;
+  const int b = blockIdx.x / a.blocks, H = a.groups * a.per_group;
+  const Span s = span_of(a, b);
+  raw* const dst = static_cast<raw*>(const_cast<void*>(x.dst.p)) +
+                   (a.offsets != nullptr ? s.first * x.dst.token : (int64_t)b * x.dst.batch);
   for (int64_t i = (blockIdx.x % a.blocks) * 256ll + threadIdx.x; i < n; i += a.blocks * 256ll) {
-    const int d = (int)(i % a.D);
-    const int g = (int)(i / a.D % a.groups);
-    const int64_t t = i / a.D / a.groups;
+    const int d = (int)(i % x.D), g = (int)(i / x.D % a.groups);
+    const int64_t t = i / x.D / a.groups;
     if (t >= s.len && a.lengths == nullptr) break;
     // src is dense: [T][B][H][D], or [rows][H][D] packed
     const int64_t row = a.offsets != nullptr ? s.first + t : t * a.B + b;
     float sum = 0.f;
     if (t < s.len)
-      for (int j = 0; j < a.per_group; ++j) sum += a.src[(row * H + g * a.per_group + j) * a.D + d];
-    const int64_t base = a.offsets != nullptr ? s.first * a.dst.token : (int64_t)b * a.dst.batch;
-    dst[base + t * a.dst.token + (int64_t)g * a.dst.head + d] = E::put(sum);
+      for (int j = 0; j < a.per_group; ++j) sum += x.src[(row * H + g * a.per_group + j) * x.D + d];
+    dst[t * x.dst.token + (int64_t)g * x.dst.head + d] = E::put(sum);
   }
 }
 
@@ -138,15 +138,16 @@ size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
     j.o_vec = j.Dv % 8 == 0 && vectors(j.o, j.Dv, a->H / j.o.group, j.o_f32 ? 4 : e);
   }
   a->dkp = dk <= 64 ? 64 : dk <= 128 ? 128 : 256;
-  a->waves = dv > 64 ? 8 : 4;
-  const int cols = 16 * a->waves;
+  a->nt = dv > 64 && a->dkp < 256 ? 2 : 1;
+  const int cols = 64 * a->nt;
   a->tiles = (dv + cols - 1) / cols;
-  // Segments: enough workgroups for two on each compute unit, of at least 8
-  // chunks of 64 tokens (a segment's state costs k and v a second read).
-  const int64_t groups = (int64_t)a->tiles * a->B * a->H * a->jobs;
-  const int64_t want = std::max<int64_t>(1, 2 * compute_units / std::max<int64_t>(1, groups));
-  const int64_t most = std::max(1, a->T / 512);
-  const int64_t segments = std::min(want, most);
+  // Segments: as many as fill the compute units (3 workgroups on each for
+  // states of 64 x 64, else 2), of at least 64 tokens.  Packed sequences count
+  // as so many of the longest's length.
+  const int64_t sequences = a->offsets != nullptr && a->T > 0 ? std::max<int64_t>(1, std::min<int64_t>(a->B, a->rows / a->T)) : a->B;
+  const int64_t groups = std::max<int64_t>(1, a->tiles * sequences * a->H * a->jobs);
+  const int64_t want = compute_units * (a->dkp == 64 && a->nt == 1 ? 3 : 2) / groups;
+  const int64_t segments = std::max<int64_t>(1, std::min<int64_t>(want, a->T / 64));
   a->seg_tokens = std::max(64, (int)(((a->T + segments - 1) / segments + 63) / 64 * 64));
   a->segments = std::max(1, (a->T + a->seg_tokens - 1) / a->seg_tokens);
   return a->segments > 1 ? (size_t)a->segments * a->tiles * a->B * a->H * a->dkp * cols : 0;
@@ -162,9 +163,9 @@ hipError_t launch_attention(const AttnArgs& a, prnnDataType_t type, hipStream_t 
 
 hipError_t launch_attention_reduce(const AttnReduceArgs& args, prnnDataType_t type, hipStream_t stream) {
   AttnReduceArgs a = args;
-  const int64_t blocks = ((int64_t)a.T * a.groups * a.D + 255) / 256, most = a.B < 2048 ? 2048 / a.B : 1;
+  const int64_t blocks = ((int64_t)a.T * a.groups * std::max(a.grad[0].D, a.grad[1].D) + 255) / 256, most = a.B < 2048 ? 2048 / a.B : 1;
   a.blocks = (int)(blocks < most ? blocks : most);
-  const dim3 grid((unsigned)a.blocks * a.B);
+  const dim3 grid((unsigned)a.blocks * a.B, 2);
   return for_type(type, [&](auto e) {
     attention_reduce_kernel<decltype(e)><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();

@@ -355,14 +355,12 @@ prnnStatus_t prnn_linear_attention_backward(prnnHandle_t h, const prnnAttention_
     r.T = a.T;
     r.groups = d->Hkv;
     r.per_group = group;
-    r.src = work;
-    r.dst = operand(dk, 1);
-    r.D = d->Dk;
-    st = launched(launch_attention_reduce(r, d->type, stream));
-    if (st != PRNN_STATUS_SUCCESS) return st;
-    r.src = work + wide_k / 4;
-    r.dst = operand(dv, 1);
-    r.D = d->Dv;
+    r.grad[0].src = work;
+    r.grad[0].dst = operand(dk, 1);
+    r.grad[0].D = d->Dk;
+    r.grad[1].src = work + wide_k / 4;
+    r.grad[1].dst = operand(dv, 1);
+    r.grad[1].D = d->Dv;
     st = launched(launch_attention_reduce(r, d->type, stream));
   }
   if (st == PRNN_STATUS_SUCCESS) log_call(h, "linear attention backward", p);

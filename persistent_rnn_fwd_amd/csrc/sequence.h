@@ -58,7 +58,7 @@ struct AttnArgs {
   int64_t rows;
   int jobs, B, T, H;
   // set by plan_attention
-  int dkp, waves; // kernel instance: rows of the state; waves, 16 columns of it each
+  int dkp, nt;    // kernel instance: rows of the state, tiles of 16 columns a wave
   int vec;        // 16-byte loads of q, k and v
   int tiles;      // workgroups along the columns of the widest job's Dv
   int segments;   // workgroups along a sequence
@@ -75,14 +75,17 @@ hipError_t launch_attention_f16(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attention_bf16(const AttnArgs& a, hipStream_t stream);
 
 // dst[t][b][g] = sum over the heads of group g of src[t][b][H] (fp32, dense
-// rows of D), in head order.  Rows as the attention's outputs.
+// rows of D), in head order, for two gradients.  Rows as the attention's outputs.
 struct AttnReduceArgs {
-  const float* src;
-  AttnOperand dst;
+  struct {
+    const float* src;
+    AttnOperand dst;
+    int D;
+  } grad[2];
   const int32_t* lengths;
   const int32_t* offsets;
   int64_t rows;
-  int B, T, groups, per_group, D;
+  int B, T, groups, per_group;
   int blocks;  // workgroups for each sequence (set by the launch)
 };
 hipError_t launch_attention_reduce(const AttnReduceArgs& a, prnnDataType_t type, hipStream_t stream);
