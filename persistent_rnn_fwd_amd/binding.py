@@ -10,6 +10,7 @@ from __future__ import annotations
 import atexit
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -78,32 +79,9 @@ ATTENTION_MAX_D = 256  # PRNN_ATTENTION_MAX_D
 SEQUENCE_TYPES = {torch.float32: DATA_FLOAT, torch.float16: DATA_HALF, torch.bfloat16: DATA_BFLOAT}
 
 
-class Attention(ctypes.Structure):
-    """prnnAttention_t."""
-    _fields_ = [
-        ("B", ctypes.c_int),
-        ("T", ctypes.c_int),
-        ("H", ctypes.c_int),
-        ("Hkv", ctypes.c_int),
-        ("Dk", ctypes.c_int),
-        ("Dv", ctypes.c_int),
-        ("type", ctypes.c_int),
-        ("scale", ctypes.c_float),
-        ("log_decay", ctypes.c_void_p),
-        ("lengths", ctypes.c_void_p),
-        ("offsets", ctypes.c_void_p),
-        ("rows", ctypes.c_int64),
-    ]
-
-
-class Sequence(ctypes.Structure):
-    """prnnSequence_t."""
-    _fields_ = [
-        ("data", ctypes.c_void_p),
-        ("token", ctypes.c_int64),
-        ("batch", ctypes.c_int64),
-        ("head", ctypes.c_int64),
-    ]
+# prnnAttention_t, and prnnSequence_t: data, token, batch, head
+_ATTENTION = struct.Struct("@7if3Pq")
+_SEQUENCE = struct.Struct("@P3q")
 
 
 class PlanInfo(ctypes.Structure):
@@ -161,6 +139,13 @@ def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
     return s.cuda_stream
 
 
+try:  # the stream's pointer alone, without a Stream object
+    from torch._C import _cuda_getCurrentRawStream as _current_raw_stream
+except ImportError:
+    def _current_raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def _need(t: torch.Tensor, name: str, dtypes, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -188,22 +173,16 @@ def _need_strided(t: torch.Tensor, name: str, device: torch.device, dtypes, shap
         raise ValueError(f"{name} must be contiguous along its last axis")
 
 
-def _empty(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+def _empty(like: torch.Tensor, shape, dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
     """A new output that belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr() if t is not None else None
-
-
-def _sequence(t: torch.Tensor, axes) -> Sequence:
-    """axes: the tensor's axis of the tokens and of the batch (None: it has none)."""
-    token, batch = (t.stride(a) if a is not None and t.shape[a] > 1 else 0 for a in axes)
-    return Sequence(t.data_ptr(), token, batch, t.stride(-2) if t.shape[-2] > 1 else 0)
 
 
 class Handle:
@@ -215,6 +194,11 @@ class Handle:
         _check("prnn_create", self._lib.prnn_create(ctypes.byref(h)))
         self._h = h
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
+        # descriptors of one call (an attention and up to 7 sequences); the
+        # library reads them before it returns
+        self._desc = ctypes.create_string_buffer(_ATTENTION.size + 7 * _SEQUENCE.size)
+        self._desc_at = ctypes.addressof(self._desc)
 
     # -- lifetime ---------------------------------------------------------
     def close(self):
@@ -516,47 +500,81 @@ class Handle:
         return outs
 
     # -- linear attention with a decay for each head -------------------------
-    def _attention(self, q, k, v, log_decay, scale, offsets, lengths, max_len, step):
-        """Checks the inputs; the descriptor, the axes of tokens and batch, the
-        leading shape of q and the shape of the states."""
+    # (The checks are written for few Python calls: a step's kernel takes a
+    # few microseconds.)
+    def _stream(self, stream):
+        return _stream_ptr(stream) if stream is not None else _current_raw_stream(self._index)
+
+    def _strided(self, t, name, dtype, shape):
+        """t's strides, once it is what it should be."""
+        if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != self._index
+                or (t.stride(-1) != 1 and shape[-1] > 1)):
+            _need_strided(t, name, self.device, (dtype,), shape)
+        return t.stride()
+
+    def _dense(self, t, name, dtype, shape):
+        if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != self._index
+                or not t.is_contiguous()):
+            _need(t, name, (dtype,), shape)
+            _need_strided(t, name, self.device, (dtype,), shape)  # another GPU's
+        return t.data_ptr()
+
+    def _attention(self, q, k, v, log_decay, scale, offsets, lengths, max_len, step, more):
+        """Checks the inputs, writes the descriptors of the attention, of q, k
+        and v and of the sequences in `more` (heads, head size, dtype, tensor
+        or None for a new one, name, stream), and returns those tensors and the
+        shape of the states."""
         lead = 1 if step or offsets is not None else 2
         for t, name in ((q, "q"), (k, "k"), (v, "v")):
             if not isinstance(t, torch.Tensor) or t.dim() != lead + 2:
                 raise ValueError(f"{name} must have {lead + 2} axes")
-        H, Dk = q.shape[-2:]
+        dtype = q.dtype
+        code = SEQUENCE_TYPES.get(dtype)
+        if code is None:
+            raise TypeError(f"q must have dtype in {tuple(SEQUENCE_TYPES)}, got {dtype}")
+        *rows, H, Dk = q.shape
         Hkv, Dv = v.shape[-2:]
-        rows = tuple(q.shape[:-2])
-        if q.dtype not in SEQUENCE_TYPES:
-            raise TypeError(f"q must have dtype in {tuple(SEQUENCE_TYPES)}, got {q.dtype}")
-        _need_strided(q, "q", self.device, (q.dtype,), rows + (H, Dk))
-        _need_strided(k, "k", self.device, (q.dtype,), rows + (Hkv, Dk))
-        _need_strided(v, "v", self.device, (q.dtype,), rows + (Hkv, Dv))
-        _need(log_decay, "log_decay", (torch.float32,), (H,))
-        if offsets is not None and lengths is not None:
-            raise ValueError("give offsets (packed sequences) or lengths, not both")
-        a = Attention(H=H, Hkv=Hkv, Dk=Dk, Dv=Dv, type=SEQUENCE_TYPES[q.dtype],
-                      scale=Dk ** -0.5 if scale is None else scale, log_decay=log_decay.data_ptr())
+        rows = tuple(rows)
+        total, at_lengths, at_offsets = 0, None, None
         if step:
-            a.B, a.T, axes = rows[0], 1, (None, 0)
+            B, T, axes = rows[0], 1, (None, 0)
         elif offsets is not None:
-            if offsets.dim() != 1 or offsets.shape[0] < 1:
-                raise ValueError("offsets must be [B + 1]")
-            _need(offsets, "offsets", (torch.int32,), offsets.shape)
-            a.B, a.T, a.rows = offsets.shape[0] - 1, rows[0] if max_len is None else int(max_len), rows[0]
-            a.offsets, axes = offsets.data_ptr(), (0, None)
-        else:
-            a.T, a.B = rows
-            axes = (0, 1)
             if lengths is not None:
-                _need(lengths, "lengths", (torch.int32,), (a.B,))
-                a.lengths = lengths.data_ptr()
-        return a, axes, rows, (a.B, H, Dk, Dv)
+                raise ValueError("give offsets (packed sequences) or lengths, not both")
+            if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
+                raise ValueError("offsets must be [B + 1]")
+            B, total, axes = offsets.shape[0] - 1, rows[0], (0, None)
+            T = total if max_len is None else int(max_len)
+            at_offsets = self._dense(offsets, "offsets", torch.int32, (B + 1,))
+        else:
+            (T, B), axes = rows, (0, 1)
+            if lengths is not None:
+                at_lengths = self._dense(lengths, "lengths", torch.int32, (B,))
+        _ATTENTION.pack_into(self._desc, 0, B, T, H, Hkv, Dk, Dv, code, Dk ** -0.5 if scale is None else scale,
+                             self._dense(log_decay, "log_decay", torch.float32, (H,)), at_lengths or 0,
+                             at_offsets or 0, total)
+        at = _ATTENTION.size
+        outs = []
+        token, batch = axes
+        shapes = {"H": H, "Hkv": Hkv, "Dk": Dk, "Dv": Dv}
+        for t, name, heads, size, stream in (
+                (q, "q", "H", "Dk", 0), (k, "k", "Hkv", "Dk", 0), (v, "v", "Hkv", "Dv", 0), *more):
+            shape = (*rows, shapes[heads], shapes[size])
+            if t is None:
+                t = _empty(q, shape, dtype, stream)
+                strides = t.stride()
+            else:
+                strides = self._strided(t, name, dtype, shape)
+            _SEQUENCE.pack_into(self._desc, at, t.data_ptr(),
+                                strides[token] if token is not None and shape[token] > 1 else 0,
+                                strides[batch] if batch is not None and shape[batch] > 1 else 0,
+                                strides[-2] if shape[-2] > 1 else 0)
+            at += _SEQUENCE.size
+            outs.append(t)
+        return outs[3:], (B, H, Dk, Dv)
 
-    def _sequence_out(self, out, name, dtype, shape, stream):
-        if out is None:
-            return _empty(shape, dtype, self.device, stream)
-        _need_strided(out, name, self.device, (dtype,), shape)
-        return out
+    def _state(self, t, name, shape):
+        return self._dense(t, name, torch.float32, shape) if t is not None else None
 
     def linear_attention(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
                          scale: Optional[float] = None, initial_state: Optional[torch.Tensor] = None,
@@ -573,16 +591,13 @@ class Handle:
         and max_len the longest sequence's tokens (None: rows).
         initial_state (None: zeros) and final_state (written, may be the
         initial one) are fp32 [B, H, Dk, Dv]."""
-        a, axes, rows, state = self._attention(q, k, v, log_decay, scale, offsets, lengths, max_len, False)
-        for t, name in ((initial_state, "initial_state"), (final_state, "final_state")):
-            if t is not None:
-                _need(t, name, (torch.float32,), state)
-        out = self._sequence_out(out, "out", q.dtype, rows + (a.H, a.Dv), stream)
-        seqs = [_sequence(t, axes) for t in (q, k, v, out)]
-        r = [ctypes.byref(x) for x in seqs]
+        (out,), state = self._attention(q, k, v, log_decay, scale, offsets, lengths, max_len, False,
+                                        ((out, "out", "H", "Dv", stream),))
+        a = self._desc_at
+        s = a + _ATTENTION.size
         _check("prnn_linear_attention", self._lib.prnn_linear_attention(
-            self._h, ctypes.byref(a), r[0], r[1], r[2], _ptr(initial_state), r[3], _ptr(final_state),
-            _stream_ptr(stream)))
+            self._h, a, s, s + 32, s + 64, self._state(initial_state, "initial_state", state), s + 96,
+            self._state(final_state, "final_state", state), self._stream(stream)))
         return out
 
     def linear_attention_backward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
@@ -597,19 +612,18 @@ class Handle:
         """Gradients of linear_attention: (dq, dk, dv), and into grad_initial_state
         where it is given.  The inputs are those of the forward call; the decays
         are constants."""
-        a, axes, rows, state = self._attention(q, k, v, log_decay, scale, offsets, lengths, max_len, False)
-        _need_strided(grad_out, "grad_out", self.device, (q.dtype,), rows + (a.H, a.Dv))
-        for t, name in ((initial_state, "initial_state"), (grad_final_state, "grad_final_state"),
-                        (grad_initial_state, "grad_initial_state")):
-            if t is not None:
-                _need(t, name, (torch.float32,), state)
-        grads = [self._sequence_out(t, name, q.dtype, of.shape, stream)
-                 for t, name, of in ((grad_q, "grad_q", q), (grad_k, "grad_k", k), (grad_v, "grad_v", v))]
-        seqs = [_sequence(t, axes) for t in (q, k, v, grad_out, *grads)]
-        r = [ctypes.byref(x) for x in seqs]
+        if grad_out is None:
+            raise TypeError("grad_out must be a torch tensor")
+        (_, *grads), state = self._attention(
+            q, k, v, log_decay, scale, offsets, lengths, max_len, False,
+            ((grad_out, "grad_out", "H", "Dv", None), (grad_q, "grad_q", "H", "Dk", stream),
+             (grad_k, "grad_k", "Hkv", "Dk", stream), (grad_v, "grad_v", "Hkv", "Dv", stream)))
+        a = self._desc_at
+        s = a + _ATTENTION.size
         _check("prnn_linear_attention_backward", self._lib.prnn_linear_attention_backward(
-            self._h, ctypes.byref(a), r[0], r[1], r[2], _ptr(initial_state), r[3], _ptr(grad_final_state), r[4], r[5],
-            r[6], _ptr(grad_initial_state), _stream_ptr(stream)))
+            self._h, a, s, s + 32, s + 64, self._state(initial_state, "initial_state", state), s + 96,
+            self._state(grad_final_state, "grad_final_state", state), s + 128, s + 160, s + 192,
+            self._state(grad_initial_state, "grad_initial_state", state), self._stream(stream)))
         return tuple(grads)
 
     def linear_attention_step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
@@ -619,34 +633,49 @@ class Handle:
         """One new token of every sequence: q [B, H, Dk], k [B, Hkv, Dk], v [B, Hkv,
         Dv] give o [B, H, Dv].  state fp32 [B, H, Dk, Dv] is updated in place, or
         left as it is and the new one written to new_state."""
-        a, axes, rows, shape = self._attention(q, k, v, log_decay, scale, None, None, None, True)
-        _need(state, "state", (torch.float32,), shape)
-        if new_state is None:
-            new_state = state
-        _need(new_state, "new_state", (torch.float32,), shape)
-        out = self._sequence_out(out, "out", q.dtype, rows + (a.H, a.Dv), stream)
-        seqs = [_sequence(t, axes) for t in (q, k, v, out)]
-        r = [ctypes.byref(x) for x in seqs]
+        (out,), shape = self._attention(q, k, v, log_decay, scale, None, None, None, True,
+                                        ((out, "out", "H", "Dv", stream),))
+        a = self._desc_at
+        s = a + _ATTENTION.size
+        s0 = self._dense(state, "state", torch.float32, shape)
+        s1 = s0 if new_state is None else self._dense(new_state, "new_state", torch.float32, shape)
         _check("prnn_linear_attention_step", self._lib.prnn_linear_attention_step(
-            self._h, ctypes.byref(a), r[0], r[1], r[2], state.data_ptr(), r[3], new_state.data_ptr(),
-            _stream_ptr(stream)))
+            self._h, a, s, s + 32, s + 64, s0, s + 96, s1, self._stream(stream)))
         return out
 
     # -- layer norm -------------------------------------------------------------
-    def _norm_rows(self, t, name, dtypes, shape):
+    def _norm_rows(self, t, name, dtype, shape):
         """The rows of t [..., N]: how many, and the elements from one to the next."""
-        _need_strided(t, name, self.device, dtypes, shape)
-        N = t.shape[-1]
+        strides = self._strided(t, name, dtype, shape)
+        N = shape[-1]
+        if len(shape) == 2:
+            return (shape[0], strides[0]) if shape[0] > 1 else (shape[0], N)
         M, ld = 1, N
-        for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
             if size == 1:
                 continue
             if M == 1:
                 ld = stride
-            elif t.numel() > 0 and stride != ld * M:
+            elif stride != ld * M and t.numel() > 0:
                 raise ValueError(f"the rows of {name} must lie at one stride")
             M *= size
         return M, max(ld, N) if M <= 1 else ld
+
+    def _norm_params(self, params, dtype, N):
+        """Pointers of [N] parameters (None where absent), and their type's code."""
+        ptype = None
+        for p, name in params:
+            if p is not None:
+                ptype = p.dtype if ptype is None else ptype
+                if ptype != dtype and ptype != torch.float32:
+                    raise TypeError(f"{name} must have dtype in {(torch.float32, dtype)}, got {ptype}")
+        ptype = torch.float32 if ptype is None else ptype
+        return [None if p is None else self._dense(p, name, ptype, (N,)) for p, name in params], SEQUENCE_TYPES[ptype]
+
+    def _norm_type(self, x):
+        if not isinstance(x, torch.Tensor) or x.dtype not in SEQUENCE_TYPES or x.dim() < 1:
+            raise TypeError(f"x must be a tensor with dtype in {tuple(SEQUENCE_TYPES)}")
+        return SEQUENCE_TYPES[x.dtype]
 
     def layer_norm(self, x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                    eps: float = 1e-5, *, out: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
@@ -655,21 +684,19 @@ class Handle:
         bf16); weight and bias [N], fp32 or x's dtype, or None.  mean and rstd
         (fp32, x's shape without its last axis) are written where given, for
         the backward pass; out may be x."""
-        M, ldx = self._norm_rows(x, "x", tuple(SEQUENCE_TYPES), x.shape)
-        N, lead = x.shape[-1], tuple(x.shape[:-1])
-        pdtype = next((p.dtype for p in (weight, bias) if p is not None), torch.float32)
-        for p, name in ((weight, "weight"), (bias, "bias")):
-            if p is not None:
-                _need(p, name, (pdtype,) if pdtype in (torch.float32, x.dtype) else (torch.float32, x.dtype), (N,))
-        for t, name in ((mean, "mean"), (rstd, "rstd")):
-            if t is not None:
-                _need(t, name, (torch.float32,), lead)
+        code, shape = self._norm_type(x), x.shape
+        M, ldx = self._norm_rows(x, "x", x.dtype, shape)
+        (w, b), pcode = self._norm_params(((weight, "weight"), (bias, "bias")), x.dtype, shape[-1])
+        m = None if mean is None else self._dense(mean, "mean", torch.float32, shape[:-1])
+        r = None if rstd is None else self._dense(rstd, "rstd", torch.float32, shape[:-1])
         if out is None:
-            out = _empty(x.shape, x.dtype, self.device, stream)
-        _, ldy = self._norm_rows(out, "out", (x.dtype,), x.shape)
+            out = _empty(x, shape, x.dtype, stream)
+            ldy = shape[-1]
+        else:
+            _, ldy = self._norm_rows(out, "out", x.dtype, shape)
         _check("prnn_layer_norm", self._lib.prnn_layer_norm(
-            self._h, M, N, SEQUENCE_TYPES[x.dtype], x.data_ptr(), ldx, SEQUENCE_TYPES[pdtype], _ptr(weight), _ptr(bias),
-            eps, out.data_ptr(), ldy, _ptr(mean), _ptr(rstd), _stream_ptr(stream)))
+            self._h, M, shape[-1], code, x.data_ptr(), ldx, pcode, w, b, eps, out.data_ptr(), ldy, m, r,
+            self._stream(stream)))
         return out
 
     def layer_norm_backward(self, grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -679,25 +706,25 @@ class Handle:
         """Gradients of layer_norm: (dx, dweight, dbias).  dweight and dbias have
         weight's dtype; without a weight they are computed only into the
         buffers given, and are None otherwise."""
-        M, ldx = self._norm_rows(x, "x", tuple(SEQUENCE_TYPES), x.shape)
-        N, lead = x.shape[-1], tuple(x.shape[:-1])
-        _, lddy = self._norm_rows(grad_out, "grad_out", (x.dtype,), x.shape)
-        _need(mean, "mean", (torch.float32,), lead)
-        _need(rstd, "rstd", (torch.float32,), lead)
-        pdtype = next((p.dtype for p in (weight, grad_weight, grad_bias) if p is not None), torch.float32)
+        code, shape = self._norm_type(x), x.shape
+        N = shape[-1]
+        M, ldx = self._norm_rows(x, "x", x.dtype, shape)
+        _, lddy = self._norm_rows(grad_out, "grad_out", x.dtype, shape)
+        m = self._dense(mean, "mean", torch.float32, shape[:-1])
+        r = self._dense(rstd, "rstd", torch.float32, shape[:-1])
         if weight is not None:
-            grad_weight = _empty((N,), pdtype, self.device, stream) if grad_weight is None else grad_weight
-            grad_bias = _empty((N,), pdtype, self.device, stream) if grad_bias is None else grad_bias
-        for p, name in ((weight, "weight"), (grad_weight, "grad_weight"), (grad_bias, "grad_bias")):
-            if p is not None:
-                _need(p, name, (pdtype,) if pdtype in (torch.float32, x.dtype) else (torch.float32, x.dtype), (N,))
+            grad_weight = _empty(x, (N,), weight.dtype, stream) if grad_weight is None else grad_weight
+            grad_bias = _empty(x, (N,), weight.dtype, stream) if grad_bias is None else grad_bias
+        (w, dw, db), pcode = self._norm_params(
+            ((weight, "weight"), (grad_weight, "grad_weight"), (grad_bias, "grad_bias")), x.dtype, N)
         if grad_x is None:
-            grad_x = _empty(x.shape, x.dtype, self.device, stream)
-        _, lddx = self._norm_rows(grad_x, "grad_x", (x.dtype,), x.shape)
+            grad_x = _empty(x, shape, x.dtype, stream)
+            lddx = N
+        else:
+            _, lddx = self._norm_rows(grad_x, "grad_x", x.dtype, shape)
         _check("prnn_layer_norm_backward", self._lib.prnn_layer_norm_backward(
-            self._h, M, N, SEQUENCE_TYPES[x.dtype], grad_out.data_ptr(), lddy, x.data_ptr(), ldx, mean.data_ptr(),
-            rstd.data_ptr(), SEQUENCE_TYPES[pdtype], _ptr(weight), grad_x.data_ptr(), lddx, _ptr(grad_weight),
-            _ptr(grad_bias), _stream_ptr(stream)))
+            self._h, M, N, code, grad_out.data_ptr(), lddy, x.data_ptr(), ldx, m, r, pcode, w, grad_x.data_ptr(), lddx,
+            dw, db, self._stream(stream)))
         return grad_x, grad_weight, grad_bias
 
     def sync_floor(self, N: int, B: int, T: int, out: Optional[torch.Tensor] = None,
