@@ -12,6 +12,7 @@
 // from row to row, so the parameters' gradients are sums in registers; each
 // workgroup leaves one partial sum and a second kernel adds those in a fixed
 // order.
+#include "device_common.h"
 #include "sequence.h"
 
 namespace prnn {
@@ -37,15 +38,22 @@ __device__ __forceinline__ void load_param(const void* p, int n, bool in, float 
   }
 }
 
-// Sums over the TPR threads of a row, the same value in each of them.  `slot`
-// is the row's LDS: TPR / 64 values (TPR > 64 only; every thread of the
-// workgroup calls).
+// Sums over the TPR threads of a row, the same value in each of them: within
+// rows of 16 lanes, across them, and across the waves through `slot`, the
+// row's LDS of TPR / 64 values (TPR > 64 only; every thread of the workgroup
+// calls).
 template <int TPR, int K>
 __device__ __forceinline__ void row_sums(float (&x)[K], float* slot) {
 #pragma unroll
-  for (int m = 1; m < (TPR < 64 ? TPR : 64); m *= 2)
-#pragma unroll
-    for (int i = 0; i < K; ++i) x[i] += __shfl_xor(x[i], m);
+  for (int i = 0; i < K; ++i) {
+    x[i] = dpp_row_sum(x[i]);
+    if constexpr (TPR >= 64) {
+      float y = x[i];
+      swap16_add(x[i], y);
+      y = x[i];
+      swap32_add(x[i], y);
+    }
+  }
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     const int w = threadIdx.x % TPR / 64;
@@ -103,14 +111,13 @@ __global__ void __launch_bounds__(BLOCK) norm_kernel(NormArgs a) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int n = (i + j * TPR) * V;
-    if (n >= a.N) break;
     float w[V], b[V];
-    load_param<P, V>(a.weight, n, true, 1.f, w);
-    load_param<P, V>(a.bias, n, true, 0.f, b);
+    load_param<P, V>(a.weight, n, n < a.N, 1.f, w);
+    load_param<P, V>(a.bias, n, n < a.N, 0.f, b);
     vec out;
 #pragma unroll
     for (int e = 0; e < V; ++e) out[e] = E::put(__builtin_fmaf((E::get(xv[j][e]) - mean) * rstd, w[e], b[e]));
-    *reinterpret_cast<vec*>(y + n) = out;
+    if (n < a.N) *reinterpret_cast<vec*>(y + n) = out;
   }
   if (i == 0) {
     if (a.mean != nullptr) a.mean[m] = mean;
@@ -161,11 +168,14 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(NormArgs a) {
   extern __shared__ float comb[];  // [R - 1][V NV][TPR]
   const int i = threadIdx.x % TPR, r = threadIdx.x / TPR;
   float* slot = slots + 2 * r * (TPR / 64);
-  float dw[NV][V], db[NV][V];
+  float dw[NV][V], db[NV][V], w[NV][V];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    const int n = (i + j * TPR) * V;
+    load_param<P, V>(a.weight, n, n < a.N, 1.f, w[j]);
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[j][e] = db[j][e] = 0.f;
+  }
   vec xn[NV], dn[NV];
   auto fetch = [&](int64_t m) {
     const raw* x = static_cast<const raw*>(a.x) + m * a.ldx;
@@ -198,12 +208,10 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(NormArgs a) {
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int n = (i + j * TPR) * V;
-      float w[V];
-      load_param<P, V>(a.weight, n, n < a.N, 1.f, w);
+      // (columns past N: dy is 0 there, and so is all that follows)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float d = E::get(dv[j][e]), c = n < a.N ? (E::get(xv[j][e]) - mean) * rstd : 0.f, g = d * w[e];
+        const float d = E::get(dv[j][e]), c = (E::get(xv[j][e]) - mean) * rstd, g = d * w[j][e];
         dw[j][e] = __builtin_fmaf(d, c, dw[j][e]);
         db[j][e] += d;
         s[0] += g;
@@ -217,16 +225,13 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int n = (i + j * TPR) * V;
-        if (n >= a.N) break;
-        float w[V];
-        load_param<P, V>(a.weight, n, true, 1.f, w);
         vec out;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float c = (E::get(xv[j][e]) - mean) * rstd, g = E::get(dv[j][e]) * w[e];
+          const float c = (E::get(xv[j][e]) - mean) * rstd, g = E::get(dv[j][e]) * w[j][e];
           out[e] = E::put(rstd * (g - g0 - c * g1));
         }
-        *reinterpret_cast<vec*>(dx + n) = out;
+        if (n < a.N) *reinterpret_cast<vec*>(dx + n) = out;
       }
     }
   }
@@ -339,18 +344,19 @@ __global__ void __launch_bounds__(1024) norm_params_kernel(const float* partial,
 
 // Threads a row (TPR) and vectors a thread (NV) for rows of N: the fewest
 // threads whose registers hold the row, so that most of a vector load's lanes
-// are used; vectors of 16 bytes, or single elements.
+// are used; vectors of 16 bytes, up to `columns` elements a thread, or single
+// elements.
 struct Shape {
   bool vec;
   int tpr, nv;  // tpr 0: the row does not fit
 };
-Shape shape_of(int N, int elems, bool vec) {
+Shape shape_of(int N, int elems, bool vec, int columns) {
   Shape s = {vec, 0, 0};
   const int units = vec ? N / elems : N;
   if (vec) {
     static const int kShapes[][2] = {{16, 1}, {16, 2}, {16, 4}, {64, 2}, {64, 4}, {256, 2}, {256, 3}, {256, 4}, {512, 3}, {512, 4}, {512, 6}};
     for (const auto& p : kShapes)
-      if (p[0] * p[1] >= units && p[1] * elems <= 32) {  // more columns a thread do not fit the backward pass's registers
+      if (p[0] * p[1] >= units && p[1] * elems <= columns) {
         s.tpr = p[0];
         s.nv = p[1];
         return s;
@@ -375,7 +381,7 @@ Shape shape_for(const NormArgs& a, prnnDataType_t type, bool backward) {
   bool vec = a.N % elems == 0 && a.ldx % elems == 0 && aligned16(a.x) && aligned16(a.weight) && aligned16(a.bias) &&
              (a.y == nullptr || (a.ldy % elems == 0 && aligned16(a.y)));
   if (backward) vec = vec && a.lddy % elems == 0 && aligned16(a.dy);
-  return shape_of(a.N, elems, vec);
+  return shape_of(a.N, elems, vec, backward ? 24 : 32);  // (the backward pass holds five values a column)
 }
 
 constexpr int block_of(int tpr) { return tpr > 256 ? tpr : 256; }
@@ -395,8 +401,9 @@ struct Config {
   static constexpr int v = V, tpr = TPR, nv = NV, block = block_of(TPR);
 };
 
-// Calls f(Config) for the shape; false when the row does not fit.
-template <int V, class F>
+// Calls f(Config) for the shape; false when the row does not fit.  COLUMNS: as
+// shape_of's.
+template <int V, int COLUMNS, class F>
 bool for_shape(const Shape& s, F f) {
 #define PRNN_SHAPE(VV, TPR, NV)                 \
   if (s.tpr == TPR && s.nv == NV) {             \
@@ -404,9 +411,14 @@ bool for_shape(const Shape& s, F f) {
     return true;                                \
   }
   if (s.vec) {
-    PRNN_SHAPE(V, 16, 1) PRNN_SHAPE(V, 16, 2) PRNN_SHAPE(V, 16, 4) PRNN_SHAPE(V, 64, 2) PRNN_SHAPE(V, 64, 4)
-    PRNN_SHAPE(V, 256, 2) PRNN_SHAPE(V, 256, 3) PRNN_SHAPE(V, 256, 4) PRNN_SHAPE(V, 512, 3)
-    PRNN_SHAPE(V, 512, 4)
+    PRNN_SHAPE(V, 16, 1) PRNN_SHAPE(V, 16, 2) PRNN_SHAPE(V, 64, 2)
+    if constexpr (V == 4 || COLUMNS == 32) {
+      PRNN_SHAPE(V, 16, 4) PRNN_SHAPE(V, 64, 4)
+    }
+    PRNN_SHAPE(V, 256, 2) PRNN_SHAPE(V, 256, 3) PRNN_SHAPE(V, 512, 3)
+    if constexpr (V == 4 || COLUMNS == 32) {
+      PRNN_SHAPE(V, 256, 4) PRNN_SHAPE(V, 512, 4)
+    }
     if constexpr (V == 4) {
       PRNN_SHAPE(V, 512, 6)
     }
@@ -426,7 +438,7 @@ hipError_t launch_layer_norm(const NormArgs& a, prnnDataType_t type, prnnDataTyp
     typedef decltype(e) E;
     typedef decltype(p) P;
     constexpr int V = E::id == PRNN_DATA_FLOAT ? 4 : 8;
-    const bool fits = for_shape<V>(s, [&](auto c) {
+    const bool fits = for_shape<V, 32>(s, [&](auto c) {
       typedef decltype(c) C;
       const int64_t grid = (a.M + C::block / C::tpr - 1) / (C::block / C::tpr);
       norm_kernel<E, P, C::v, C::tpr, C::nv, C::block><<<(unsigned)grid, C::block, 0, stream>>>(a);
@@ -441,7 +453,10 @@ int layer_norm_backward_grid(const NormArgs& a, prnnDataType_t type, int compute
   if (s.tpr == 0) return (int)(a.M < 64 ? a.M : 64);
   const int R = block_of(s.tpr) / s.tpr;
   const int64_t sets = (a.M + R - 1) / R;
-  const int64_t most = 2ll * compute_units;
+  // Two workgroups of 256 threads on a compute unit, one of 512: more leave
+  // more partial sums than their loads in flight gain.  Measured (1 / 2 / 3 on
+  // each): 16384 x 5760 bf16 137 / 125 / 139 us, 3000 x 12000 bf16 58 / 76 / 98.
+  const int64_t most = (s.tpr > 256 ? 1ll : 2ll) * compute_units;
   return (int)(sets < most ? sets : most);
 }
 
@@ -453,7 +468,7 @@ hipError_t launch_layer_norm_backward(const NormArgs& a, prnnDataType_t type, pr
     typedef decltype(p) P;
     constexpr int V = E::id == PRNN_DATA_FLOAT ? 4 : 8;
     if (grid > 0) {
-      const bool fits = for_shape<V>(s, [&](auto c) {
+      const bool fits = for_shape<V, 24>(s, [&](auto c) {
         typedef decltype(c) C;
         constexpr int R = C::block / C::tpr;
         norm_backward_kernel<E, P, C::v, C::tpr, C::nv, C::block>
