@@ -5,37 +5,66 @@
 //   with n = (x - mean) rstd and g = dy w
 //
 // Both passes are bound by memory: x in and y out, or x and dy in and dx out.
-// A row is read once into the registers of TPR threads, 16 bytes at a time
-// where width, strides and addresses allow it (V elements a vector, NV vectors
-// a thread), so mean and variance are sums over centred values without a
-// second read.  In the backward pass the threads of a row keep their columns
-// from row to row, so the parameters' gradients are sums in registers; each
-// workgroup leaves one partial sum and a second kernel adds those in a fixed
-// order.
+// A row is read once into the registers of TPR threads, 16 bytes at a time (V
+// elements a vector, NV vectors a thread), so mean and variance are sums over
+// centred values without a second read.  The threads of a row set keep their
+// columns from row to row: the parameters stay in registers, the next row's
+// loads are in flight during this row's sums, and the parameters' gradients are
+// sums in registers; each workgroup leaves one partial sum of them and a second
+// kernel adds those in a fixed order.  Sums and statistics are fp32; y, dx and
+// the parameters' gradients are rounded once.
+//
+// Rows whose width, stride or address no 16-byte vector divides use the same
+// vectors unaligned, the last one moved back to end with the row: 50000 x 500
+// bf16 backward takes 33 us against 100 with that vector read by elements, whose
+// waits end the loads ahead.
+//
+// Measured: forward 16384 x 5760 bf16 71-75 us (5.2 TB/s; with the parameters
+// read again for every row 90), backward 115 us (4.9 TB/s, a few percent of it
+// the partial sums), 4099 x 1153 fp32 backward 18 us.
 #include "device_common.h"
 #include "sequence.h"
 
 namespace prnn {
 namespace {
 
-template <class E, int V>
+// V neighbouring elements of a row of N.  ODD: rows start at any element and the
+// last vector of a row may overlap the one before it, since it ends where the row
+// does; else every vector is aligned and the last one ends there by itself.
+template <class E, int V, bool ODD>
 struct Vec {
   typedef typename E::raw raw;
   typedef raw type __attribute__((ext_vector_type(V)));
+  typedef raw any __attribute__((ext_vector_type(V), aligned(ODD ? sizeof(raw) : sizeof(type))));
+  static __device__ __forceinline__ type load(const raw* p, bool live, raw absent) {
+    return live ? *reinterpret_cast<const any*>(p) : type(absent);
+  }
+  static __device__ __forceinline__ void store(raw* p, bool live, const type& v) {
+    if (live) *reinterpret_cast<any*>(p) = v;
+  }
+};
+
+// Vector c of a row of N: its first column, whether it exists, and how many of
+// its columns the vector before it has.
+template <int V, bool ODD>
+struct Columns {
+  int n, again;
+  bool in;
+  __device__ __forceinline__ Columns(int c, int N) : n(c * V), again(0), in(c * V < N) {
+    if (ODD && in && n + V > N) {
+      again = n + V - N;
+      n = N - V;
+    }
+  }
+  __device__ __forceinline__ bool own(int e) const { return !ODD || e >= again; }
 };
 
 // Parameters: fp32 or the rows' own type; absent ones are a constant.
-template <class P, int V>
+template <class P, int V, bool ODD>
 __device__ __forceinline__ void load_param(const void* p, int n, bool in, float absent, float (&f)[V]) {
-  typedef typename Vec<P, V>::type vec;
-  if (p != nullptr && in) {
-    const vec v = *reinterpret_cast<const vec*>(static_cast<const typename P::raw*>(p) + n);
+  const auto v = Vec<P, V, ODD>::load(static_cast<const typename P::raw*>(p) + n, p != nullptr && in, P::put(absent));
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = P::get(v[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = absent;
-  }
+  for (int e = 0; e < V; ++e) f[e] = P::get(v[e]);
 }
 
 // Sums over the TPR threads of a row, the same value in each of them: within
@@ -71,57 +100,78 @@ __device__ __forceinline__ void row_sums(float (&x)[K], float* slot) {
   }
 }
 
-template <class E, class P, int V, int TPR, int NV, int BLOCK>
+// Forward.  The grid's row sets take rows r, r + R grid, ...; thread i of a set
+// keeps the parameters of vectors i + j TPR.  The next row's loads are issued
+// before this row's sums.
+template <class E, class P, int V, bool ODD, int TPR, int NV, int BLOCK>
 __global__ void __launch_bounds__(BLOCK) norm_kernel(NormArgs a) {
   typedef typename E::raw raw;
-  typedef typename Vec<E, V>::type vec;
+  typedef Vec<E, V, ODD> Row;
+  typedef Columns<V, ODD> Cols;
+  constexpr int R = BLOCK / TPR;
   __shared__ float slots[BLOCK / 64 + 1];
   const int i = threadIdx.x % TPR, r = threadIdx.x / TPR;
   float* slot = slots + r * (TPR / 64);
-  const int64_t m = (int64_t)blockIdx.x * (BLOCK / TPR) + r;
-  const bool live = m < a.M;
-  const raw* x = static_cast<const raw*>(a.x) + m * a.ldx;
-  vec xv[NV];
-  float s[1] = {0.f};
+  typename Row::type xn[NV];
+  auto fetch = [&](int64_t m) {
+    const raw* x = static_cast<const raw*>(a.x) + m * a.ldx;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int n = (i + j * TPR) * V;
-    xv[j] = live && n < a.N ? *reinterpret_cast<const vec*>(x + n) : vec(raw(0));
-  }
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < V; ++e) s[0] += E::get(xv[j][e]);
-  row_sums<TPR>(s, slot);
-  const float mean = s[0] / (float)a.N;
-  s[0] = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const bool in = (i + j * TPR) * V < a.N;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float c = E::get(xv[j][e]) - mean;
-      s[0] += in ? c * c : 0.f;
+    for (int j = 0; j < NV; ++j) {
+      const Cols c(i + j * TPR, a.N);
+      xn[j] = Row::load(x + c.n, m < a.M && c.in, raw(0));
     }
-  }
-  row_sums<TPR>(s, slot);
-  const float rstd = 1.f / sqrtf(s[0] / (float)a.N + a.eps);
-  if (!live) return;
-  raw* y = static_cast<raw*>(a.y) + m * a.ldy;
+  };
+  fetch((int64_t)blockIdx.x * R + r);
+  float w[NV][V], b[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int n = (i + j * TPR) * V;
-    float w[V], b[V];
-    load_param<P, V>(a.weight, n, n < a.N, 1.f, w);
-    load_param<P, V>(a.bias, n, n < a.N, 0.f, b);
-    vec out;
-#pragma unroll
-    for (int e = 0; e < V; ++e) out[e] = E::put(__builtin_fmaf((E::get(xv[j][e]) - mean) * rstd, w[e], b[e]));
-    if (n < a.N) *reinterpret_cast<vec*>(y + n) = out;
+    const Cols c(i + j * TPR, a.N);
+    load_param<P, V, ODD>(a.weight, c.n, c.in, 1.f, w[j]);
+    load_param<P, V, ODD>(a.bias, c.n, c.in, 0.f, b[j]);
   }
-  if (i == 0) {
-    if (a.mean != nullptr) a.mean[m] = mean;
-    if (a.rstd != nullptr) a.rstd[m] = rstd;
+  const int64_t step = (int64_t)gridDim.x * R;
+  for (int64_t m0 = (int64_t)blockIdx.x * R; m0 < a.M; m0 += step) {
+    const int64_t m = m0 + r;
+    float x[NV][V], s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const Cols c(i + j * TPR, a.N);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        x[j][e] = E::get(xn[j][e]);
+        s[0] += c.own(e) ? x[j][e] : 0.f;
+      }
+    }
+    fetch(m + step);
+    row_sums<TPR>(s, slot);
+    const float mean = s[0] / (float)a.N;
+    s[0] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const Cols c(i + j * TPR, a.N);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        x[j][e] -= mean;
+        s[0] += c.in && c.own(e) ? x[j][e] * x[j][e] : 0.f;
+      }
+    }
+    row_sums<TPR>(s, slot);
+    const float rstd = 1.f / sqrtf(s[0] / (float)a.N + a.eps);
+    if (m < a.M) {
+      raw* y = static_cast<raw*>(a.y) + m * a.ldy;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const Cols c(i + j * TPR, a.N);
+        typename Row::type out;
+#pragma unroll
+        for (int e = 0; e < V; ++e) out[e] = E::put(__builtin_fmaf(x[j][e] * rstd, w[j][e], b[j][e]));
+        Row::store(y + c.n, c.in, out);
+      }
+      if (i == 0) {
+        if (a.mean != nullptr) a.mean[m] = mean;
+        if (a.rstd != nullptr) a.rstd[m] = rstd;
+      }
+    }
   }
 }
 
@@ -147,8 +197,8 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(NormArgs a) {
   const float rstd = 1.f / sqrtf(s[0] / (float)a.N + a.eps);
   for (int n = threadIdx.x; n < a.N; n += 1024) {
     float w[1], b[1];
-    load_param<P, 1>(a.weight, n, true, 1.f, w);
-    load_param<P, 1>(a.bias, n, true, 0.f, b);
+    load_param<P, 1, false>(a.weight, n, true, 1.f, w);
+    load_param<P, 1, false>(a.bias, n, true, 0.f, b);
     y[n] = E::put(__builtin_fmaf((E::get(x[n]) - mean) * rstd, w[0], b[0]));
   }
   if (threadIdx.x == 0) {
@@ -157,61 +207,58 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(NormArgs a) {
   }
 }
 
-// Backward.  The grid's row sets take rows r, r + R grid, ...; thread i of a
-// set keeps columns V (i + j TPR) .. + V - 1.
-template <class E, class P, int V, int TPR, int NV, int BLOCK>
+// Backward, in the same way; what a vector has again counts in dx alone.
+template <class E, class P, int V, bool ODD, int TPR, int NV, int BLOCK>
 __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(NormArgs a) {
   typedef typename E::raw raw;
-  typedef typename Vec<E, V>::type vec;
+  typedef Vec<E, V, ODD> Row;
+  typedef typename Row::type vec;
+  typedef Columns<V, ODD> Cols;
   constexpr int R = BLOCK / TPR;
   __shared__ float slots[2 * (BLOCK / 64) + 2];
   extern __shared__ float comb[];  // [R - 1][V NV][TPR]
   const int i = threadIdx.x % TPR, r = threadIdx.x / TPR;
   float* slot = slots + 2 * r * (TPR / 64);
-  float dw[NV][V], db[NV][V], w[NV][V];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int n = (i + j * TPR) * V;
-    load_param<P, V>(a.weight, n, n < a.N, 1.f, w[j]);
-#pragma unroll
-    for (int e = 0; e < V; ++e) dw[j][e] = db[j][e] = 0.f;
-  }
   vec xn[NV], dn[NV];
   auto fetch = [&](int64_t m) {
     const raw* x = static_cast<const raw*>(a.x) + m * a.ldx;
     const raw* dy = static_cast<const raw*>(a.dy) + m * a.lddy;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int n = (i + j * TPR) * V;
-      const bool in = m < a.M && n < a.N;
-      xn[j] = in ? *reinterpret_cast<const vec*>(x + n) : vec(raw(0));
-      dn[j] = in ? *reinterpret_cast<const vec*>(dy + n) : vec(raw(0));
+      const Cols c(i + j * TPR, a.N);
+      xn[j] = Row::load(x + c.n, m < a.M && c.in, raw(0));
+      dn[j] = Row::load(dy + c.n, m < a.M && c.in, raw(0));
     }
   };
-  // The next row's loads are issued before this row's sums where there are
-  // registers for them.
-  constexpr bool kAhead = V > 1 || NV <= 16;
+  fetch((int64_t)blockIdx.x * R + r);
+  float dw[NV][V], db[NV][V], w[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const Cols c(i + j * TPR, a.N);
+    load_param<P, V, ODD>(a.weight, c.n, c.in, 1.f, w[j]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) dw[j][e] = db[j][e] = 0.f;
+  }
   const int64_t step = (int64_t)gridDim.x * R;
-  if (kAhead) fetch((int64_t)blockIdx.x * R + r);
   for (int64_t m0 = (int64_t)blockIdx.x * R; m0 < a.M; m0 += step) {
     const int64_t m = m0 + r;
     const bool live = m < a.M;
     const float mean = live ? a.mean_in[m] : 0.f, rstd = live ? a.rstd_in[m] : 0.f;
     vec xv[NV], dv[NV];
-    if (!kAhead) fetch(m);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       xv[j] = xn[j];
       dv[j] = dn[j];
     }
-    if (kAhead) fetch(m + step);
+    fetch(m + step);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      // (columns past N: dy is 0 there, and so is all that follows)
+      // (vectors that do not exist: dy is 0 there, and so is all that follows)
+      const Cols k(i + j * TPR, a.N);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float d = E::get(dv[j][e]), c = (E::get(xv[j][e]) - mean) * rstd, g = d * w[j][e];
+        const float d = k.own(e) ? E::get(dv[j][e]) : 0.f, c = (E::get(xv[j][e]) - mean) * rstd, g = d * w[j][e];
         dw[j][e] = __builtin_fmaf(d, c, dw[j][e]);
         db[j][e] += d;
         s[0] += g;
@@ -224,14 +271,14 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(NormArgs a) {
       raw* dx = static_cast<raw*>(a.y) + m * a.ldy;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int n = (i + j * TPR) * V;
+        const Cols k(i + j * TPR, a.N);
         vec out;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float c = (E::get(xv[j][e]) - mean) * rstd, g = E::get(dv[j][e]) * w[j][e];
           out[e] = E::put(rstd * (g - g0 - c * g1));
         }
-        if (n < a.N) *reinterpret_cast<vec*>(dx + n) = out;
+        Row::store(dx + k.n, k.in, out);
       }
     }
   }
@@ -251,14 +298,15 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(NormArgs a) {
     }
     if (r == 0) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        const Cols k(i + j * TPR, a.N);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           float t = which ? db[j][e] : dw[j][e];
           for (int q = 0; q < R - 1; ++q) t += comb[(q * NV * V + j * V + e) * TPR + i];
-          const int n = (i + j * TPR) * V + e;
-          if (n < a.N) out[(size_t)which * a.N + n] = t;
+          if (k.in && k.own(e)) out[(size_t)which * a.N + k.n + e] = t;
         }
+      }
     }
   }
 }
@@ -276,7 +324,7 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(NormArgs a) {
   float s[2] = {0.f, 0.f};
   for (int n = threadIdx.x; n < a.N; n += 1024) {
     float w[1];
-    load_param<P, 1>(a.weight, n, true, 1.f, w);
+    load_param<P, 1, false>(a.weight, n, true, 1.f, w);
     const float g = E::get(dy[n]) * w[0];
     s[0] += g;
     s[1] = __builtin_fmaf(g, (E::get(x[n]) - mean) * rstd, s[1]);
@@ -285,7 +333,7 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(NormArgs a) {
   const float g0 = s[0] / (float)a.N, g1 = s[1] / (float)a.N;
   for (int n = threadIdx.x; n < a.N; n += 1024) {
     float w[1];
-    load_param<P, 1>(a.weight, n, true, 1.f, w);
+    load_param<P, 1, false>(a.weight, n, true, 1.f, w);
     const float c = (E::get(x[n]) - mean) * rstd, g = E::get(dy[n]) * w[0];
     dx[n] = E::put(rstd * (g - g0 - c * g1));
   }
@@ -344,44 +392,30 @@ __global__ void __launch_bounds__(1024) norm_params_kernel(const float* partial,
 
 // Threads a row (TPR) and vectors a thread (NV) for rows of N: the fewest
 // threads whose registers hold the row, so that most of a vector load's lanes
-// are used; vectors of 16 bytes, up to `columns` elements a thread, or single
-// elements.
+// are used; vectors of 16 bytes, up to `columns` elements a thread.
 struct Shape {
-  bool vec;
+  bool odd;
   int tpr, nv;  // tpr 0: the row does not fit
 };
-Shape shape_of(int N, int elems, bool vec, int columns) {
-  Shape s = {vec, 0, 0};
-  const int units = vec ? N / elems : N;
-  if (vec) {
-    static const int kShapes[][2] = {{16, 1}, {16, 2}, {16, 4}, {64, 2}, {64, 4}, {256, 2}, {256, 3}, {256, 4}, {512, 3}, {512, 4}, {512, 6}};
-    for (const auto& p : kShapes)
-      if (p[0] * p[1] >= units && p[1] * elems <= columns) {
-        s.tpr = p[0];
-        s.nv = p[1];
-        return s;
-      }
-  } else {
-    static const int kShapes[][2] = {{16, 8}, {64, 4}, {64, 8}, {256, 5}, {256, 8}, {512, 8}, {512, 16}, {512, 24}};
-    for (const auto& p : kShapes)
-      if (p[0] * p[1] >= units) {
-        s.tpr = p[0];
-        s.nv = p[1];
-        return s;
-      }
-  }
-  return s;
+Shape shape_of(int N, int elems, bool odd, int columns) {
+  static const int kShapes[][2] = {{16, 1},  {16, 2},  {64, 1},  {64, 2},  {64, 3},  {128, 2}, {128, 3},
+                                   {256, 2}, {256, 3}, {256, 4}, {512, 3}, {512, 4}, {512, 6}};
+  const int units = (N + elems - 1) / elems;
+  if (N < elems) return {odd, 0, 0};  // (narrower than a vector: as the widest)
+  for (const auto& p : kShapes)
+    if (p[0] * p[1] >= units && p[1] * elems <= columns) return {odd, p[0], p[1]};
+  return {odd, 0, 0};
 }
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
-// Whether every row and parameter vector starts at a multiple of 16 bytes.
+// (odd: not every row and parameter vector starts at a multiple of 16 bytes)
 Shape shape_for(const NormArgs& a, prnnDataType_t type, bool backward) {
   const int elems = type == PRNN_DATA_FLOAT ? 4 : 8;
-  bool vec = a.N % elems == 0 && a.ldx % elems == 0 && aligned16(a.x) && aligned16(a.weight) && aligned16(a.bias) &&
-             (a.y == nullptr || (a.ldy % elems == 0 && aligned16(a.y)));
-  if (backward) vec = vec && a.lddy % elems == 0 && aligned16(a.dy);
-  return shape_of(a.N, elems, vec, backward ? 24 : 32);  // (the backward pass holds five values a column)
+  bool whole = a.N % elems == 0 && a.ldx % elems == 0 && aligned16(a.x) && aligned16(a.weight) && aligned16(a.bias) &&
+               (a.y == nullptr || (a.ldy % elems == 0 && aligned16(a.y)));
+  if (backward) whole = whole && a.lddy % elems == 0 && aligned16(a.dy);
+  return shape_of(a.N, elems, !whole, backward ? 24 : 32);  // (the backward pass holds five values a column)
 }
 
 constexpr int block_of(int tpr) { return tpr > 256 ? tpr : 256; }
@@ -396,38 +430,31 @@ hipError_t for_types(prnnDataType_t type, prnnDataType_t ptype, F f) {
   }
 }
 
-template <int V, int TPR, int NV>
+template <int V, bool ODD, int TPR, int NV>
 struct Config {
   static constexpr int v = V, tpr = TPR, nv = NV, block = block_of(TPR);
+  static constexpr bool odd = ODD;
 };
 
 // Calls f(Config) for the shape; false when the row does not fit.  COLUMNS: as
 // shape_of's.
-template <int V, int COLUMNS, class F>
+template <int V, int COLUMNS, bool ODD, class F>
 bool for_shape(const Shape& s, F f) {
-#define PRNN_SHAPE(VV, TPR, NV)                 \
-  if (s.tpr == TPR && s.nv == NV) {             \
-    f(Config<VV, TPR, NV>());                   \
-    return true;                                \
-  }
-  if (s.vec) {
-    PRNN_SHAPE(V, 16, 1) PRNN_SHAPE(V, 16, 2) PRNN_SHAPE(V, 64, 2)
-    if constexpr (V == 4 || COLUMNS == 32) {
-      PRNN_SHAPE(V, 16, 4) PRNN_SHAPE(V, 64, 4)
+#define PRNN_SHAPE(TPR, NV)                   \
+  if constexpr (NV * V <= COLUMNS)            \
+    if (s.tpr == TPR && s.nv == NV) {         \
+      f(Config<V, ODD, TPR, NV>());           \
+      return true;                            \
     }
-    PRNN_SHAPE(V, 256, 2) PRNN_SHAPE(V, 256, 3) PRNN_SHAPE(V, 512, 3)
-    if constexpr (V == 4 || COLUMNS == 32) {
-      PRNN_SHAPE(V, 256, 4) PRNN_SHAPE(V, 512, 4)
-    }
-    if constexpr (V == 4) {
-      PRNN_SHAPE(V, 512, 6)
-    }
-  } else {
-    PRNN_SHAPE(1, 16, 8) PRNN_SHAPE(1, 64, 4) PRNN_SHAPE(1, 64, 8) PRNN_SHAPE(1, 256, 5) PRNN_SHAPE(1, 256, 8)
-    PRNN_SHAPE(1, 512, 8) PRNN_SHAPE(1, 512, 16) PRNN_SHAPE(1, 512, 24)
-  }
+  PRNN_SHAPE(16, 1) PRNN_SHAPE(16, 2) PRNN_SHAPE(64, 1) PRNN_SHAPE(64, 2) PRNN_SHAPE(64, 3) PRNN_SHAPE(128, 2)
+  PRNN_SHAPE(128, 3) PRNN_SHAPE(256, 2) PRNN_SHAPE(256, 3) PRNN_SHAPE(256, 4) PRNN_SHAPE(512, 3) PRNN_SHAPE(512, 4)
+  PRNN_SHAPE(512, 6)
 #undef PRNN_SHAPE
   return false;
+}
+template <int V, int COLUMNS, class F>
+bool for_shape(const Shape& s, F f) {
+  return s.odd ? for_shape<V, COLUMNS, true>(s, f) : for_shape<V, COLUMNS, false>(s, f);
 }
 
 }  // namespace
@@ -440,8 +467,11 @@ hipError_t launch_layer_norm(const NormArgs& a, prnnDataType_t type, prnnDataTyp
     constexpr int V = E::id == PRNN_DATA_FLOAT ? 4 : 8;
     const bool fits = for_shape<V, 32>(s, [&](auto c) {
       typedef decltype(c) C;
-      const int64_t grid = (a.M + C::block / C::tpr - 1) / (C::block / C::tpr);
-      norm_kernel<E, P, C::v, C::tpr, C::nv, C::block><<<(unsigned)grid, C::block, 0, stream>>>(a);
+      const int64_t sets = (a.M + C::block / C::tpr - 1) / (C::block / C::tpr);
+      // Four workgroups on a compute unit.  Measured (1 / 2 / 4 / 8 on each / one for every row set): 16384 x 5760
+      // bf16 119 / 75 / 73 / 72 / 87 us, 50000 x 500 bf16 24 / 19 / 20 / 19 / 21, 3000 x 4096 fp32 21 / 17 / 16 / 16 / 16.
+      const int64_t most = 4ll * a.compute_units, grid = sets < most ? sets : most;
+      norm_kernel<E, P, C::v, C::odd, C::tpr, C::nv, C::block><<<(unsigned)grid, C::block, 0, stream>>>(a);
     });
     if (!fits) norm_wide_kernel<E, P><<<(unsigned)a.M, 1024, 0, stream>>>(a);
     return hipGetLastError();
@@ -455,7 +485,7 @@ int layer_norm_backward_grid(const NormArgs& a, prnnDataType_t type, int compute
   const int64_t sets = (a.M + R - 1) / R;
   // Two workgroups of 256 threads on a compute unit, one of 512: more leave
   // more partial sums than their loads in flight gain.  Measured (1 / 2 / 3 on
-  // each): 16384 x 5760 bf16 137 / 125 / 139 us, 3000 x 12000 bf16 58 / 76 / 98.
+  // each): 16384 x 5760 bf16 140 / 115 / 133 us, 3000 x 12000 bf16 48 / 58 / 70.
   const int64_t most = (s.tpr > 256 ? 1ll : 2ll) * compute_units;
   return (int)(sets < most ? sets : most);
 }
@@ -471,7 +501,7 @@ hipError_t launch_layer_norm_backward(const NormArgs& a, prnnDataType_t type, pr
       const bool fits = for_shape<V, 24>(s, [&](auto c) {
         typedef decltype(c) C;
         constexpr int R = C::block / C::tpr;
-        norm_backward_kernel<E, P, C::v, C::tpr, C::nv, C::block>
+        norm_backward_kernel<E, P, C::v, C::odd, C::tpr, C::nv, C::block>
             <<<grid, C::block, (R - 1) * C::v * C::nv * C::tpr * 4, stream>>>(a);
       });
       if (!fits) {

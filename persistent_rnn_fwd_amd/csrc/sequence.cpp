@@ -444,6 +444,7 @@ prnnStatus_t prnn_layer_norm(prnnHandle_t h, int64_t M, int N, prnnDataType_t ty
   a.ldx = ldx;
   a.ldy = ldy;
   a.eps = eps;
+  a.compute_units = handle_compute_units(h);
   return launched(launch_layer_norm(a, type, ptype, stream));
 }
 

@@ -118,6 +118,7 @@ struct NormArgs {
   int64_t M, ldx, ldy, lddy;
   int N;
   float eps;
+  int compute_units;   // forward: of the device
 };
 hipError_t launch_layer_norm(const NormArgs& a, prnnDataType_t type, prnnDataType_t ptype, hipStream_t stream);
 // Workgroups of the backward pass (each leaves one partial sum).
