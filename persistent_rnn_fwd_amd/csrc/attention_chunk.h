@@ -548,12 +548,10 @@ __device__ __forceinline__ void read_keys(b16x8 (&K)[C / 32][Parts<E>::kIn], con
     }
 }
 
-// S <- decay S + k^T (D of all the chunk's tokens), for 16 rows of the state.
+// S += k^T (D of all the chunk's tokens), for 16 rows of the state.
 template <class E, int NT, int ST, int C>
 __device__ __forceinline__ void update_tile(f32x4 (&S)[NT], const b16x8 (&D)[C / 32][NT][ST],
-                                            const b16x8 (&K)[C / 32][Parts<E>::kIn], float decay) {
-#pragma unroll
-  for (int m = 0; m < NT; ++m) S[m] *= decay;
+                                            const b16x8 (&K)[C / 32][Parts<E>::kIn]) {
 #pragma unroll
   for (int j = 0; j < C / 32; ++j) products<Parts<E>::kIn, ST, ST - 1, NT>(S, K[j], D[j]);
 }
@@ -646,7 +644,11 @@ __device__ __forceinline__ void last_state(const f32x4 (&S)[DKP / 16][NT], const
   }
 }
 
-// Slots 0 .. segments - 2: grid tiles x B H x (segments - 1), jobs.
+// Slots 0 .. segments - 2: grid tiles x B H x (segments - 1), jobs.  The chunks
+// are taken from a segment's last to its first, each weighted for the tokens
+// behind it: the state itself is not touched between products, and the main
+// kernel, which starts where this one ends, finds the tokens it reads first in
+// the caches.
 template <class E, int DKP, int NT, int WAVES, bool VEC>
 __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs a) {
   typedef Shape<E, DKP, NT, WAVES> Sh;
@@ -666,15 +668,18 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs
   Rows<E, C, DKP, 64 * WAVES, VEC> rk(ks, job.Dk, job.reverse);
   Rows<E, C, Sh::DVT, 64 * WAVES, VEC> rv(vs, w.cols, job.reverse);
   auto fetch = [&](int i) {
-    const int n = max(0, min(C, hi - i));
+    const int n = i < lo ? 0 : min(C, hi - i);
     const int64_t t0 = n == 0 ? 0 : job.reverse ? w.s.len - i - n : i;
     rk.load(w.k, t0, n, ks, job.Dk, job.reverse);
     rv.load(w.v, t0, n, vs, w.cols, job.reverse);
   };
-  fetch(lo);
+  const bool used = hi < w.s.len;  // a segment follows
+  if (!used && w.seg > 0) return;
+  const int end = lo + (hi - lo - 1) / C * C;  // the last chunk's first token
+  if (used) fetch(end);
   w.log_decay = uniform(a.log_decay[w.h]);
-  if ((int)threadIdx.x < C) weights[threadIdx.x] = state_weight(job, w.log_decay, C, p, threadIdx.x);
   const float decay = uniform(decay_power(w.log_decay, C));
+  const float weight = (int)threadIdx.x < C ? state_weight(job, w.log_decay, C, p, threadIdx.x) : 0.f;
   const size_t head = (size_t)w.b * a.H + w.h;
   f32x4 S[Sh::KT][NT];
   auto start = [&]() {
@@ -695,15 +700,25 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs
       for (int m = 0; m < NT; ++m) to[(t * NT + m) * 64] = S[t][m];
   };
   start();
-  if (w.seg == 0) put(a.segments - 1);
-  for (int i = lo; i < hi; i += C) {
+  if (w.seg == 0) {
+    put(a.segments - 1);
+    if (!used) return;
+    const float whole = uniform(decay_power(w.log_decay, hi - lo));
+#pragma unroll
+    for (int t = 0; t < Sh::KT; ++t)
+#pragma unroll
+      for (int m = 0; m < NT; ++m) S[t][m] *= whole;
+  }
+  float after = 1.f;  // decay of the tokens behind the chunk
+  for (int i = end; i >= lo; i -= C) {
     const int n = min(C, hi - i);
-    if (n < C && (int)threadIdx.x < C) weights[threadIdx.x] = state_weight(job, w.log_decay, n, p, threadIdx.x);
+    if ((int)threadIdx.x < C)
+      weights[threadIdx.x] = n == C ? weight * after : state_weight(job, w.log_decay, n, p, threadIdx.x);
+    after = n == C ? after * decay : uniform(decay_power(w.log_decay, n));
     rk.store(kt);
     rv.store(vt);
     __syncthreads();
-    fetch(i + C);
-    const float dn = n == C ? decay : uniform(decay_power(w.log_decay, n));
+    fetch(i - C);
     b16x8 D[C / 32][NT][3];
 #pragma unroll
     for (int j = 0; j < C / 32; ++j) decayed_values<E, NT, 3, Sh::DVT, C>(D[j], vt, weights, wave, lane, j);
@@ -712,7 +727,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs
     for (int t = 0; t < Sh::KT; ++t) {
       b16x8 K[C / 32][Parts<E>::kIn];
       read_keys<E, DKP, C>(K, kt, base, t);
-      update_tile<E, NT, 3, C>(S[t], D, K, dn);
+      update_tile<E, NT, 3, C>(S[t], D, K);
     }
     __syncthreads();
   }
@@ -727,25 +742,26 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs
 
 // Turns the segments' own states into the sequence's states after them, 4
 // elements a thread, the loads of 8 slots ahead.  grid: tiles x B H x (DKP DVT /
-// 1024) workgroups, jobs.  (Slots that a sequence does not reach hold what no
-// one reads.)
+// 1024) workgroups, jobs.  (Slots that a sequence does not reach stay as they are:
+// no one reads them.)
 template <int DKP, int NT, int WAVES>
 __global__ void __launch_bounds__(256) attention_scan_kernel(AttnArgs a) {
   constexpr int DVT = 16 * NT * WAVES, kBlocks = DKP * DVT / 1024, kAhead = 8;
   const AttnJob& job = a.job[blockIdx.y];
-  const int id = blockIdx.x / kBlocks, h = id / a.tiles % a.H;
+  const int id = blockIdx.x / kBlocks, bh = id / a.tiles, h = bh % a.H;
   if (id % a.tiles * DVT >= job.Dv) return;
+  const int reached = (span_of(a, bh / a.H).len + a.seg_tokens - 1) / a.seg_tokens - 1;  // slots that are read
   const float whole = decay_power(a.log_decay[h], a.seg_tokens);
   f32x4* p = reinterpret_cast<f32x4*>(job.segments) + (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t step = (int64_t)a.B * a.H * a.tiles * (DKP * DVT / 4);
   f32x4 S = *p;
-  for (int i0 = 1; i0 < a.segments - 1; i0 += kAhead) {
+  for (int i0 = 1; i0 < reached; i0 += kAhead) {
     f32x4 own[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) own[i] = i0 + i < a.segments - 1 ? p[(i0 + i) * step] : f32x4(0.f);
+    for (int i = 0; i < kAhead; ++i) own[i] = i0 + i < reached ? p[(i0 + i) * step] : f32x4(0.f);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (i0 + i >= a.segments - 1) break;
+      if (i0 + i >= reached) break;
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[r] = __builtin_fmaf(S[r], whole, own[i][r]);
       p[(i0 + i) * step] = S;
@@ -972,7 +988,11 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_chunk_kernel(AttnArgs
 #pragma unroll
       for (int t = 0; t < IT; ++t) products<OUT, IN, OUT - 1, NT>(O[t], A, Q[s % 2][t]);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) update_tile<E, NT, ST, C>(S[2 * s + y], D, K[y], dn);
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int m = 0; m < NT; ++m) S[2 * s + y][m] *= dn;
+        update_tile<E, NT, ST, C>(S[2 * s + y], D, K[y]);
+      }
     }
     // times d^(i + p)
     float f = from_state;

@@ -15,26 +15,43 @@ using attn::Span;
 using attn::span_of;
 
 // The heads' gradients of k and of v, summed over each group in head order.
-// grid: `blocks` workgroups for each sequence, 2; a thread one element at a time.
-template <class E>
+// grid: `blocks` workgroups for each sequence, 2; a thread 4 columns of one row
+// and group at a time (VEC: D % 4 == 0), else one.
+template <class E, bool VEC>
 __global__ void __launch_bounds__(256) attention_reduce_kernel(AttnReduceArgs a) {
   typedef typename E::raw raw;
+  constexpr int W = VEC ? 4 : 1;
+  typedef float vec __attribute__((ext_vector_type(W)));
+  typedef raw out __attribute__((ext_vector_type(W), aligned(sizeof(raw))));
   const auto& x = a.grad[blockIdx.y];
-  const int64_t n = (int64_t)a.T * a.groups * x.D;
+  const uint32_t per_row = (uint32_t)(a.groups * (x.D / W)), per_group = (uint32_t)(x.D / W);
   const int b = blockIdx.x / a.blocks, H = a.groups * a.per_group;
   const Span s = span_of(a, b);
   raw* const dst = static_cast<raw*>(const_cast<void*>(x.dst.p)) +
                    (a.offsets != nullptr ? s.first * x.dst.token : (int64_t)b * x.dst.batch);
-  for (int64_t i = (blockIdx.x % a.blocks) * 256ll + threadIdx.x; i < n; i += a.blocks * 256ll) {
-    const int d = (int)(i % x.D), g = (int)(i / x.D % a.groups);
-    const int64_t t = i / x.D / a.groups;
-    if (t >= s.len && a.lengths == nullptr) break;
+  const int rows = a.lengths != nullptr ? a.T : s.len;  // (padding: zeros)
+  const uint32_t step = (uint32_t)a.blocks * 256u;
+  uint32_t i = (blockIdx.x % a.blocks) * 256u + threadIdx.x;
+  uint32_t t = i / per_row, at = i - t * per_row;
+  const uint32_t dt = step / per_row, dat = step - dt * per_row;
+  for (; t < (uint32_t)rows; t += dt, at += dat) {
+    if (at >= per_row) {
+      at -= per_row;
+      if (++t >= (uint32_t)rows) break;
+    }
+    const uint32_t g = at / per_group;
+    const int d = (int)(at - g * per_group) * W;
     // src is dense: [T][B][H][D], or [rows][H][D] packed
-    const int64_t row = a.offsets != nullptr ? s.first + t : t * a.B + b;
-    float sum = 0.f;
-    if (t < s.len)
-      for (int j = 0; j < a.per_group; ++j) sum += x.src[(row * H + g * a.per_group + j) * x.D + d];
-    dst[t * x.dst.token + (int64_t)g * x.dst.head + d] = E::put(sum);
+    const int64_t row = a.offsets != nullptr ? s.first + t : (int64_t)t * a.B + b;
+    vec sum = vec(0.f);
+    if ((int)t < s.len) {
+      const float* src = x.src + (row * H + (int)g * a.per_group) * x.D + d;
+      for (int j = 0; j < a.per_group; ++j, src += x.D) sum += *reinterpret_cast<const vec*>(src);
+    }
+    out y;
+#pragma unroll
+    for (int e = 0; e < W; ++e) y[e] = E::put(sum[e]);
+    *reinterpret_cast<out*>(dst + (int64_t)t * x.dst.token + (int64_t)g * x.dst.head + d) = y;
   }
 }
 
@@ -115,6 +132,8 @@ hipError_t for_type(prnnDataType_t type, F f) {
   }
 }
 
+bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
 }  // namespace
 
 size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
@@ -163,11 +182,17 @@ hipError_t launch_attention(const AttnArgs& a, prnnDataType_t type, hipStream_t 
 
 hipError_t launch_attention_reduce(const AttnReduceArgs& args, prnnDataType_t type, hipStream_t stream) {
   AttnReduceArgs a = args;
-  const int64_t blocks = ((int64_t)a.T * a.groups * std::max(a.grad[0].D, a.grad[1].D) + 255) / 256, most = a.B < 2048 ? 2048 / a.B : 1;
+  const bool vec = a.grad[0].D % 4 == 0 && a.grad[1].D % 4 == 0 && aligned16(a.grad[0].src) && aligned16(a.grad[1].src);
+  const int64_t blocks = ((int64_t)a.T * a.groups * std::max(a.grad[0].D, a.grad[1].D) / (vec ? 4 : 1) + 255) / 256,
+                most = a.B < 2048 ? 2048 / a.B : 1;
   a.blocks = (int)(blocks < most ? blocks : most);
   const dim3 grid((unsigned)a.blocks * a.B, 2);
   return for_type(type, [&](auto e) {
-    attention_reduce_kernel<decltype(e)><<<grid, 256, 0, stream>>>(a);
+    typedef decltype(e) E;
+    if (vec)
+      attention_reduce_kernel<E, true><<<grid, 256, 0, stream>>>(a);
+    else
+      attention_reduce_kernel<E, false><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();
   });
 }
