@@ -74,6 +74,12 @@ constexpr int chunk_tokens() {
   return E::id == PRNN_DATA_BFLOAT && DKP <= 128 ? 64 : 32;
 }
 
+// n / d, with inverse_of(d): the estimate is right or one less.
+__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t d, uint32_t inverse) {
+  const uint32_t q = __umulhi(n, inverse);
+  return n - q * d >= d ? q + 1 : q;
+}
+
 // First row and number of tokens of sequence b (see prnnAttention_t).
 struct Span {
   int64_t first;
@@ -100,7 +106,7 @@ __device__ __forceinline__ Span span_of(const A& a, int b) {  // b the same in e
 // Element offset of token 0 of sequence b, head h, of an operand.
 template <class A>
 __device__ __forceinline__ int64_t base_of(const AttnOperand& x, const A& a, const Span& s, int b, int h) {
-  return (a.offsets != nullptr ? s.first * x.token : (int64_t)b * x.batch) + (int64_t)(h / x.group) * x.head;
+  return (a.offsets != nullptr ? s.first * x.token : (int64_t)b * x.batch) + (int64_t)divide((uint32_t)h, (uint32_t)x.group, x.inverse) * x.head;
 }
 
 // exp(log_decay n) to fp32's precision: the product's rounding error re-enters
@@ -386,25 +392,30 @@ template <class E, int DKP, int NT, int WAVES>
 __device__ __forceinline__ bool where(const AttnArgs& a, const AttnJob& job, int segments, Where& w) {
   typedef typename E::raw raw;
   constexpr int DVT = 16 * NT * WAVES;
-  int id = blockIdx.x;
-  w.col0 = id % a.tiles * DVT;
-  const int tile = id % a.tiles;
-  id /= a.tiles;
-  const int bh = id % (a.B * a.H);
-  w.seg = id / (a.B * a.H);
-  w.b = bh / a.H;
-  w.h = bh % a.H;
+  // Every argument that the first loads need, and every cache line of the
+  // others, at once: read where they are used, they take one trip to memory
+  // after another.
+  const AttnOperand q = job.q, k = job.k, v = job.v;
+  asm volatile("" ::"s"(q.p), "s"(q.token), "s"(q.batch), "s"(q.head), "s"(q.group), "s"(q.inverse), "s"(k.p),
+               "s"(k.token), "s"(k.batch), "s"(k.head), "s"(k.group), "s"(k.inverse), "s"(v.p), "s"(v.token),
+               "s"(v.batch), "s"(v.head), "s"(v.group), "s"(v.inverse), "s"(a.lengths), "s"(a.offsets), "s"(a.rows),
+               "s"(a.B), "s"(a.T), "s"(a.H), "s"(a.tiles), "s"(a.seg_tokens), "s"(a.by_tiles), "s"(job.Dv),
+               "s"(job.o.p), "s"(job.s_out), "s"(job.reverse));
+  const uint32_t id = blockIdx.x, state = divide(id, a.tiles, a.by_tiles), tile = id - state * a.tiles;
+  const uint32_t states = (uint32_t)a.B * a.H, seg = divide(state, states, a.by_states), bh = state - seg * states;
+  w.col0 = (int)tile * DVT;
+  w.seg = (int)seg;
+  w.b = (int)divide(bh, a.H, a.by_heads);
+  w.h = (int)bh - w.b * a.H;
   w.cols = job.Dv - w.col0;
   if (w.cols <= 0) return false;
   w.s = span_of(a, w.b);
-  w.q = static_cast<const char*>(job.q.p) + base_of(job.q, a, w.s, w.b, w.h) * (int64_t)sizeof(raw);
-  w.k = static_cast<const char*>(job.k.p) + base_of(job.k, a, w.s, w.b, w.h) * (int64_t)sizeof(raw);
-  w.v = static_cast<const char*>(job.v.p) + (base_of(job.v, a, w.s, w.b, w.h) + w.col0) * (int64_t)sizeof(raw);
+  w.q = static_cast<const char*>(q.p) + base_of(q, a, w.s, w.b, w.h) * (int64_t)sizeof(raw);
+  w.k = static_cast<const char*>(k.p) + base_of(k, a, w.s, w.b, w.h) * (int64_t)sizeof(raw);
+  w.v = static_cast<const char*>(v.p) + (base_of(v, a, w.s, w.b, w.h) + w.col0) * (int64_t)sizeof(raw);
   w.o = base_of(job.o, a, w.s, w.b, w.h) + w.col0;
-  w.states = job.segments == nullptr
-                 ? nullptr
-                 : job.segments + ((int64_t)bh * a.tiles + tile) * (DKP * DVT);
-  w.slot = (int64_t)a.B * a.H * a.tiles * (DKP * DVT);
+  w.states = job.segments == nullptr ? nullptr : job.segments + (int64_t)(bh * a.tiles + tile) * (DKP * DVT);
+  w.slot = (int64_t)states * a.tiles * (DKP * DVT);
   if (w.cols > DVT) w.cols = DVT;
   return true;
 }
@@ -592,8 +603,8 @@ __device__ __forceinline__ void initial_state(f32x4 (&S)[DKP / 16][NT], const At
 
 // Split sequences.  Slot i of the workspace holds the state that segment i
 // leaves by itself (segment 0: from the initial state), or after the scan the
-// sequence's state after segment i; the last slot holds the initial state,
-// which the launch that needs it may overwrite in its own place.
+// sequence's state after segment i; the last slot holds the initial state, if there is
+// one, which the launch that needs it may overwrite in its own place.
 template <int KT, int NT>
 __device__ __forceinline__ f32x4* slot_at(const Where& w, int slot, int wave, int lane) {
   return reinterpret_cast<f32x4*>(w.states + slot * w.slot) + wave * (KT * NT * 64) + lane;
@@ -605,7 +616,7 @@ template <int DKP, int NT>
 __device__ __forceinline__ void first_state(f32x4 (&S)[DKP / 16][NT], const AttnArgs& a, const AttnJob& job,
                                             const Where& w, size_t head, int wave, int lane) {
   constexpr int KT = DKP / 16;
-  if (w.states == nullptr) {
+  if (w.states == nullptr || (w.seg == 0 && job.s_in == nullptr)) {
     initial_state<DKP, NT>(S, job, w, head, wave, lane);
     return;
   }
@@ -701,7 +712,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs
   };
   start();
   if (w.seg == 0) {
-    put(a.segments - 1);
+    if (job.s_in != nullptr) put(a.segments - 1);
     if (!used) return;
     const float whole = uniform(decay_power(w.log_decay, hi - lo));
 #pragma unroll

@@ -11,6 +11,7 @@ namespace {
 
 using attn::base_of;
 using attn::decay_power;
+using attn::divide;
 using attn::Span;
 using attn::span_of;
 
@@ -65,12 +66,13 @@ __global__ void __launch_bounds__(256) attention_step_kernel(AttnStepArgs a) {
   typedef float vec __attribute__((ext_vector_type(VEC ? 4 : 1)));
   constexpr int W = VEC ? 4 : 1, kCols = 32 / W, kRows = 256 / kCols, U = 4;
   __shared__ float part[kRows][33];
-  const int bh = blockIdx.x / a.tiles, col0 = (int)(blockIdx.x % a.tiles) * 32, b = bh / a.H, h = bh % a.H;
+  const int bh = (int)divide(blockIdx.x, a.tiles, a.by_tiles), col0 = ((int)blockIdx.x - bh * a.tiles) * 32;
+  const int b = (int)divide(bh, a.H, a.by_heads), h = bh - b * a.H;
   const int rg = threadIdx.x / kCols, cl = W * (threadIdx.x % kCols), c = col0 + cl;
   const bool live = c < a.Dv;
-  const raw* q = static_cast<const raw*>(a.q.p) + (int64_t)b * a.q.batch + (int64_t)(h / a.q.group) * a.q.head;
-  const raw* k = static_cast<const raw*>(a.k.p) + (int64_t)b * a.k.batch + (int64_t)(h / a.k.group) * a.k.head;
-  const raw* v = static_cast<const raw*>(a.v.p) + (int64_t)b * a.v.batch + (int64_t)(h / a.v.group) * a.v.head;
+  const raw* q = static_cast<const raw*>(a.q.p) + (int64_t)b * a.q.batch + (int64_t)divide(h, a.q.group, a.q.inverse) * a.q.head;
+  const raw* k = static_cast<const raw*>(a.k.p) + (int64_t)b * a.k.batch + (int64_t)divide(h, a.k.group, a.k.inverse) * a.k.head;
+  const raw* v = static_cast<const raw*>(a.v.p) + (int64_t)b * a.v.batch + (int64_t)divide(h, a.v.group, a.v.inverse) * a.v.head;
   const size_t state = (size_t)bh * a.Dk * a.Dv + c;
   const float d = decay_power(a.log_decay[h], 1);
   float vv[W], acc[W];
@@ -149,6 +151,7 @@ size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
   };
   for (int i = 0; i < a->jobs; ++i) {
     AttnJob& j = a->job[i];
+    for (AttnOperand* x : {&j.q, &j.k, &j.v, &j.o}) x->inverse = inverse_of(x->group);
     dk = std::max(dk, j.Dk);
     dv = std::max(dv, j.Dv);
     for (const AttnOperand* x : {&j.q, &j.k, &j.v})
@@ -157,18 +160,31 @@ size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
     j.o_vec = j.Dv % 8 == 0 && vectors(j.o, j.Dv, a->H / j.o.group, j.o_f32 ? 4 : e);
   }
   a->dkp = dk <= 64 ? 64 : dk <= 128 ? 128 : 256;
-  a->nt = dv > 64 && a->dkp < 256 ? 2 : 1;
+  // Packed sequences count as so many of the longest's length.
+  const int64_t sequences = a->offsets != nullptr && a->T > 0 ? std::max<int64_t>(1, std::min<int64_t>(a->B, a->rows / a->T)) : a->B;
+  const int64_t heads = std::max<int64_t>(1, sequences * a->H * a->jobs);
+  // 32 columns a wave share its reads of q and k, 16 make twice the workgroups:
+  // the narrow form where pieces of 64 tokens of the wide one would not fill the
+  // chip.  Measured (32 / 16 columns): 14 heads of 128, 300 tokens fp32 41 / 32
+  // us, 56 heads, 256 tokens 31 / 29; 128 heads, 1024 tokens 116 / 124.
+  const int64_t wide = heads * ((dv + 127) / 128) * ((a->T + 63) / 64);
+  a->nt = dv > 64 && a->dkp < 256 && wide >= 2 * compute_units ? 2 : 1;
   const int cols = 64 * a->nt;
   a->tiles = (dv + cols - 1) / cols;
-  // Segments: as many as fill the compute units (3 workgroups on each for
-  // states of 64 x 64, else 2), of at least 64 tokens.  Packed sequences count
-  // as so many of the longest's length.
-  const int64_t sequences = a->offsets != nullptr && a->T > 0 ? std::max<int64_t>(1, std::min<int64_t>(a->B, a->rows / a->T)) : a->B;
-  const int64_t groups = std::max<int64_t>(1, a->tiles * sequences * a->H * a->jobs);
-  const int64_t want = compute_units * (a->dkp == 64 && a->nt == 1 ? 3 : 2) / groups;
-  const int64_t segments = std::max<int64_t>(1, std::min<int64_t>(want, a->T / 64));
+  // Segments: as many as give each compute unit 2 workgroups (states of 64 x 64:
+  // 3), of at least 128 tokens, or 64 where those would leave units idle.
+  // Measured at 32 heads, 64 / 128 tokens: 1024 tokens of 128 x 128 fp32 56 / 50
+  // us, bf16 39 / 30, of 64 x 64 bf16 24 / 17.  A split in 2 or 3 costs a short
+  // sequence more than it gains: 56 x 3 jobs of 256 tokens fp32 50 whole, 53 in 2;
+  // 160 heads of 4096 tokens bf16 346 whole, 312 in 2, 243 in 3.
+  const int64_t groups = heads * a->tiles, want = compute_units * (a->dkp == 64 && a->nt == 1 ? 3 : 2) / groups;
+  const int64_t least = groups * (a->T / 128) >= compute_units ? 128 : 64;
+  const int64_t segments = want < 4 && a->T < 512 ? 1 : std::max<int64_t>(1, std::min<int64_t>(want, a->T / least));
   a->seg_tokens = std::max(64, (int)(((a->T + segments - 1) / segments + 63) / 64 * 64));
   a->segments = std::max(1, (a->T + a->seg_tokens - 1) / a->seg_tokens);
+  a->by_tiles = inverse_of(a->tiles);
+  a->by_heads = inverse_of(a->H);
+  a->by_states = inverse_of(a->B * a->H);
   return a->segments > 1 ? (size_t)a->segments * a->tiles * a->B * a->H * a->dkp * cols : 0;
 }
 
@@ -200,6 +216,9 @@ hipError_t launch_attention_reduce(const AttnReduceArgs& args, prnnDataType_t ty
 hipError_t launch_attention_step(const AttnStepArgs& args, prnnDataType_t type, hipStream_t stream) {
   AttnStepArgs a = args;
   a.tiles = (a.Dv + 31) / 32;
+  a.by_tiles = inverse_of(a.tiles);
+  a.by_heads = inverse_of(a.H);
+  for (AttnOperand* x : {&a.q, &a.k, &a.v}) x->inverse = inverse_of(x->group);
   const dim3 grid((unsigned)a.tiles * a.B * a.H);
   const bool vec = a.Dv % 4 == 0 && ((uintptr_t)a.s_in | (uintptr_t)a.s_out) % 16 == 0;
   return for_type(type, [&](auto e) {

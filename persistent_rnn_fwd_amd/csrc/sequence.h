@@ -27,7 +27,11 @@ struct AttnOperand {
   const void* p;
   int64_t token, batch, head;
   int group;
+  uint32_t inverse;  // of group (set by the launch)
 };
+
+// 2^32 / d for the kernels' divisions by d (attn::divide).
+inline uint32_t inverse_of(int d) { return d > 1 ? (uint32_t)((1ull << 32) / (uint32_t)d) : 0xffffffffu; }
 
 // One linear attention of a launch, in its own roles: the forward pass is one
 // job, the backward pass three.
@@ -40,7 +44,7 @@ struct AttnJob {
   AttnOperand q, k, v, o;
   const float* s_in;   // or nullptr (zeros)
   float* s_out;        // or nullptr
-  float* segments;     // split sequences: [segments][B][H][Dk][Dv] states, or nullptr
+  float* segments;     // split sequences: a state of each segment ("slots" in attention_chunk.h), or nullptr
   int Dk, Dv;
   int s_row, s_col;
   float kscale, oscale;
@@ -63,6 +67,7 @@ struct AttnArgs {
   int tiles;      // workgroups along the columns of the widest job's Dv
   int segments;   // workgroups along a sequence
   int seg_tokens; // tokens of a segment
+  uint32_t by_tiles, by_heads, by_states;  // inverses of tiles, H and B H
 };
 
 // Chooses the instance and the split, and returns the floats of workspace
@@ -97,6 +102,7 @@ struct AttnStepArgs {
   float* s_out;
   int B, H, Dk, Dv;
   int tiles;  // tiles of 32 columns (set by the launch)
+  uint32_t by_tiles, by_heads;
   float scale;
 };
 hipError_t launch_attention_step(const AttnStepArgs& a, prnnDataType_t type, hipStream_t stream);
