@@ -142,3 +142,24 @@ def test_norm_rows_do_not_mix(handle):  # noqa: F811
         keep = torch.arange(M, device="cuda") != M // 2
         assert torch.equal(y2[keep], y[keep]) and torch.equal(dx2[keep], dx[keep])
         assert torch.isnan(y2[M // 2]).any() and torch.isnan(dx2[M // 2]).all()
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("Dv", [1, 2, 3, 4, 5, 6, 7, 31, 33, 34, 35, 63, 97, 130, 255])
+def test_step_of_rows_no_vector_divides(handle, type, Dv):  # noqa: F811
+    """The columns that the last vector of a row shares with the one before it,
+    in place (where they may be written before they are read) and out of place,
+    states at addresses that only fp32 divides."""
+    for B, H, Hkv, Dk, offset in ((3, 4, 2, 37, 0), (9, 6, 6, 128, 1)):
+        p, x = attention_problem(Dv + B, type, 1, B, H, Hkv, Dk, Dv)
+        one = {n: (t[0] if n != "log_decay" else t) for n, t in p.items()}
+        room = torch.full((2, x["S0"].numel() + 8), 7.0, device="cuda")
+        states = [r[offset:offset + x["S0"].numel()].view(x["S0"].shape) for r in room]
+        for s in states:
+            s.copy_(x["S0"])
+        o = handle.linear_attention_step(**one, state=states[0], scale=0.3)
+        check_forward(o[None], states[0], p, 0.3, x["S0"])
+        new = torch.empty_like(x["S0"])
+        again = handle.linear_attention_step(**one, state=states[1], scale=0.3, new_state=new)
+        assert torch.equal(o, again) and torch.equal(new, states[0]) and torch.equal(states[1], x["S0"])
+        assert (room[:, :offset] == 7).all() and (room[:, offset + x["S0"].numel():] == 7).all()
