@@ -9,25 +9,46 @@
 //
 // Every exponent is >= 0, so nothing overflows that the recurrence does not.
 //
-// Work split.  One workgroup of 4 or 8 waves owns 16 columns a wave of one
-// head's state and walks its segment of the sequence; each wave keeps its DKP x
-// 16 of the state in registers as fp32 accumulators, for all its chunks.  q, k and v
-// of a chunk are read once into LDS (the next chunk's loads are in flight
-// meanwhile, held in registers), and the scores P, which all waves need, are
-// computed once and exchanged through LDS.  The state never leaves the
+// Work split.  One workgroup of 4 waves owns 16 NT columns a wave (NT 1 or 2)
+// of one head's state and walks its segment of the sequence; each wave keeps its
+// DKP x 16 NT of the state in registers as fp32 accumulators, for all its chunks.
+// q, k and v of a chunk are read once into LDS (the next chunk's loads are in
+// flight meanwhile, held in registers), and the scores P, which all waves need,
+// are computed once and exchanged through LDS.  The state never leaves the
 // registers: an MFMA accumulator (lane l: rows 4 (l / 16) + r, column l % 16)
 // has exactly the layout of an operand once the 32 rows of two accumulator
 // tiles are dealt as row 8 (l / 16) + 4 tile + r, so S^T enters o^T = S^T q^T
 // as its A operand without a shuffle, and the transposed operands k^T and v^T
 // come from LDS with transposing reads (ds_read_b64_tr_b16) whose addresses
-// deal the same rows.
+// deal the same rows.  32 rows at a time enter the output's products and then
+// take the chunk's tokens, so that two independent groups of products are in
+// hand.  NT = 2 halves the reads of q and k a product needs, and is taken where
+// its workgroups fill the chip; a chunk is 64 tokens where registers and LDS
+// allow, which halves the splitting and scaling of the state a token.
+//
+// Split sequences.  Where the heads do not fill the chip, segments of a sequence
+// run side by side: a first kernel leaves each segment's own end state (k and v
+// read once more), from 9 segments on a second one adds them up along the
+// sequence (fewer are added by whoever needs them), and the main kernel starts
+// each segment from its sum.
+//
+// What bounds it.  Large calls in 16 bits: the loads, at the pattern's own rate
+// (the main kernel without its products moves 4.2 TB/s, with them 3.9: rows of
+// 256 bytes, read and written), and the extra read of k and v.  Measured:
+// 32768 bf16 tokens of 32 heads of 128 399 us (main 265, states 117, sum 11),
+// backward of 8 x 2048 tokens of 16 bf16 heads 194 us (221 TFLOP/s of the
+// recurrence's own operations; a chunk takes 6.5 us with one or two workgroups on
+// a unit, of it 2 us of MFMA issue).  fp32: the issue of its six products a
+// product and of the splitting, 5.3 us a chunk of 32 tokens alone on a unit.
+// Small calls: launches and first loads, 3 us a kernel before its first product.
 //
 // Precision.  Operands are split into bf16 parts, high part first, each the
 // truncation of what is left (the last one rounded): bf16 is one part, fp16
 // two, fp32 three, all exact.  Scores and state enter the output's products
 // in 2 parts (2^-16) for 16-bit types and 3 (2^-24) for fp32; the decayed v
-// enters the state, which is fp32 for every type, in 3 parts.  Products of
-// parts below the last kept bit are left out.  bf16 parts have fp32's range,
+// enters the state, which is fp32 for every type, in 3 parts, or in 2 where
+// only 16-bit outputs are read from it.  Products of parts below the last kept
+// bit are left out.  bf16 parts have fp32's range,
 // so large fp16 scores and states do not overflow.  Sums are fp32.
 //
 // Infinities and NaN.  A masked score is 0, and 0 times a later token's
@@ -781,7 +802,10 @@ __global__ void __launch_bounds__(256) attention_scan_kernel(AttnArgs a) {
 }
 
 // Stores the chunk's rows of o, element type or fp32: a lane has 4 NT
-// neighbouring columns of token 16 t + l.
+// neighbouring columns of token 16 t + l.  Nontemporal: no one here reads o, and
+// the caches keep q, k and v instead (backward of 8 x 2048 tokens of 16 bf16
+// heads of 128: 207 us with plain stores, 194).
+constexpr int kStream = 2;
 template <class E, int IT, int NT, bool WIDE>
 __device__ __forceinline__ void put_rows(const Out& x, const Where& w, const f32x4 (&O)[IT][NT], int64_t t0, int n,
                                          bool reverse, int wave, int lane) {
@@ -800,16 +824,16 @@ __device__ __forceinline__ void put_rows(const Out& x, const Where& w, const f32
       if constexpr (WIDE) {
 #pragma unroll
         for (int m = 0; m < NT; ++m)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t][m]), out, to + 16 * m, 0, kPlain);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[t][m]), out, to + 16 * m, 0, kStream);
       } else {
         typedef raw vec __attribute__((ext_vector_type(4 * NT)));
         vec y;
 #pragma unroll
         for (int e = 0; e < 4 * NT; ++e) y[e] = E::put(O[t][e / 4][e % 4]);
         if constexpr (NT == 2)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), out, to, 0, kPlain);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), out, to, 0, kStream);
         else
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), out, to, 0, kPlain);
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), out, to, 0, kStream);
       }
     }
     return;
@@ -821,9 +845,9 @@ __device__ __forceinline__ void put_rows(const Out& x, const Where& w, const f32
       const uint32_t to = row + 16 * t < n && c0 + e < w.cols ? (uint32_t)(first + t * step + e * kSize) : kOutside;
       const float f = O[t][e / 4][e % 4];
       if constexpr (WIDE)
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), out, to, 0, kPlain);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), out, to, 0, kStream);
       else
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, E::put(f)), out, to, 0, kPlain);
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, E::put(f)), out, to, 0, kStream);
     }
 }
 

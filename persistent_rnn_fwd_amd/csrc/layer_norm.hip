@@ -19,6 +19,9 @@
 // bf16 backward takes 33 us against 100 with that vector read by elements, whose
 // waits end the loads ahead.
 //
+// y and dx are stored plainly, for the next layer to find in the caches: a chain
+// of norms of 4096 x 5760 bf16 takes 15.5 us each, with nontemporal stores 18.8.
+//
 // Measured: forward 16384 x 5760 bf16 71-75 us (5.2 TB/s; with the parameters
 // read again for every row 90), backward 115 us (4.9 TB/s, a few percent of it
 // the partial sums), 4099 x 1153 fp32 backward 18 us.
