@@ -17,7 +17,8 @@ using attn::span_of;
 
 // The heads' gradients of k and of v, summed over each group in head order.
 // grid: `blocks` workgroups for each sequence, 2; a thread 4 columns of one row
-// and group at a time (VEC: D % 4 == 0), else one.
+// and group at a time (VEC: D % 4 == 0), else one.  Bound by memory and, at this
+// size, by its launch: 1024 rows of 18 fp32 heads of 64 on 9, twice, 14 MB, 5 us.
 template <class E, bool VEC>
 __global__ void __launch_bounds__(256) attention_reduce_kernel(AttnReduceArgs a) {
   typedef typename E::raw raw;
@@ -64,8 +65,9 @@ __global__ void __launch_bounds__(256) attention_reduce_kernel(AttnReduceArgs a)
 // has too, it stores none (they may be written already where the state is
 // updated in place).
 //
-// Measured: 64 sequences of 32 heads of 128 x 128, 273 MB, 43 us (6.3 TB/s; 46
-// with plain stores, which leave the new state in caches that it does not fit).
+// Measured: 64 sequences of 32 heads of 128 x 128, 270 MB, 43 us over and over on
+// the same states (46 with plain stores, which leave the new state in caches
+// that it does not fit), 53 us with cold ones (5.0 TB/s).
 template <class E, int W, bool ODD>
 __global__ void __launch_bounds__(256) attention_step_kernel(AttnStepArgs a) {
   typedef typename E::raw raw;
@@ -205,7 +207,7 @@ size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
   a->segments = std::max(1, (a->T + a->seg_tokens - 1) / a->seg_tokens);
   a->by_tiles = inverse_of(a->tiles);
   a->by_heads = inverse_of(a->H);
-  a->by_states = inverse_of(a->B * a->H);
+  a->by_states = inverse_of((int)std::min<int64_t>((int64_t)a->B * a->H, 0x7fffffff));  // (more do not fit a grid)
   return a->segments > 1 ? (size_t)a->segments * a->tiles * a->B * a->H * a->dkp * cols : 0;
 }
 
