@@ -551,9 +551,8 @@ prnnStatus_t prnn_debug_jitter(prnnHandle_t handle, uint32_t seed, int span);
  * Head h of q, o, the decay and the state uses head h / (H / Hkv) of k and v.
  * The decays are constants of the layer (exp(log_decay) <= 1 in use; any fp32
  * value is taken as it is, -infinity forgets everything before the token);
- * they have no gradient.  States are fp32 and dense, [B][H][Dk][Dv]; sums are
- * fp32, and the products of 16-bit operands see every operand whole and the
- * decayed scores and the state to 2^-16 or better.  A row of o depends on no
+ * they have no gradient.  States are fp32 and dense, [B][H][Dk][Dv]; sums,
+ * decayed scores and states are fp32 for every type.  A row of o depends on no
  * later token, whatever that holds (infinities and NaN included). */
 typedef struct {
   int B;                    /* sequences                                        */

@@ -44,12 +44,17 @@
 //
 // Precision.  Operands are split into bf16 parts, high part first, each the
 // truncation of what is left (the last one rounded): bf16 is one part, fp16
-// two, fp32 three, all exact.  Scores and state enter the output's products
-// in 2 parts (2^-16) for 16-bit types and 3 (2^-24) for fp32; the decayed v
-// enters the state, which is fp32 for every type, in 3 parts, or in 2 where
-// only 16-bit outputs are read from it.  Products of parts below the last kept
-// bit are left out.  bf16 parts have fp32's range,
-// so large fp16 scores and states do not overflow.  Sums are fp32.
+// two, fp32 three, all exact.  What is fp32 between the products (the decayed
+// scores, the state, the decayed v that enters it) is three parts for every
+// type, so it keeps fp32's 24 bits.  Products of parts whose orders add up to 3
+// or more are left out: at most 2^-21 of the product, 2^-25 on average, where
+// both operands have them (a bf16 operand has one part, so none are missing, and
+// fp16 scores have all four).  Two parts between the products of 16-bit types
+// would take 204 us instead of 251 for the backward of 8 x 2048 tokens of 16 bf16
+// heads of 128, and 409 instead of 441 for 32768 tokens of 32, but where terms
+// cancel the result is off by up to 2^-17 of them, and 2^-14 for fp16 scores.
+// bf16 parts have fp32's range, so large fp16 scores and states do not overflow.
+// Sums are fp32.
 //
 // Infinities and NaN.  A masked score is 0, and 0 times a later token's
 // infinity would be NaN.  A wave whose output accumulators hold a value that
@@ -70,22 +75,22 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// Parts of an input (kIn), and of the scores and the state in the output's
-// products (kOut).
+// Parts of an input, and of an fp32 value.
 template <class E>
 struct Parts;
 template <>
 struct Parts<BF16> {
-  static constexpr int kIn = 1, kOut = 2;
+  static constexpr int kIn = 1;
 };
 template <>
 struct Parts<F16> {
-  static constexpr int kIn = 2, kOut = 2;
+  static constexpr int kIn = 2;
 };
 template <>
 struct Parts<F32> {
-  static constexpr int kIn = 3, kOut = 3;
+  static constexpr int kIn = 3;
 };
+constexpr int kFull = 3;
 
 // Tokens of a chunk.  64 halves what a token pays for splitting and scaling
 // the state; the parts of the other types, and 256 rows, leave LDS and
@@ -184,12 +189,12 @@ __device__ __forceinline__ b16x8 operand(const uint32_t (&w)[4]) {
   return __builtin_bit_cast(b16x8, v);
 }
 
-// acc[m] += x y[m] over the parts' products that matter, i + j <= L, the
+// acc[m] += x y[m] over the parts' products that matter, i + j < 3, the
 // accumulators in turn.
-template <int NX, int NY, int L, int M>
+template <int NX, int NY, int M>
 __device__ __forceinline__ void products(f32x4 (&acc)[M], const b16x8 (&x)[NX], const b16x8 (&y)[M][NY]) {
 #pragma unroll
-  for (int s = L; s >= 0; --s)  // small terms first
+  for (int s = kFull - 1; s >= 0; --s)  // small terms first
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const int j = s - i;
@@ -199,10 +204,10 @@ __device__ __forceinline__ void products(f32x4 (&acc)[M], const b16x8 (&x)[NX], 
     }
 }
 // ... and acc[m] += x[m] y.
-template <int NX, int NY, int L, int M>
+template <int NX, int NY, int M>
 __device__ __forceinline__ void products(f32x4 (&acc)[M], const b16x8 (&x)[M][NX], const b16x8 (&y)[NY]) {
 #pragma unroll
-  for (int s = L; s >= 0; --s)
+  for (int s = kFull - 1; s >= 0; --s)
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const int j = s - i;
@@ -354,7 +359,7 @@ struct Shape {
   static constexpr int kQ = 0, kK = kTile * DKP, kV = 2 * kTile * DKP, kP = kV + kTile * DVT;
   static constexpr int kPRow = C + 8;       // bf16 of a row of scores: rows 16 bytes apart on the banks
   static constexpr int kPPart = 2 * C * kPRow;
-  static constexpr int kW = kP + Parts<E>::kOut * kPPart;  // C weights of the state (state_weight)
+  static constexpr int kW = kP + kFull * kPPart;  // C weights of the state (state_weight)
   static constexpr int kD = kW + 4 * C;  // oscale kscale d^(C - x), x = 0 .. C; zeros to C + 15
   static constexpr int kLds = kD + 4 * (C + 16);
   // without scores: k and v only
@@ -532,8 +537,8 @@ __device__ __forceinline__ void read_values(b16x8 (&V)[NT][Parts<E>::kIn], const
 }
 
 // Rows 32 j .. + 31 of the wave's columns of weights[j] v_j, as operands.
-template <class E, int NT, int ST, int W, int C>
-__device__ __forceinline__ void decayed_values(b16x8 (&D)[NT][ST], const char* v, const float* weights, int wave,
+template <class E, int NT, int W, int C>
+__device__ __forceinline__ void decayed_values(b16x8 (&D)[NT][kFull], const char* v, const float* weights, int wave,
                                                int lane, int j) {
   constexpr int IN = Parts<E>::kIn;
   b16x8 V[NT][IN];
@@ -555,10 +560,10 @@ __device__ __forceinline__ void decayed_values(b16x8 (&D)[NT][ST], const char* v
       for (int p = IN - 2; p >= 0; --p) x[e] += (float)V[m][p][e];
       x[e] *= w[e];
     }
-    uint32_t parts[ST][4];
-    split<ST, 8>(x, parts);
+    uint32_t parts[kFull][4];
+    split<kFull, 8>(x, parts);
 #pragma unroll
-    for (int p = 0; p < ST; ++p) D[m][p] = operand(parts[p]);
+    for (int p = 0; p < kFull; ++p) D[m][p] = operand(parts[p]);
   }
 }
 
@@ -581,11 +586,11 @@ __device__ __forceinline__ void read_keys(b16x8 (&K)[C / 32][Parts<E>::kIn], con
 }
 
 // S += k^T (D of all the chunk's tokens), for 16 rows of the state.
-template <class E, int NT, int ST, int C>
-__device__ __forceinline__ void update_tile(f32x4 (&S)[NT], const b16x8 (&D)[C / 32][NT][ST],
+template <class E, int NT, int C>
+__device__ __forceinline__ void update_tile(f32x4 (&S)[NT], const b16x8 (&D)[C / 32][NT][kFull],
                                             const b16x8 (&K)[C / 32][Parts<E>::kIn]) {
 #pragma unroll
-  for (int j = 0; j < C / 32; ++j) products<Parts<E>::kIn, ST, ST - 1, NT>(S, K[j], D[j]);
+  for (int j = 0; j < C / 32; ++j) products<Parts<E>::kIn, kFull, NT>(S, K[j], D[j]);
 }
 
 // NaN from the first value on that is not finite, 0 until then.
@@ -752,15 +757,15 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs
     rv.store(vt);
     __syncthreads();
     fetch(i - C);
-    b16x8 D[C / 32][NT][3];
+    b16x8 D[C / 32][NT][kFull];
 #pragma unroll
-    for (int j = 0; j < C / 32; ++j) decayed_values<E, NT, 3, Sh::DVT, C>(D[j], vt, weights, wave, lane, j);
+    for (int j = 0; j < C / 32; ++j) decayed_values<E, NT, Sh::DVT, C>(D[j], vt, weights, wave, lane, j);
     const int base = row_at<DKP>(8 * (lane >> 4) + ((lane & 15) >> 2)) ^ ((lane & 3) << 4);
 #pragma unroll
     for (int t = 0; t < Sh::KT; ++t) {
       b16x8 K[C / 32][Parts<E>::kIn];
       read_keys<E, DKP, C>(K, kt, base, t);
-      update_tile<E, NT, 3, C>(S[t], D, K);
+      update_tile<E, NT, C>(S[t], D, K);
     }
     __syncthreads();
   }
@@ -854,11 +859,11 @@ __device__ __forceinline__ void put_rows(const Out& x, const Where& w, const f32
 }
 
 // The attention: grid tiles x B H x segments, jobs.
-template <class E, int DKP, int NT, int WAVES, bool VEC, int ST>
+template <class E, int DKP, int NT, int WAVES, bool VEC>
 __global__ void __launch_bounds__(64 * WAVES, 2) attention_chunk_kernel(AttnArgs a) {
   typedef Shape<E, DKP, NT, WAVES> Sh;
   typedef typename E::raw raw;
-  constexpr int C = Sh::C, IT = C / 16, IN = Parts<E>::kIn, OUT = Parts<E>::kOut;
+  constexpr int C = Sh::C, IT = C / 16, IN = Parts<E>::kIn;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char *const qt = lds + Sh::kQ, *const kt = lds + Sh::kK, *const vt = lds + Sh::kV, *const pt = lds + Sh::kP;
   float *const weights = reinterpret_cast<float*>(lds + Sh::kW), *const decays = reinterpret_cast<float*>(lds + Sh::kD);
@@ -912,7 +917,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_chunk_kernel(AttnArgs
     decays[x] = x <= C ? job.oscale * job.kscale * decay_power(w.log_decay, C - x) : 0.f;
   }
   // Score tiles above the diagonal that the products read: zero throughout.
-  for (int x = threadIdx.x; x < OUT * Sh::kPPart / 4; x += 64 * WAVES) reinterpret_cast<uint32_t*>(pt)[x] = 0u;
+  for (int x = threadIdx.x; x < kFull * Sh::kPPart / 4; x += 64 * WAVES) reinterpret_cast<uint32_t*>(pt)[x] = 0u;
   const float d16 = uniform(decay_power(w.log_decay, 16)), decay = uniform(decay_power(w.log_decay, C));
   const float from_state = job.oscale * decay_power(w.log_decay, l + p);  // of i = l
 
@@ -962,7 +967,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_chunk_kernel(AttnArgs
         for (int x = 0; x < kTiles; ++x)
           if (tj0 + x <= ti) {
             f32x4 y[1] = {acc[x]};
-            products<IN, IN, IN - 1, 1>(y, K[x], Q);
+            products<IN, IN, 1>(y, K[x], Q);
             acc[x] = y[0];
           }
       }
@@ -974,10 +979,10 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_chunk_kernel(AttnArgs
         float f[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) f[r] = acc[x][r] * d[r];
-        uint32_t words[OUT][2];
-        split<OUT, 4>(f, words);
+        uint32_t words[kFull][2];
+        split<kFull, 4>(f, words);
 #pragma unroll
-        for (int c = 0; c < OUT; ++c)
+        for (int c = 0; c < kFull; ++c)
           *reinterpret_cast<u32x2*>(pt + c * Sh::kPPart + 2 * ((16 * ti + l) * Sh::kPRow + 16 * tj + 4 * g)) =
               u32x2{words[c][0], words[c][1]};
       }
@@ -985,11 +990,11 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_chunk_kernel(AttnArgs
 
     // o^T = S^T q^T, 32 rows of the state at a time, which then take the
     // chunk's tokens.  The reads of a step's operands are issued one product
-    // ahead, and held there: the compiler would move them to their use.
+    // ahead.
     const float dn = n == C ? decay : uniform(decay_power(w.log_decay, n));
-    b16x8 D[C / 32][NT][ST];
+    b16x8 D[C / 32][NT][kFull];
 #pragma unroll
-    for (int j = 0; j < C / 32; ++j) decayed_values<E, NT, ST, Sh::DVT, C>(D[j], vt, weights, wave, lane, j);
+    for (int j = 0; j < C / 32; ++j) decayed_values<E, NT, Sh::DVT, C>(D[j], vt, weights, wave, lane, j);
     const int columns = row_at<DKP>(8 * g + (l >> 2)) ^ ((l & 3) << 4);
     f32x4 O[IT][NT];
 #pragma unroll
@@ -1010,25 +1015,24 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_chunk_kernel(AttnArgs
 #pragma unroll
       for (int y = 0; y < 2; ++y) read_keys<E, DKP, C>(K[y], kt, columns, 2 * s + y);
       if (s + 1 < DKP / 32) read_queries(s + 1);
-      if (C == 64 && ST == 2 && VEC) __builtin_amdgcn_sched_barrier(0);
-      b16x8 A[NT][OUT];
+      b16x8 A[NT][kFull];
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = S[2 * s + e / 4][m][e % 4];
-        uint32_t words[OUT][4];
-        split<OUT, 8>(x, words);
+        uint32_t words[kFull][4];
+        split<kFull, 8>(x, words);
 #pragma unroll
-        for (int c = 0; c < OUT; ++c) A[m][c] = operand(words[c]);
+        for (int c = 0; c < kFull; ++c) A[m][c] = operand(words[c]);
       }
 #pragma unroll
-      for (int t = 0; t < IT; ++t) products<OUT, IN, OUT - 1, NT>(O[t], A, Q[s % 2][t]);
+      for (int t = 0; t < IT; ++t) products<kFull, IN, NT>(O[t], A, Q[s % 2][t]);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
 #pragma unroll
         for (int m = 0; m < NT; ++m) S[2 * s + y][m] *= dn;
-        update_tile<E, NT, ST, C>(S[2 * s + y], D, K[y]);
+        update_tile<E, NT, C>(S[2 * s + y], D, K[y]);
       }
     }
     // times d^(i + p)
@@ -1043,15 +1047,15 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_chunk_kernel(AttnArgs
     // o^T += v^T P^T
 #pragma unroll
     for (int j = 0; j < C / 32; ++j) {
-      b16x8 V[NT][IN], P[IT][OUT];
+      b16x8 V[NT][IN], P[IT][kFull];
       read_values<E, NT, Sh::DVT, C>(V, vt, wave, lane, j);
 #pragma unroll
       for (int t = 2 * j; t < IT; ++t)
 #pragma unroll
-        for (int c = 0; c < OUT; ++c)
+        for (int c = 0; c < kFull; ++c)
           P[t][c] = read_row(pt, c * Sh::kPPart + 2 * ((16 * t + l) * Sh::kPRow + 32 * j + 8 * g));
 #pragma unroll
-      for (int t = 2 * j; t < IT; ++t) products<IN, OUT, OUT - 1, NT>(O[t], V, P[t]);
+      for (int t = 2 * j; t < IT; ++t) products<IN, kFull, NT>(O[t], V, P[t]);
     }
     if (!kEarly) fetch_v(i0 + C);
     float z = 0.f;
@@ -1110,12 +1114,7 @@ hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
     }
   }
   const dim3 grid(states * a.segments, a.jobs);
-  bool whole = Parts<E>::kOut == 3;  // the state in fp32's precision: where it is fp32's output, or a state is handed on
-  for (int i = 0; i < a.jobs; ++i) whole = whole || a.job[i].s_out != nullptr;
-  if constexpr (Parts<E>::kOut < 3)
-    if (!whole)
-      return launch_wide(attention_chunk_kernel<E, DKP, NT, WAVES, VEC, 2>, grid, 64 * WAVES, Sh::kLds, a, stream);
-  return launch_wide(attention_chunk_kernel<E, DKP, NT, WAVES, VEC, 3>, grid, 64 * WAVES, Sh::kLds, a, stream);
+  return launch_wide(attention_chunk_kernel<E, DKP, NT, WAVES, VEC>, grid, 64 * WAVES, Sh::kLds, a, stream);
 }
 
 template <class E, bool VEC>
