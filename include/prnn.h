@@ -556,7 +556,7 @@ prnnStatus_t prnn_debug_jitter(prnnHandle_t handle, uint32_t seed, int span);
  * later token, whatever that holds (infinities and NaN included). */
 typedef struct {
   int B;                    /* sequences                                        */
-  int T;                    /* tokens of the longest sequence                   */
+  int T;                    /* tokens of the longest sequence (packed: or any number above, `rows` counts then) */
   int H, Hkv;               /* heads; key-value heads, H a multiple of Hkv      */
   int Dk, Dv;               /* head sizes, 1 .. PRNN_ATTENTION_MAX_D            */
   prnnDataType_t type;      /* of q, k, v, o and their gradients                */
@@ -601,7 +601,8 @@ typedef struct {
  * negative strides, both lengths and offsets, rows < 0; an output that
  * overlaps itself, an input or another output (slices of one buffer whose
  * rows interleave are fine).  NOT_SUPPORTED: a token stride above 2^23
- * elements; more workgroups than a grid holds.
+ * elements; a sequence above 2^31 - 2^17 tokens, or 2^31 - 1 rows; more
+ * workgroups than a grid holds.
  * B == 0 does nothing; T == 0 only passes the states on. */
 prnnStatus_t prnn_linear_attention(prnnHandle_t handle, const prnnAttention_t* attention, const prnnSequence_t* q,
                                    const prnnSequence_t* k, const prnnSequence_t* v, const float* S0,

@@ -544,13 +544,13 @@ class Handle:
             if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
                 raise ValueError("offsets must be [B + 1]")
             B, total, axes = offsets.shape[0] - 1, rows[0], (0, None)
-            T = total if max_len is None else int(max_len)
+            T = total if max_len is None else max(-1, min(int(max_len), total))  # (longer than the rows: as long)
             at_offsets = self._dense(offsets, "offsets", torch.int32, (B + 1,))
         else:
             (T, B), axes = rows, (0, 1)
             if lengths is not None:
                 at_lengths = self._dense(lengths, "lengths", torch.int32, (B,))
-        _ATTENTION.pack_into(self._desc, 0, B, T, H, Hkv, Dk, Dv, code, Dk ** -0.5 if scale is None else scale,
+        _ATTENTION.pack_into(self._desc, 0, B, min(T, 0x7fffffff), H, Hkv, Dk, Dv, code, Dk ** -0.5 if scale is None else scale,
                              self._dense(log_decay, "log_decay", torch.float32, (H,)), at_lengths or 0,
                              at_offsets or 0, total)
         at = _ATTENTION.size

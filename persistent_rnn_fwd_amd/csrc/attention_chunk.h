@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(256) attention_scan_kernel(AttnArgs a) {
   const AttnJob& job = a.job[blockIdx.y];
   const int id = blockIdx.x / kBlocks, bh = id / a.tiles, h = bh % a.H;
   if (id % a.tiles * DVT >= job.Dv) return;
-  const int reached = (span_of(a, bh / a.H).len + a.seg_tokens - 1) / a.seg_tokens - 1;  // slots that are read
+  const int reached = (span_of(a, bh / a.H).len - 1) / a.seg_tokens;  // slots that are read
   const float whole = decay_power(a.log_decay[h], a.seg_tokens);
   f32x4* p = reinterpret_cast<f32x4*>(job.segments) + (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t step = (int64_t)a.B * a.H * a.tiles * (DKP * DVT / 4);

@@ -1,5 +1,5 @@
-// Linear attention with a decay for each head: the plan of a launch, the sum
-// over shared heads, and one token (the chunks are in attention_chunk.h).
+// Linear attention with a decay for each head: the sum over shared heads, and one
+// token (the chunks are in attention_chunk.h, the plan in attention_plan.cpp).
 //
 //   S[t] = d S[t-1] + k[t] v[t]^T,  o[t] = scale S[t]^T q[t],  d = exp(log_decay)
 #include <algorithm>
@@ -160,56 +160,6 @@ hipError_t for_type(prnnDataType_t type, F f) {
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
 }  // namespace
-
-size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
-  int dk = 0, dv = 0;
-  a->vec = 1;
-  const int e = type == PRNN_DATA_FLOAT ? 4 : 2;
-  // whole 16-byte vectors: the rows' lengths, and every stride that is used
-  auto vectors = [&](const AttnOperand& x, int D, int heads, int size) {
-    const int per = 16 / size;
-    return D % per == 0 && (uintptr_t)x.p % 16 == 0 && (a->T <= 1 || x.token % per == 0) &&
-           (a->offsets != nullptr ? x.token % per == 0 : a->B <= 1 || x.batch % per == 0) &&
-           (heads <= 1 || x.head % per == 0);
-  };
-  for (int i = 0; i < a->jobs; ++i) {
-    AttnJob& j = a->job[i];
-    for (AttnOperand* x : {&j.q, &j.k, &j.v, &j.o}) x->inverse = inverse_of(x->group);
-    dk = std::max(dk, j.Dk);
-    dv = std::max(dv, j.Dv);
-    for (const AttnOperand* x : {&j.q, &j.k, &j.v})
-      if (!vectors(*x, x == &j.v ? j.Dv : j.Dk, a->H / x->group, e)) a->vec = 0;
-    // (8 columns at a time also where o is fp32)
-    j.o_vec = j.Dv % 8 == 0 && vectors(j.o, j.Dv, a->H / j.o.group, j.o_f32 ? 4 : e);
-  }
-  a->dkp = dk <= 64 ? 64 : dk <= 128 ? 128 : 256;
-  // Packed sequences count as so many of the longest's length.
-  const int64_t sequences = a->offsets != nullptr && a->T > 0 ? std::max<int64_t>(1, std::min<int64_t>(a->B, a->rows / a->T)) : a->B;
-  const int64_t heads = std::max<int64_t>(1, sequences * a->H * a->jobs);
-  // 32 columns a wave share its reads of q and k, 16 make twice the workgroups:
-  // the narrow form where pieces of 64 tokens of the wide one would not fill the
-  // chip.  Measured (32 / 16 columns): 14 heads of 128, 300 tokens fp32 41 / 32
-  // us, 56 heads, 256 tokens 31 / 29; 128 heads, 1024 tokens 116 / 124.
-  const int64_t wide = heads * ((dv + 127) / 128) * ((a->T + 63) / 64);
-  a->nt = dv > 64 && a->dkp < 256 && wide >= 2 * compute_units ? 2 : 1;
-  const int cols = 64 * a->nt;
-  a->tiles = (dv + cols - 1) / cols;
-  // Segments: as many as give each compute unit 2 workgroups (states of 64 x 64:
-  // 3), of at least 128 tokens, or 64 where those would leave units idle.
-  // Measured at 32 heads, 64 / 128 tokens: 1024 tokens of 128 x 128 fp32 56 / 50
-  // us, bf16 39 / 30, of 64 x 64 bf16 24 / 17.  A split in 2 or 3 costs a short
-  // sequence more than it gains: 56 x 3 jobs of 256 tokens fp32 50 whole, 53 in 2;
-  // 160 heads of 4096 tokens bf16 346 whole, 312 in 2, 243 in 3.
-  const int64_t groups = heads * a->tiles, want = compute_units * (a->dkp == 64 && a->nt == 1 ? 3 : 2) / groups;
-  const int64_t least = groups * (a->T / 128) >= compute_units ? 128 : 64;
-  const int64_t segments = want < 4 && a->T < 512 ? 1 : std::max<int64_t>(1, std::min<int64_t>(want, a->T / least));
-  a->seg_tokens = std::max(64, (int)(((a->T + segments - 1) / segments + 63) / 64 * 64));
-  a->segments = std::max(1, (a->T + a->seg_tokens - 1) / a->seg_tokens);
-  a->by_tiles = inverse_of(a->tiles);
-  a->by_heads = inverse_of(a->H);
-  a->by_states = inverse_of((int)std::min<int64_t>((int64_t)a->B * a->H, 0x7fffffff));  // (more do not fit a grid)
-  return a->segments > 1 ? (size_t)a->segments * a->tiles * a->B * a->H * a->dkp * cols : 0;
-}
 
 hipError_t launch_attention(const AttnArgs& a, prnnDataType_t type, hipStream_t stream) {
   switch (type) {

@@ -97,6 +97,9 @@ Region rows_of(const void* p, int64_t M, int N, int64_t ld, size_t e) {
 // Strides beyond this cannot address memory; products of sizes stay in 64 bits.
 constexpr int64_t kMaxStride = 1ll << 40;
 constexpr int64_t kMaxTokenStride = 1ll << 23;
+// Tokens of a sequence: the segments that cover them, and a chunk more, stay in
+// 31 bits (of at most 768 segments each is rounded up to 64 tokens).
+constexpr int64_t kMaxTokens = 0x7fffffffll - (1 << 17) + 1;
 
 struct Problem {
   prnnAttention_t d;
@@ -139,6 +142,8 @@ prnnStatus_t check_attention(prnnContext* h, const prnnAttention_t* d, bool step
     p->tokens = d->offsets != nullptr ? d->rows : d->T;
     if (d->T == 0) p->tokens = 0;
     if (p->tokens > 0x7fffffffll) return PRNN_STATUS_NOT_SUPPORTED;
+    p->d.T = (int)std::min<int64_t>(d->T, p->tokens);  // (packed: no sequence is longer than the rows)
+    if (p->d.T > kMaxTokens) return PRNN_STATUS_NOT_SUPPORTED;
   }
   if (d->B == 0) return PRNN_STATUS_SUCCESS;
   if (d->log_decay == nullptr || !aligned(d->log_decay, 4)) return PRNN_STATUS_BAD_PARAM;

@@ -1,0 +1,146 @@
+// Calls linear attention with stand-ins for the handle and the launches, and
+// checks what would have been launched (see test_attention_jobs.py).  Device
+// pointers are numbers: nothing here reads them.
+#include <algorithm>
+#include <cstdio>
+#include <cstring>
+
+#include "sequence.h"
+
+struct prnnContext {};
+
+static const uintptr_t kWork = 0x700000000000ull;
+static size_t workspace = 0;  // bytes asked for by the last call
+static prnn::AttnArgs args;   // of the last launch
+static prnn::AttnReduceArgs reduced;
+static int launches = 0, reductions = 0;
+
+namespace prnn {
+bool handle_failed(prnnContext*) { return false; }
+int handle_compute_units(const prnnContext*) { return 256; }
+bool handle_logs(const prnnContext*) { return false; }
+prnnStatus_t handle_workspace(prnnContext*, size_t bytes, hipStream_t, void** out) {
+  workspace = bytes;
+  *out = reinterpret_cast<void*>(kWork);
+  return PRNN_STATUS_SUCCESS;
+}
+hipError_t launch_attention(const AttnArgs& a, prnnDataType_t, hipStream_t) {
+  args = a;
+  ++launches;
+  return hipSuccess;
+}
+hipError_t launch_attention_reduce(const AttnReduceArgs& a, prnnDataType_t, hipStream_t) {
+  reduced = a;
+  ++reductions;
+  return hipSuccess;
+}
+hipError_t launch_attention_step(const AttnStepArgs&, prnnDataType_t, hipStream_t) { return hipSuccess; }
+hipError_t launch_layer_norm(const NormArgs&, prnnDataType_t, prnnDataType_t, hipStream_t) { return hipSuccess; }
+int layer_norm_backward_grid(const NormArgs&, prnnDataType_t, int) { return 0; }
+hipError_t launch_layer_norm_backward(const NormArgs&, prnnDataType_t, prnnDataType_t, int, hipStream_t) { return hipSuccess; }
+}  // namespace prnn
+extern "C" hipError_t hipGetLastError() { return hipSuccess; }
+
+static int failures = 0;
+#define CHECK(ok, ...)                          \
+  do {                                          \
+    if (!(ok)) {                                \
+      std::printf("%s: ", #ok);                 \
+      std::printf(__VA_ARGS__);                 \
+      std::printf("\n");                        \
+      ++failures;                               \
+    }                                           \
+  } while (0)
+
+// Operands of a problem, dense and far apart, time first or batch first.
+struct Problem {
+  prnnAttention_t d = {};
+  prnnSequence_t q, k, v, o, dq, dk, dv;
+  prnnContext h;
+  float *S0 = nullptr, *S1 = nullptr, *dS1 = nullptr, *dS0 = nullptr;
+  static float* state(int i) { return reinterpret_cast<float*>(0x100000000000ull + 0x10000000000ull * i); }
+  Problem(int B, int T, int H, int Hkv, int Dk, int Dv, prnnDataType_t type, bool batch_first = false) {
+    d.B = B;
+    d.T = T;
+    d.H = H;
+    d.Hkv = Hkv;
+    d.Dk = Dk;
+    d.Dv = Dv;
+    d.type = type;
+    d.scale = 1.f;
+    d.log_decay = reinterpret_cast<float*>(0x1000);
+    prnnSequence_t* all[] = {&q, &k, &v, &o, &dq, &dk, &dv};
+    const int heads[] = {H, Hkv, Hkv, H, H, Hkv, Hkv}, size[] = {Dk, Dk, Dv, Dv, Dk, Dk, Dv};
+    for (int i = 0; i < 7; ++i) {
+      const int64_t row = (int64_t)heads[i] * size[i];
+      all[i]->data = reinterpret_cast<void*>(0x200000000000ull + 0x40000000000ull * i);
+      all[i]->head = size[i];
+      all[i]->token = batch_first ? row : row * B;
+      all[i]->batch = batch_first ? row * T : row;
+    }
+  }
+  void packed(int64_t rows, int max_len) {
+    d.offsets = reinterpret_cast<int32_t*>(0x2000);
+    d.rows = rows;
+    d.T = max_len;
+    prnnSequence_t* all[] = {&q, &k, &v, &o, &dq, &dk, &dv};
+    for (prnnSequence_t* s : all) s->token = s->head * (s == &k || s == &v || s == &dk || s == &dv ? d.Hkv : d.H);
+  }
+  prnnStatus_t forward() { return prnn_linear_attention(&h, &d, &q, &k, &v, S0, &o, S1, nullptr); }
+  prnnStatus_t backward() {
+    return prnn_linear_attention_backward(&h, &d, &q, &k, &v, S0, &o, dS1, &dq, &dk, &dv, dS0, nullptr);
+  }
+};
+
+// The segments of a launch cover its sequences, in the integers the kernels use.
+static void check_segments(const char* what) {
+  const prnn::AttnArgs& a = args;
+  CHECK(a.segments >= 1 && a.seg_tokens >= 64 && a.seg_tokens % 64 == 0, "%s: %d of %d", what, a.segments, a.seg_tokens);
+  CHECK((int64_t)a.segments * a.seg_tokens >= a.T, "%s: %d of %d tokens for %d", what, a.segments, a.seg_tokens, a.T);
+  CHECK((int64_t)a.segments * a.seg_tokens + 64 <= 0x7fffffffll, "%s: %d of %d tokens", what, a.segments, a.seg_tokens);
+}
+
+static void long_sequences() {
+  const prnnDataType_t type = PRNN_DATA_BFLOAT;
+  // a length beyond the rows there are is the rows
+  for (int H : {1, 2, 16, 64, 256, 1000})
+    for (int64_t rows : {200ll, 5000ll, 100000ll})
+      for (int call = 0; call < 2; ++call) {
+        int segments = 0, seg_tokens = 0;
+        for (int max_len : {(int)rows, 0x7fffffff, 0x7fffffff - 63, 0x7ffe0000}) {
+          Problem p(3, 1, H, H, 128, 128, type);
+          p.packed(rows, max_len);
+          const prnnStatus_t st = call == 0 ? p.forward() : p.backward();
+          CHECK(st == PRNN_STATUS_SUCCESS, "%d heads, max_len %d: %d", H, max_len, (int)st);
+          check_segments("packed");
+          if (max_len == rows) {
+            segments = args.segments;
+            seg_tokens = args.seg_tokens;
+          }
+          CHECK(args.T == rows && args.segments == segments && args.seg_tokens == seg_tokens,
+                "%d heads, %lld rows, max_len %d: T %d, %d segments of %d", H, (long long)rows, max_len, args.T,
+                args.segments, args.seg_tokens);
+        }
+      }
+  // the longest that a launch counts, and what is refused
+  for (int T : {100, 1 << 20, 1 << 30, 0x7ffe0000})
+    for (int H : {1, 3, 256}) {
+      Problem p(1, T, H, H, 1, 1, type);
+      CHECK(p.forward() == PRNN_STATUS_SUCCESS, "%d tokens", T);
+      check_segments("whole");
+    }
+  for (int T : {0x7ffe0001, 0x7fffffff}) {
+    Problem p(1, T, 1, 1, 1, 1, type);
+    launches = 0;
+    CHECK(p.forward() == PRNN_STATUS_NOT_SUPPORTED && launches == 0, "%d tokens", T);
+    CHECK(p.backward() == PRNN_STATUS_NOT_SUPPORTED && launches == 0, "%d tokens", T);
+  }
+}
+
+int main(int argc, char** argv) {
+  const char* const which = argc > 1 ? argv[1] : "";
+  if (!std::strcmp(which, "long sequences")) long_sequences();
+  else ++failures;
+  if (failures == 0) std::printf("all checks passed\n");
+  return failures == 0 ? 0 : 1;
+}
