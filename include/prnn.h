@@ -611,7 +611,8 @@ prnnStatus_t prnn_linear_attention(prnnHandle_t handle, const prnnAttention_t* a
 /* Gradients of prnn_linear_attention: do_ the gradient of o, dS1 that of S1
  * (or NULL), the inputs as they were; writes dq [..][H][Dk], dk [..][Hkv][Dk]
  * and dv [..][Hkv][Dv] (sums over a shared head's group, added in fp32 in a
- * fixed order) and, unless NULL, dS0 (which may be dS1).  Each of the three is
+ * fixed order) and, unless NULL, dS0 (which may be dS1, for a copy of it in
+ * the workspace).  Each of the three is
  * itself a linear attention: dq of (do, v, k), and backwards in time dk of (v,
  * do, q) and dv of (k, q, do).  Errors as prnn_linear_attention. */
 prnnStatus_t prnn_linear_attention_backward(prnnHandle_t handle, const prnnAttention_t* attention,

@@ -57,6 +57,19 @@ __global__ void __launch_bounds__(256) attention_reduce_kernel(AttnReduceArgs a)
   }
 }
 
+// Copies a state, 4 elements a thread at a time.  Bound by memory.
+__global__ void __launch_bounds__(256) attention_keep_kernel(const float* from, float* to, int64_t n) {
+  constexpr int U = 4;
+  for (int64_t i0 = (int64_t)blockIdx.x * (256 * U) + threadIdx.x; i0 < n; i0 += (int64_t)gridDim.x * (256 * U)) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = i0 + u * 256 < n ? from[i0 + u * 256] : 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * 256 < n) to[i0 + u * 256] = x[u];
+  }
+}
+
 // One token: grid column tiles of 32 x B H.  Lane l of the workgroup owns W = 4
 // columns, 4 (l % 8) .. + 3 of the tile, and rows l / 8 + 32 j, or one column, l
 // % 32, and rows l / 32 + 8 j.  The state is read once and written once, which is
@@ -162,6 +175,12 @@ bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 }  // namespace
 
 hipError_t launch_attention(const AttnArgs& a, prnnDataType_t type, hipStream_t stream) {
+  if (a.keep > 0) {
+    const int64_t blocks = (a.keep + 1023) / 1024;
+    attention_keep_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(a.keep_from, a.keep_to, a.keep);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   switch (type) {
     case PRNN_DATA_FLOAT: return launch_attention_f32(a, stream);
     case PRNN_DATA_HALF: return launch_attention_f16(a, stream);

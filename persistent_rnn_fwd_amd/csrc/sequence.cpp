@@ -337,12 +337,21 @@ prnnStatus_t prnn_linear_attention_backward(prnnHandle_t h, const prnnAttention_
   jv.reverse = 1;
   const size_t floats = plan_attention(&a, d->type, handle_compute_units(h));
   if (!grid_fits(a)) return PRNN_STATUS_NOT_SUPPORTED;
-  float* work = nullptr;  // the heads' gradients, then the segments of the three jobs
-  if (wide_k + wide_v + floats > 0) {
+  // dS0 in the place of dS1: dk's job reads dS1, dv's writes dS0, and nothing
+  // orders the workgroups of one launch, so dk's reads a copy.
+  const size_t kept = dS0 != nullptr && dS0 == dS1 ? (size_t)state_bytes(*d) : 0;
+  float* work = nullptr;  // the heads' gradients, the segments of the three jobs, the kept state
+  if (wide_k + wide_v + floats + kept > 0) {
     void* mem = nullptr;
-    st = handle_workspace(h, wide_k + wide_v + 12 * floats, stream, &mem);
+    st = handle_workspace(h, wide_k + wide_v + 12 * floats + kept, stream, &mem);
     if (st != PRNN_STATUS_SUCCESS) return st;
     work = static_cast<float*>(mem);
+    if (kept > 0) {
+      a.keep_from = dS1;
+      a.keep_to = work + (wide_k + wide_v) / 4 + 3 * floats;
+      a.keep = (int64_t)(kept / 4);
+      jk.s_in = a.keep_to;
+    }
     if (group > 1) {
       jk.o.p = work;
       jv.o.p = work + wide_k / 4;

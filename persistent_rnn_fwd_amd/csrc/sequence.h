@@ -61,6 +61,10 @@ struct AttnArgs {
   const int32_t* offsets;
   int64_t rows;
   int jobs, B, T, H;
+  // A state that a job reads and another one writes: copied ahead of the launch.
+  const float* keep_from;
+  float* keep_to;
+  int64_t keep;  // elements, or 0
   // set by plan_attention
   int dkp, nt;    // kernel instance: rows of the state, tiles of 16 columns a wave
   int vec;        // 16-byte loads of q, k and v

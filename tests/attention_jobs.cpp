@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cstdio>
 #include <cstring>
+#include <vector>
 
 #include "sequence.h"
 
@@ -137,9 +138,59 @@ static void long_sequences() {
   }
 }
 
+// Whether [p, p + bytes) lies in the workspace, apart from what else is there.
+struct Piece {
+  uint64_t at, bytes;
+  const char* what;
+};
+static void check_pieces(const std::vector<Piece>& pieces) {
+  for (size_t i = 0; i < pieces.size(); ++i) {
+    CHECK(pieces[i].at >= kWork && pieces[i].at + pieces[i].bytes <= kWork + workspace, "%s", pieces[i].what);
+    for (size_t j = 0; j < i; ++j)
+      CHECK(pieces[i].at >= pieces[j].at + pieces[j].bytes || pieces[j].at >= pieces[i].at + pieces[i].bytes,
+            "%s and %s", pieces[i].what, pieces[j].what);
+  }
+}
+
+// dS0 in the place of dS1: one launch's jobs run in any order, so none may read
+// what another one writes.
+static void gradients_in_place() {
+  for (int T : {0, 1, 200, 9000})
+    for (int B : {1, 4, 64})
+      for (int group : {1, 4})
+        for (bool packed : {false, true})
+          for (bool same : {false, true}) {
+            Problem p(B, T, 8, 8 / group, 64, 96, PRNN_DATA_HALF);
+            if (packed) p.packed(T, T);
+            p.S0 = Problem::state(0);
+            p.dS1 = Problem::state(1);
+            p.dS0 = same ? p.dS1 : Problem::state(2);
+            CHECK(p.backward() == PRNN_STATUS_SUCCESS, "%d tokens", T);
+            for (int i = 0; i < 3; ++i)
+              for (int j = 0; j < 3; ++j)
+                CHECK(i == j || args.job[j].s_out == nullptr || args.job[i].s_in != args.job[j].s_out,
+                      "%d tokens: job %d reads what job %d writes", T, i, j);
+            CHECK(args.job[2].s_in == p.dS1 && args.job[2].s_out == p.dS0 && args.job[0].s_in == p.S0, "%d tokens", T);
+            if (!same) {
+              CHECK(args.keep == 0 && args.job[1].s_in == p.dS1, "%d tokens", T);
+              continue;
+            }
+            const size_t n = (size_t)B * 8 * 64 * 96;
+            CHECK(args.keep_from == p.dS1 && args.keep_to == args.job[1].s_in && args.keep == (int64_t)n, "%d tokens", T);
+            std::vector<Piece> pieces = {{(uint64_t)args.keep_to, 4 * n, "states"}};
+            if (group > 1 && T > 0) {
+              const size_t rows = (size_t)T * (packed ? 1 : B) * 8;
+              pieces.push_back({(uint64_t)args.job[1].o.p, rows * 64 * 4, "dk"});
+              pieces.push_back({(uint64_t)args.job[2].o.p, rows * 96 * 4, "dv"});
+            }
+            check_pieces(pieces);
+          }
+}
+
 int main(int argc, char** argv) {
   const char* const which = argc > 1 ? argv[1] : "";
   if (!std::strcmp(which, "long sequences")) long_sequences();
+  else if (!std::strcmp(which, "gradients in place")) gradients_in_place();
   else ++failures;
   if (failures == 0) std::printf("all checks passed\n");
   return failures == 0 ? 0 : 1;

@@ -6,6 +6,7 @@ Tolerances are those of test_gpu_sequence.py, whose derivation they share.
 import pytest
 import torch
 
+from persistent_rnn_fwd_amd import Handle
 from test_gpu_sequence import TYPES, attention_problem, check_backward, check_forward, handle  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +45,82 @@ def test_a_length_past_the_rows_is_the_rows(handle, max_len):  # noqa: F811
                                               grad_initial_state=dS02)
     assert all(torch.equal(m, n) for m, n in zip((*grads, dS0), (*grads2, dS02)))
     check_backward([g[700:2200, None, :1] for g in grads], dS0[2:3, :1], one, x["do"][700:2200, :, :1], 0.3, x["S0"][2:3, :1])
+
+
+# -- buffers that are one ----------------------------------------------------------------------------------------
+
+def same(got, want):
+    return got.shape == want.shape and bool(((got == want) | (torch.isnan(got) & torch.isnan(want))).all())
+
+
+@pytest.mark.parametrize("value", [None, float("inf"), float("nan")])
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("shape", [(90, 3, 4, 2, 64, 80), (200, 16, 9, 9, 64, 64), (130, 40, 8, 4, 128, 128), (2500, 1, 2, 2, 64, 48)],
+                         ids=str)
+def test_state_gradients_in_place(handle, type, shape, value):  # noqa: F811
+    """dS0 over dS1 gives what dS0 elsewhere does: whole and split sequences, of
+    equal and of very unequal lengths, also where a value that is not finite has a
+    sequence done again."""
+    T, B, H, Hkv, Dk, Dv = shape
+    p, x = attention_problem(2, type, *shape)
+    if value is not None:
+        p["v"][T // 3, 0, 0, 3] = value
+        x["do"][T // 2, B - 1, H - 1, 5] = value
+    short = torch.randint(0, 4, (B,), generator=torch.Generator().manual_seed(3)).int()
+    short[:: 7] = T
+    for lengths in (None, short.cuda()):
+        kw = {"grad_out": x["do"], "scale": 0.3, "initial_state": x["S0"], "lengths": lengths}
+        apart = torch.full_like(x["S0"], 7.0)
+        want = handle.linear_attention_backward(**p, grad_final_state=x["dS1"], grad_initial_state=apart, **kw)
+        state = x["dS1"].clone()
+        got = handle.linear_attention_backward(**p, grad_final_state=state, grad_initial_state=state, **kw)
+        assert all(same(m, n) for m, n in zip((*got, state), (*want, apart)))
+    if value is None:
+        check_backward(got, state, p, x["do"], 0.3, x["S0"], x["dS1"], short.tolist())
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+def test_state_gradients_in_place_of_packed_sequences(handle, type):  # noqa: F811
+    lengths = [0, 1, 1300, 64, 2, 130, 0]
+    p, x, packed, off, offsets = packed_problem(4, type, lengths, 4, 2, 64, 64)
+    kw = {"grad_out": x["do"][:, 0].contiguous(), "scale": 0.3, "offsets": off, "initial_state": x["S0"]}
+    for max_len in (1300, None):
+        apart = torch.full_like(x["S0"], 7.0)
+        want = handle.linear_attention_backward(**packed, grad_final_state=x["dS1"], grad_initial_state=apart,
+                                                max_len=max_len, **kw)
+        state = x["dS1"].clone()
+        got = handle.linear_attention_backward(**packed, grad_final_state=state, grad_initial_state=state,
+                                               max_len=max_len, **kw)
+        assert all(same(m, n) for m, n in zip((*got, state), (*want, apart)))
+        for b, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+            one = {n: (t[lo:hi] if n != "log_decay" else t) for n, t in p.items()}
+            check_backward([g[lo:hi, None] for g in got], state[b:b + 1], one, x["do"][lo:hi], 0.3, x["S0"][b:b + 1],
+                           x["dS1"][b:b + 1])
+
+
+def test_state_gradients_in_place_in_a_graph(gpu):
+    p, x = attention_problem(5, "bf16", 300, 2, 4, 2, 64, 64)
+    state, given = x["dS1"].clone(), x["dS1"].clone()
+    grads = [torch.empty_like(p[n]) for n in ("q", "k", "v")]
+
+    def call(h, s):
+        return h.linear_attention_backward(**p, grad_out=x["do"], grad_final_state=s, grad_initial_state=s,
+                                           grad_q=grads[0], grad_k=grads[1], grad_v=grads[2])
+
+    with Handle() as h:
+        call(h, state.clone())  # the workspace grows here
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(h, state)
+        for seed in range(3):
+            given.copy_(torch.randn(given.shape, generator=torch.Generator().manual_seed(seed)))
+            eager = given.clone()
+            want = [g.clone() for g in call(h, eager)]
+            state.copy_(given)
+            for g in grads:
+                g.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(state, eager) and all(torch.equal(m, n) for m, n in zip(grads, want))
+        del graph
