@@ -27,10 +27,12 @@ __global__ void __launch_bounds__(256) attention_reduce_kernel(AttnReduceArgs a)
   typedef raw out __attribute__((ext_vector_type(W), aligned(sizeof(raw))));
   const auto& x = a.grad[blockIdx.y];
   const uint32_t per_row = (uint32_t)(a.groups * (x.D / W)), per_group = (uint32_t)(x.D / W);
-  const int b = blockIdx.x / a.blocks, H = a.groups * a.per_group;
+  const int b = blockIdx.x / a.blocks;
   const Span s = span_of(a, b);
   raw* const dst = static_cast<raw*>(const_cast<void*>(x.dst.p)) +
                    (a.offsets != nullptr ? s.first * x.dst.token : (int64_t)b * x.dst.batch);
+  const float* const from = static_cast<const float*>(x.src.p) +
+                            (a.offsets != nullptr ? s.first * x.src.token : (int64_t)b * x.src.batch);
   const int rows = a.lengths != nullptr ? a.T : s.len;  // (padding: zeros)
   const uint32_t step = (uint32_t)a.blocks * 256u;
   uint32_t i = (blockIdx.x % a.blocks) * 256u + threadIdx.x;
@@ -43,12 +45,10 @@ __global__ void __launch_bounds__(256) attention_reduce_kernel(AttnReduceArgs a)
     }
     const uint32_t g = at / per_group;
     const int d = (int)(at - g * per_group) * W;
-    // src is dense: [T][B][H][D], or [rows][H][D] packed
-    const int64_t row = a.offsets != nullptr ? s.first + t : (int64_t)t * a.B + b;
     vec sum = vec(0.f);
     if ((int)t < s.len) {
-      const float* src = x.src + (row * H + (int)g * a.per_group) * x.D + d;
-      for (int j = 0; j < a.per_group; ++j, src += x.D) sum += *reinterpret_cast<const vec*>(src);
+      const float* src = from + (int64_t)t * x.src.token + (int64_t)g * a.per_group * x.src.head + d;
+      for (int j = 0; j < a.per_group; ++j, src += x.src.head) sum += *reinterpret_cast<const vec*>(src);
     }
     out y;
 #pragma unroll
@@ -190,7 +190,7 @@ hipError_t launch_attention(const AttnArgs& a, prnnDataType_t type, hipStream_t 
 
 hipError_t launch_attention_reduce(const AttnReduceArgs& args, prnnDataType_t type, hipStream_t stream) {
   AttnReduceArgs a = args;
-  const bool vec = a.grad[0].D % 4 == 0 && a.grad[1].D % 4 == 0 && aligned16(a.grad[0].src) && aligned16(a.grad[1].src);
+  const bool vec = a.grad[0].D % 4 == 0 && a.grad[1].D % 4 == 0 && aligned16(a.grad[0].src.p) && aligned16(a.grad[1].src.p);
   const int64_t blocks = ((int64_t)a.T * a.groups * std::max(a.grad[0].D, a.grad[1].D) / (vec ? 4 : 1) + 255) / 256,
                 most = a.B < 2048 ? 2048 / a.B : 1;
   a.blocks = (int)(blocks < most ? blocks : most);

@@ -283,14 +283,14 @@ prnnStatus_t prnn_linear_attention_backward(prnnHandle_t h, const prnnAttention_
   const int group = d->H / d->Hkv;
   const int64_t rows = d->offsets != nullptr ? p.tokens : p.tokens * d->B;
   // A shared head's gradient: every head's own in fp32 first, then their sum.
+  // Heads outermost, so that a row is D elements whatever their number (the
+  // kernels count a chunk's rows in 32 bits).
+  if (group > 1 && (double)rows * d->H * (d->Dk + d->Dv) > 1e15) return PRNN_STATUS_ALLOC_FAILED;  // no memory holds it
   const size_t wide_k = group > 1 ? ((size_t)rows * d->H * d->Dk * 4 + 255) / 256 * 256 : 0;
   const size_t wide_v = group > 1 ? ((size_t)rows * d->H * d->Dv * 4 + 255) / 256 * 256 : 0;
   auto dense = [&](float* mem, int D) {
-    AttnOperand x = {mem, (int64_t)d->H * D, 0, D, 1};
-    if (d->offsets == nullptr) {
-      x.batch = x.token;
-      x.token *= d->B;
-    }
+    AttnOperand x = {mem, D, 0, p.tokens * D, 1};
+    if (d->offsets == nullptr) x.batch = d->H * x.head;
     return x;
   };
   AttnArgs a = base_args(p, 3);
@@ -369,10 +369,10 @@ prnnStatus_t prnn_linear_attention_backward(prnnHandle_t h, const prnnAttention_
     r.T = a.T;
     r.groups = d->Hkv;
     r.per_group = group;
-    r.grad[0].src = work;
+    r.grad[0].src = jk.o;
     r.grad[0].dst = operand(dk, 1);
     r.grad[0].D = d->Dk;
-    r.grad[1].src = work + wide_k / 4;
+    r.grad[1].src = jv.o;
     r.grad[1].dst = operand(dv, 1);
     r.grad[1].D = d->Dv;
     st = launched(launch_attention_reduce(r, d->type, stream));

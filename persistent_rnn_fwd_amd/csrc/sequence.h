@@ -83,12 +83,12 @@ hipError_t launch_attention_f32(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attention_f16(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attention_bf16(const AttnArgs& a, hipStream_t stream);
 
-// dst[t][b][g] = sum over the heads of group g of src[t][b][H] (fp32, dense
-// rows of D), in head order, for two gradients.  Rows as the attention's outputs.
+// dst(t, b, g) = sum over the heads h of group g of src(t, b, h) (fp32, rows and
+// strides multiples of 16 bytes where D is of 4), in head order, for two
+// gradients.  Rows as the attention's outputs.
 struct AttnReduceArgs {
   struct {
-    const float* src;
-    AttnOperand dst;
+    AttnOperand src, dst;
     int D;
   } grad[2];
   const int32_t* lengths;

@@ -187,10 +187,52 @@ static void gradients_in_place() {
           }
 }
 
+// Shared heads: every head's own gradient lies in the workspace.  The kernels
+// count a chunk's rows in 32 bits, below 2^30 bytes for up to 64 tokens, whatever
+// number of heads and sequences there is.
+static void shared_heads() {
+  const struct {
+    int B, T, H, Hkv, Dk, Dv;
+  } shapes[] = {{2, 5, 4, 2, 8, 16},        {1, 300, 8, 1, 64, 64},     {2048, 64, 64, 32, 128, 96}, {4096, 64, 64, 32, 128, 128},
+                {8192, 64, 32, 8, 128, 128}, {1024, 3, 1024, 1, 256, 1}, {1, 64, 1 << 20, 1 << 19, 256, 256}};
+  for (const auto& s : shapes)
+    for (bool packed : {false, true}) {
+      Problem p(s.B, s.T, s.H, s.Hkv, s.Dk, s.Dv, PRNN_DATA_BFLOAT, true);
+      for (prnnSequence_t* x : {&p.q, &p.k, &p.v, &p.o, &p.dq, &p.dk, &p.dv}) {  // heads outermost: any number of them
+        x->token = x->head;
+        x->batch = x->token * s.T;
+        x->head = x->batch * s.B;
+      }
+      if (packed) {
+        p.d.offsets = reinterpret_cast<int32_t*>(0x2000);
+        p.d.rows = (int64_t)s.T * s.B;
+      }
+      const prnnStatus_t st = p.backward();
+      CHECK(st == PRNN_STATUS_SUCCESS, "%d x %d heads: %d", s.B, s.H, (int)st);
+      if (st != PRNN_STATUS_SUCCESS) continue;
+      const uint64_t all = (uint64_t)s.T * s.B * s.H;
+      check_pieces({{(uint64_t)args.job[1].o.p, all * s.Dk * 4, "dk"}, {(uint64_t)args.job[2].o.p, all * s.Dv * 4, "dv"}});
+      for (int i : {1, 2}) {
+        const prnn::AttnOperand& o = args.job[i].o;
+        const int64_t D = i == 1 ? s.Dk : s.Dv;
+        CHECK(args.job[i].o_f32 && o.group == 1 && o.token >= D, "%d x %d heads", s.B, s.H);
+        CHECK(64 * o.token * 4 < 1ll << 30, "%d x %d heads: rows of %lld elements", s.B, s.H, (long long)o.token);
+        // the last element is the last of the piece, and the axes do not meet
+        const int64_t tokens = packed ? (int64_t)s.T * s.B : s.T, sequences = packed ? 1 : s.B;
+        CHECK((tokens - 1) * o.token + (sequences - 1) * o.batch + (s.H - 1) * o.head + D == (int64_t)all * D,
+              "%d x %d heads", s.B, s.H);
+        // and the sums read what the job writes
+        const prnn::AttnOperand& r = reduced.grad[i - 1].src;
+        CHECK(r.p == o.p && r.token == o.token && (packed || r.batch == o.batch) && r.head == o.head, "%d x %d heads", s.B, s.H);
+      }
+    }
+}
+
 int main(int argc, char** argv) {
   const char* const which = argc > 1 ? argv[1] : "";
   if (!std::strcmp(which, "long sequences")) long_sequences();
   else if (!std::strcmp(which, "gradients in place")) gradients_in_place();
+  else if (!std::strcmp(which, "shared heads")) shared_heads();
   else ++failures;
   if (failures == 0) std::printf("all checks passed\n");
   return failures == 0 ? 0 : 1;

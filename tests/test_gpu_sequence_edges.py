@@ -124,3 +124,26 @@ def test_state_gradients_in_place_in_a_graph(gpu):
             torch.cuda.synchronize()
             assert torch.equal(state, eager) and all(torch.equal(m, n) for m, n in zip(grads, want))
         del graph
+
+
+# -- many heads and sequences ------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("shape", [(40, 2048, 64, 32, 96, 128), (64, 4096, 32, 16, 128, 32)], ids=str)
+def test_gradients_of_shared_heads_at_many_heads_and_sequences(gpu, shape):
+    """Batch first: rows of all heads of all sequences together pass 2^31 bytes a
+    chunk.  Every sequence is the same, so that all of them can be compared."""
+    T, B, H, Hkv, Dk, Dv = shape
+    p, x = attention_problem(6, "bf16", T, 1, H, Hkv, Dk, Dv)
+    every = lambda t: t.transpose(0, 1).expand(B, T, *t.shape[2:]).contiguous().transpose(0, 1)
+    many = {n: (every(t) if n != "log_decay" else t) for n, t in p.items()}
+    with Handle() as h:
+        into = {"grad_" + n: torch.empty_like(many[n]) for n in ("q", "k", "v")}  # (their strides too)
+        grads = h.linear_attention_backward(**many, grad_out=every(x["do"]), scale=0.3, **into)
+        for g in grads:
+            assert (g == g[:, :1]).all()
+        check_backward([g[:, :1, :1] if i else g[:, :1, :2] for i, g in enumerate(grads)], None,
+                       {"q": p["q"][:, :, :2], "k": p["k"][:, :, :1], "v": p["v"][:, :, :1], "log_decay": p["log_decay"][:2]},
+                       x["do"][:, :, :2], 0.3)
+        check_backward([g[:, -1:, -1:] if i else g[:, -1:, -2:] for i, g in enumerate(grads)], None,
+                       {"q": p["q"][:, :, -2:], "k": p["k"][:, :, -1:], "v": p["v"][:, :, -1:], "log_decay": p["log_decay"][-2:]},
+                       x["do"][:, :, -2:], 0.3)
