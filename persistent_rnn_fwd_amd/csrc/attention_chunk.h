@@ -410,8 +410,9 @@ struct Where {
   const char *q, *k, *v;  // token 0 (v: of its columns)
   int64_t o;              // element of token 0, first column
   float log_decay;        // (set after the first loads are under way)
-  float* states;          // slot 0 of the segments' states, in register order, or nullptr
+  float* states;          // slot 0 of a split sequence's states, in register order, or nullptr
   int64_t slot;           // elements from slot to slot
+  int initial;            // the slot of the initial state, or -1
 };
 
 template <class E, int DKP, int NT, int WAVES>
@@ -425,7 +426,7 @@ __device__ __forceinline__ bool where(const AttnArgs& a, const AttnJob& job, int
   asm volatile("" ::"s"(q.p), "s"(q.token), "s"(q.batch), "s"(q.head), "s"(q.group), "s"(q.inverse), "s"(k.p),
                "s"(k.token), "s"(k.batch), "s"(k.head), "s"(k.group), "s"(k.inverse), "s"(v.p), "s"(v.token),
                "s"(v.batch), "s"(v.head), "s"(v.group), "s"(v.inverse), "s"(a.lengths), "s"(a.offsets), "s"(a.rows),
-               "s"(a.B), "s"(a.T), "s"(a.H), "s"(a.tiles), "s"(a.seg_tokens), "s"(a.by_tiles), "s"(job.Dv),
+               "s"(a.B), "s"(a.T), "s"(a.H), "s"(a.tiles), "s"(a.seg_tokens), "s"(a.by_tiles), "s"(a.by_seg), "s"(job.Dv),
                "s"(job.o.p), "s"(job.s_out), "s"(job.reverse));
   const uint32_t id = blockIdx.x, state = divide(id, a.tiles, a.by_tiles), tile = id - state * a.tiles;
   const uint32_t states = (uint32_t)a.B * a.H, seg = divide(state, states, a.by_states), bh = state - seg * states;
@@ -440,8 +441,15 @@ __device__ __forceinline__ bool where(const AttnArgs& a, const AttnJob& job, int
   w.k = static_cast<const char*>(k.p) + base_of(k, a, w.s, w.b, w.h) * (int64_t)sizeof(raw);
   w.v = static_cast<const char*>(v.p) + (base_of(v, a, w.s, w.b, w.h) + w.col0) * (int64_t)sizeof(raw);
   w.o = base_of(job.o, a, w.s, w.b, w.h) + w.col0;
-  w.states = job.segments == nullptr ? nullptr : job.segments + (int64_t)(bh * a.tiles + tile) * (DKP * DVT);
-  w.slot = (int64_t)states * a.tiles * (DKP * DVT);
+  w.states = nullptr;
+  w.slot = 0;
+  w.initial = -1;
+  if (job.segments != nullptr && w.s.len > a.seg_tokens) {
+    const int64_t slot = first_slot(a, job, w.b, divide((uint32_t)w.s.first, a.seg_tokens, a.by_seg));
+    w.states = job.segments + ((slot * a.H + w.h) * a.tiles + tile) * (DKP * DVT);
+    w.slot = (int64_t)a.H * a.tiles * (DKP * DVT);
+    if (job.s_in != nullptr) w.initial = (int)divide((uint32_t)w.s.len - 1, a.seg_tokens, a.by_seg);
+  }
   if (w.cols > DVT) w.cols = DVT;
   return true;
 }
@@ -627,10 +635,12 @@ __device__ __forceinline__ void initial_state(f32x4 (&S)[DKP / 16][NT], const At
   }
 }
 
-// Split sequences.  Slot i of the workspace holds the state that segment i
-// leaves by itself (segment 0: from the initial state), or after the scan the
-// sequence's state after segment i; the last slot holds the initial state, if there is
-// one, which the launch that needs it may overwrite in its own place.
+// Split sequences.  Slot i of a sequence holds the state that segment i leaves by
+// itself (segment 0: from the initial state), or after the scan the sequence's
+// state after segment i; the last slot holds the initial state, if there is one,
+// which the launch that needs it may overwrite in its own place.  (A sequence of
+// one segment has one workgroup for each of its columns, which reads them before
+// it writes them.)
 template <int KT, int NT>
 __device__ __forceinline__ f32x4* slot_at(const Where& w, int slot, int wave, int lane) {
   return reinterpret_cast<f32x4*>(w.states + slot * w.slot) + wave * (KT * NT * 64) + lane;
@@ -642,12 +652,12 @@ template <int DKP, int NT>
 __device__ __forceinline__ void first_state(f32x4 (&S)[DKP / 16][NT], const AttnArgs& a, const AttnJob& job,
                                             const Where& w, size_t head, int wave, int lane) {
   constexpr int KT = DKP / 16;
-  if (w.states == nullptr || (w.seg == 0 && job.s_in == nullptr)) {
+  if (w.states == nullptr || (w.seg == 0 && w.initial < 0)) {
     initial_state<DKP, NT>(S, job, w, head, wave, lane);
     return;
   }
   const bool scanned = a.segments >= kScanFrom;
-  const f32x4* p = slot_at<KT, NT>(w, w.seg == 0 ? a.segments - 1 : scanned ? w.seg - 1 : 0, wave, lane);
+  const f32x4* p = slot_at<KT, NT>(w, w.seg == 0 ? w.initial : scanned ? w.seg - 1 : 0, wave, lane);
 #pragma unroll
   for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -681,7 +691,7 @@ __device__ __forceinline__ void last_state(const f32x4 (&S)[DKP / 16][NT], const
   }
 }
 
-// Slots 0 .. segments - 2: grid tiles x B H x (segments - 1), jobs.  The chunks
+// The slots of every segment but the last: grid tiles x B H x (segments - 1), jobs.  The chunks
 // are taken from a segment's last to its first, each weighted for the tokens
 // behind it: the state itself is not touched between products, and the main
 // kernel, which starts where this one ends, finds the tokens it reads first in
@@ -711,10 +721,9 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs
     rk.load(w.k, t0, n, ks, job.Dk, job.reverse);
     rv.load(w.v, t0, n, vs, w.cols, job.reverse);
   };
-  const bool used = hi < w.s.len;  // a segment follows
-  if (!used && w.seg > 0) return;
+  if (hi >= w.s.len) return;  // no segment follows
   const int end = lo + (hi - lo - 1) / C * C;  // the last chunk's first token
-  if (used) fetch(end);
+  fetch(end);
   w.log_decay = uniform(a.log_decay[w.h]);
   const float decay = uniform(decay_power(w.log_decay, C));
   const float weight = (int)threadIdx.x < C ? state_weight(job, w.log_decay, C, p, threadIdx.x) : 0.f;
@@ -739,8 +748,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs
   };
   start();
   if (w.seg == 0) {
-    if (job.s_in != nullptr) put(a.segments - 1);
-    if (!used) return;
+    if (w.initial >= 0) put(w.initial);
     const float whole = uniform(decay_power(w.log_decay, hi - lo));
 #pragma unroll
     for (int t = 0; t < Sh::KT; ++t)
@@ -787,12 +795,16 @@ template <int DKP, int NT, int WAVES>
 __global__ void __launch_bounds__(256) attention_scan_kernel(AttnArgs a) {
   constexpr int DVT = 16 * NT * WAVES, kBlocks = DKP * DVT / 1024, kAhead = 8;
   const AttnJob& job = a.job[blockIdx.y];
-  const int id = blockIdx.x / kBlocks, bh = id / a.tiles, h = bh % a.H;
-  if (id % a.tiles * DVT >= job.Dv) return;
-  const int reached = (span_of(a, bh / a.H).len - 1) / a.seg_tokens;  // slots that are read
+  const int id = blockIdx.x / kBlocks, bh = id / a.tiles, tile = id - bh * a.tiles, b = bh / a.H, h = bh - b * a.H;
+  if (tile * DVT >= job.Dv) return;
+  const Span s = span_of(a, b);
+  const int reached = (s.len - 1) / a.seg_tokens;  // slots that are read
+  if (reached < 2) return;
   const float whole = decay_power(a.log_decay[h], a.seg_tokens);
-  f32x4* p = reinterpret_cast<f32x4*>(job.segments) + (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t step = (int64_t)a.B * a.H * a.tiles * (DKP * DVT / 4);
+  const int64_t slot = first_slot(a, job, b, (uint32_t)s.first / (uint32_t)a.seg_tokens);
+  f32x4* p = reinterpret_cast<f32x4*>(job.segments) + ((slot * a.H + h) * a.tiles + tile) * (DKP * DVT / 4) +
+             (blockIdx.x % kBlocks) * 256 + threadIdx.x;
+  const int64_t step = (int64_t)a.H * a.tiles * (DKP * DVT / 4);
   f32x4 S = *p;
   for (int i0 = 1; i0 < reached; i0 += kAhead) {
     f32x4 own[kAhead];

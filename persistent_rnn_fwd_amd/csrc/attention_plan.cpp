@@ -50,10 +50,16 @@ size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
   const int64_t segments = want < 4 && a->T < 512 ? 1 : std::max<int64_t>(1, std::min<int64_t>(want, a->T / least));
   a->seg_tokens = std::max(64, (int)(((a->T + segments - 1) / segments + 63) / 64 * 64));
   a->segments = std::max(1, (int)(((int64_t)a->T + a->seg_tokens - 1) / a->seg_tokens));
+  // (every sequence gets the longest one's workgroups, whatever its length)
+  if (a->segments > 1 && (int64_t)a->tiles * a->B * a->H * a->segments > kMaxWorkgroups) {
+    a->segments = 1;
+    a->seg_tokens = (a->T + 63) / 64 * 64;
+  }
   a->by_tiles = inverse_of(a->tiles);
   a->by_heads = inverse_of(a->H);
   a->by_states = inverse_of((int)std::min<int64_t>((int64_t)a->B * a->H, 0x7fffffff));  // (more do not fit a grid)
-  return a->segments > 1 ? (size_t)a->segments * a->tiles * a->B * a->H * a->dkp * cols : 0;
+  a->by_seg = inverse_of(a->seg_tokens);
+  return a->segments > 1 ? (size_t)slots(*a) * a->H * a->tiles * a->dkp * cols : 0;
 }
 
 }  // namespace prnn

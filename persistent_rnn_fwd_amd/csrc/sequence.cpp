@@ -173,9 +173,11 @@ AttnArgs base_args(const Problem& p, int jobs) {
   return a;
 }
 
-// Workgroups of the widest launch: elements of a state take up to 256 of them.
+// Workgroups of the widest launch: the segments', or where they are summed ahead
+// (from 9 on) up to 16 for a state.
 bool grid_fits(const AttnArgs& a) {
-  return (int64_t)a.tiles * a.B * a.H * std::max(a.segments, 256) <= 0x7fffffffll;
+  const int64_t states = (int64_t)a.tiles * a.B * a.H;
+  return states * (a.segments > 1 ? std::max(a.segments, 16) : 1) <= kMaxWorkgroups;
 }
 
 uint64_t state_bytes(const prnnAttention_t& d) { return 4ull * d.B * d.H * d.Dk * d.Dv; }

@@ -44,7 +44,7 @@ struct AttnJob {
   AttnOperand q, k, v, o;
   const float* s_in;   // or nullptr (zeros)
   float* s_out;        // or nullptr
-  float* segments;     // split sequences: a state of each segment ("slots" in attention_chunk.h), or nullptr
+  float* segments;     // split sequences: a state of each segment ("slots" below), or nullptr
   int Dk, Dv;
   int s_row, s_col;
   float kscale, oscale;
@@ -71,8 +71,30 @@ struct AttnArgs {
   int tiles;      // workgroups along the columns of the widest job's Dv
   int segments;   // workgroups along a sequence
   int seg_tokens; // tokens of a segment
-  uint32_t by_tiles, by_heads, by_states;  // inverses of tiles, H and B H
+  uint32_t by_tiles, by_heads, by_states, by_seg;  // inverses of tiles, H, B H and seg_tokens
 };
+
+// Split sequences keep states in slots of the workspace, [slot][H][tiles] of
+// them: a sequence of n > 1 segments the n - 1 that segments leave to the next
+// one, and a job with initial states those in one more.  Packed sequences share
+// as many slots as their rows can fill, however many sequences there are and
+// whatever the longest one is: n - 1 is at most the number of multiples of
+// seg_tokens that the sequence's rows pass, so a sequence whose first row is
+// `whole` seg_tokens and a rest takes its slots from `whole` (n <= 2 (n - 1): twice
+// that, with initial states).  Offsets that decrease make slots coincide, but
+// never leave the workspace.
+__host__ __device__ inline int64_t first_slot(const AttnArgs& a, const AttnJob& job, int b, uint32_t whole) {
+  return a.offsets != nullptr ? (int64_t)whole * (job.s_in != nullptr ? 2 : 1) : (int64_t)b * a.segments;
+}
+// ... and their number, enough for each of the jobs.
+inline int64_t slots(const AttnArgs& a) {
+  bool given = false;
+  for (int i = 0; i < a.jobs; ++i) given = given || a.job[i].s_in != nullptr;
+  return a.offsets != nullptr ? a.rows / a.seg_tokens * (given ? 2 : 1) : (int64_t)a.B * a.segments;
+}
+
+// Workgroups of 256 threads that a launch takes (it counts threads in 32 bits).
+constexpr int64_t kMaxWorkgroups = (1ll << 24) - 1;
 
 // Chooses the instance and the split, and returns the floats of workspace
 // that each job needs for AttnJob::segments (0: none).

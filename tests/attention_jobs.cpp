@@ -228,11 +228,69 @@ static void shared_heads() {
     }
 }
 
+// Packed sequences: the workspace follows the rows there are, not the number of
+// sequences times the longest one's segments.
+static void packed_workspace() {
+  const struct {
+    int B;
+    int64_t rows;
+    int max_len, H, Hkv, D;
+  } shapes[] = {{512, 32768, 32768, 16, 16, 128}, {512, 32768, 16384, 16, 16, 128}, {4096, 4096, 4096, 16, 4, 128},
+                {4096, 4096, 1, 16, 16, 128},     {100000, 100000, 100000, 1, 1, 64}, {7, 3001, 1200, 16, 4, 64},
+                {60, 60000, 60000, 4, 2, 256},    {1 << 22, 1 << 22, 1 << 22, 1, 1, 16}, {3, 130, 130, 2, 2, 200}};
+  for (const auto& s : shapes)
+    for (bool states : {false, true})
+      for (int call = 0; call < 2; ++call) {
+        Problem p(s.B, 1, s.H, s.Hkv, s.D, s.D, PRNN_DATA_BFLOAT);
+        p.packed(s.rows, s.max_len);
+        if (states) {
+          p.S0 = Problem::state(0);
+          p.S1 = p.dS1 = Problem::state(1);
+          p.dS0 = Problem::state(2);
+        }
+        workspace = 0;
+        const prnnStatus_t st = call == 0 ? p.forward() : p.backward();
+        CHECK(st == PRNN_STATUS_SUCCESS, "%d sequences: %d", s.B, (int)st);
+        check_segments("packed");
+        // q, k, v and o, or those with the gradients; fp32 gradients of shared heads
+        const double row = s.D * 2.0, operands = s.rows * row * (call == 0 ? 2 * s.H + 2 * s.Hkv : 3 * s.H + 4 * s.Hkv);
+        const double wide = call == 1 && s.H != s.Hkv ? 4.0 * s.rows * s.H * s.D * 2 + 512 : 0;
+        CHECK(workspace - wide <= 8 * operands + 4096, "%d sequences of %lld rows: workspace of %zu bytes for %.0f", s.B,
+              (long long)s.rows, workspace, operands);
+        CHECK((int64_t)args.tiles * s.B * s.H * args.segments < 1ll << 24, "%d sequences: %d segments", s.B, args.segments);
+        if (args.segments == 1) continue;
+        // slots of sequences of any lengths that add up to the rows: apart, and inside
+        for (int pattern = 0; pattern < 4; ++pattern)
+          for (int i = 0; i < args.jobs; ++i) {
+            const prnn::AttnJob& job = args.job[i];
+            int64_t first = 0, next = 0;
+            uint32_t seed = 1;
+            for (int b = 0; b < s.B; ++b) {
+              seed = seed * 1664525u + 1013904223u;
+              const int64_t left = s.rows - first;
+              int64_t len = pattern == 0 ? (b == s.B / 2 ? left : 0) : pattern == 1 ? args.seg_tokens * (seed >> 30)
+                          : pattern == 2 ? args.seg_tokens + 1 : seed % (2 * s.rows / s.B + 2);
+              len = std::min(len, std::min<int64_t>(left, args.T));
+              const int64_t count = len > 0 ? (len - 1) / args.seg_tokens + 1 : 0;
+              const int64_t used = count < 2 ? 0 : count - (job.s_in == nullptr ? 1 : 0);
+              const int64_t at = prnn::first_slot(args, job, b, (uint32_t)(first / args.seg_tokens));
+              CHECK(used == 0 || (at >= next && at + used <= prnn::slots(args)), "slots %lld + %lld of sequence %d",
+                    (long long)at, (long long)used, b);
+              if (used > 0) next = at + used;
+              first += len;
+            }
+          }
+        CHECK(prnn::slots(args) * s.H * args.tiles * args.dkp * 64 * args.nt * 4 * args.jobs <= (int64_t)workspace,
+              "%d sequences", s.B);
+      }
+}
+
 int main(int argc, char** argv) {
   const char* const which = argc > 1 ? argv[1] : "";
   if (!std::strcmp(which, "long sequences")) long_sequences();
   else if (!std::strcmp(which, "gradients in place")) gradients_in_place();
   else if (!std::strcmp(which, "shared heads")) shared_heads();
+  else if (!std::strcmp(which, "packed workspace")) packed_workspace();
   else ++failures;
   if (failures == 0) std::printf("all checks passed\n");
   return failures == 0 ? 0 : 1;

@@ -147,3 +147,60 @@ def test_gradients_of_shared_heads_at_many_heads_and_sequences(gpu, shape):
         check_backward([g[:, -1:, -1:] if i else g[:, -1:, -2:] for i, g in enumerate(grads)], None,
                        {"q": p["q"][:, :, -2:], "k": p["k"][:, :, -1:], "v": p["v"][:, :, -1:], "log_decay": p["log_decay"][-2:]},
                        x["do"][:, :, -2:], 0.3)
+
+
+# -- packed sequences of very unequal lengths --------------------------------------------------------------------
+
+def check_sequences(p, x, offsets, which, o, S, grads, dS0):
+    for b in which:
+        lo, hi = offsets[b], offsets[b + 1]
+        one = {n: (t[lo:hi] if n != "log_decay" else t) for n, t in p.items()}
+        check_forward(o[lo:hi, None], S[b:b + 1], one, 0.3, x["S0"][b:b + 1])
+        check_backward([g[lo:hi, None] for g in grads], dS0[b:b + 1], one, x["do"][lo:hi], 0.3, x["S0"][b:b + 1],
+                       x["dS1"][b:b + 1])
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("lengths", [[n % 41 for n in range(7, 700, 7)] + [1700] + [n % 5 for n in range(60)],
+                                     [1700] + [0] * 30 + [129, 64, 65, 1], [0, 0, 64, 128, 640, 0, 900, 1, 63]],
+                         ids=["many", "first", "some"])
+def test_long_sequences_among_short_ones(handle, type, lengths):  # noqa: F811
+    p, x, packed, off, offsets = packed_problem(8, type, lengths, 4, 2, 64, 48)
+    by_length = sorted(range(len(lengths)), key=lambda b: lengths[b])
+    which = sorted({*by_length[:2], *by_length[-4:], len(lengths) // 2})
+    do = x["do"][:, 0].contiguous()
+    for max_len in (None, max(lengths)):
+        kw = {"scale": 0.3, "offsets": off, "max_len": max_len}
+        S, dS0 = torch.full_like(x["S0"], float("nan")), torch.full_like(x["S0"], float("nan"))
+        o = handle.linear_attention(**packed, initial_state=x["S0"], final_state=S, **kw)
+        grads = handle.linear_attention_backward(**packed, grad_out=do, initial_state=x["S0"], grad_final_state=x["dS1"],
+                                                 grad_initial_state=dS0, **kw)
+        assert not torch.isnan(S).any() and not torch.isnan(dS0).any()
+        check_sequences(p, x, offsets, which, o, S, grads, dS0)
+        state = x["S0"].clone()
+        again = handle.linear_attention(**packed, initial_state=state, final_state=state, **kw)
+        assert torch.equal(again, o) and torch.equal(state, S)
+        plain = handle.linear_attention(**packed, **kw)
+        lo = offsets[which[-1]]
+        one = {n: (t[lo:offsets[which[-1] + 1]] if n != "log_decay" else t) for n, t in p.items()}
+        check_forward(plain[lo:offsets[which[-1] + 1], None], None, one, 0.3)
+
+
+def test_many_sequences_without_a_longest_take_little_memory(gpu):
+    """4096 sequences of one token each, of which any could be 4096 long."""
+    n, H, D = 4096, 16, 128
+    p, x = attention_problem(9, "bf16", n, 1, H, H, D, D)
+    packed = {m: (t[:, 0].contiguous() if m != "log_decay" else t) for m, t in p.items()}
+    off = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(packed["v"])
+    with Handle() as h:
+        h.linear_attention(*(packed[m][:1] for m in ("q", "k", "v")), packed["log_decay"], offsets=off[:2])
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        h.linear_attention(**packed, scale=1.0, offsets=off, out=out)
+        torch.cuda.synchronize()
+        used = before - torch.cuda.mem_get_info()[0]
+    # operands of 67 MB, of which a state of every 128 rows is 33 MB
+    assert used < 256 << 20
+    for t in (0, 1, 2000, n - 1):
+        check_forward(out[t:t + 1, None], None, {m: (y[t:t + 1] if m != "log_decay" else y) for m, y in p.items()}, 1.0)
