@@ -150,6 +150,13 @@ __device__ __forceinline__ float uniform(float x) {
   return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
 }
 
+// A state carried over many tokens at once, S d^n + own, with whole = d^n and one =
+// d.  The recurrence keeps an infinity, and a zero, for any number of tokens, where
+// d^n may have become 0 or infinity and the product NaN: those take one token's d.
+__device__ __forceinline__ float carried(float S, float own, float whole, float one) {
+  return __builtin_fmaf(S, S == 0.f || __builtin_isinf(S) ? one : whole, own);
+}
+
 // -- splitting into bf16 parts -----------------------------------------------------
 
 __device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
@@ -663,7 +670,7 @@ __device__ __forceinline__ void first_state(f32x4 (&S)[DKP / 16][NT], const Attn
 #pragma unroll
     for (int m = 0; m < NT; ++m) S[t][m] = p[(t * NT + m) * 64];
   if (scanned) return;
-  const float whole = uniform(decay_power(w.log_decay, a.seg_tokens));
+  const float whole = uniform(decay_power(w.log_decay, a.seg_tokens)), one = uniform(decay_power(w.log_decay, 1));
   for (int i = 1; i < w.seg; ++i) {
     const f32x4* own = slot_at<KT, NT>(w, i, wave, lane);
 #pragma unroll
@@ -672,7 +679,7 @@ __device__ __forceinline__ void first_state(f32x4 (&S)[DKP / 16][NT], const Attn
       for (int m = 0; m < NT; ++m) {
         const f32x4 x = own[(t * NT + m) * 64];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[t][m][r] = __builtin_fmaf(S[t][m][r], whole, x[r]);
+        for (int r = 0; r < 4; ++r) S[t][m][r] = carried(S[t][m][r], x[r], whole, one);
       }
   }
 }
@@ -749,11 +756,13 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs
   start();
   if (w.seg == 0) {
     if (w.initial >= 0) put(w.initial);
-    const float whole = uniform(decay_power(w.log_decay, hi - lo));
+    const float whole = uniform(decay_power(w.log_decay, hi - lo)), one = uniform(decay_power(w.log_decay, 1));
 #pragma unroll
     for (int t = 0; t < Sh::KT; ++t)
 #pragma unroll
-      for (int m = 0; m < NT; ++m) S[t][m] *= whole;
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[t][m][r] = carried(S[t][m][r], 0.f, whole, one);
   }
   float after = 1.f;  // decay of the tokens behind the chunk
   for (int i = end; i >= lo; i -= C) {
@@ -800,7 +809,7 @@ __global__ void __launch_bounds__(256) attention_scan_kernel(AttnArgs a) {
   const Span s = span_of(a, b);
   const int reached = (s.len - 1) / a.seg_tokens;  // slots that are read
   if (reached < 2) return;
-  const float whole = decay_power(a.log_decay[h], a.seg_tokens);
+  const float whole = decay_power(a.log_decay[h], a.seg_tokens), one = decay_power(a.log_decay[h], 1);
   const int64_t slot = first_slot(a, job, b, (uint32_t)s.first / (uint32_t)a.seg_tokens);
   f32x4* p = reinterpret_cast<f32x4*>(job.segments) + ((slot * a.H + h) * a.tiles + tile) * (DKP * DVT / 4) +
              (blockIdx.x % kBlocks) * 256 + threadIdx.x;
@@ -814,7 +823,7 @@ __global__ void __launch_bounds__(256) attention_scan_kernel(AttnArgs a) {
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= reached) break;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[r] = __builtin_fmaf(S[r], whole, own[i][r]);
+      for (int r = 0; r < 4; ++r) S[r] = carried(S[r], own[i][r], whole, one);
       p[(i0 + i) * step] = S;
     }
   }

@@ -3,11 +3,13 @@ lengths, strides, buffers that are one, sizes past the usual shapes.
 
 Tolerances are those of test_gpu_sequence.py, whose derivation they share.
 """
+import numpy as np
 import pytest
 import torch
 
+import oracle
 from persistent_rnn_fwd_amd import Handle
-from test_gpu_sequence import TYPES, attention_problem, check_backward, check_forward, handle  # noqa: F401
+from test_gpu_sequence import TYPES, attention_problem, check_backward, check_forward, handle, host  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -204,3 +206,68 @@ def test_many_sequences_without_a_longest_take_little_memory(gpu):
     assert used < 256 << 20
     for t in (0, 1, 2000, n - 1):
         check_forward(out[t:t + 1, None], None, {m: (y[t:t + 1] if m != "log_decay" else y) for m, y in p.items()}, 1.0)
+
+
+# -- values that are not finite ----------------------------------------------------------------------------------
+
+def check_kinds(got, want):
+    """The same NaN, and the same infinities."""
+    got = host(got)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    assert np.isfinite(got[np.isfinite(want)]).all()
+
+
+DECAYS = [-0.01, -0.5, -0.9, -2.0, -30.0, 0.0, 1e-3, -float("inf")]
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("T", [40, 150, 192, 400, 500, 700, 2500])
+@pytest.mark.parametrize("where", ["k", "v", "S0"])
+def test_infinities_follow_the_recurrence(handle, type, T, where):  # noqa: F811
+    """An infinity in the first tokens (or in the state before them) of sequences of
+    one, 2, 3, 6, 7 and more segments, at decays whose power over a segment is 0."""
+    H = len(DECAYS)
+    p, x = attention_problem(10, type, T, 1, H, H, 16, 16, decay=DECAYS)
+    if where == "S0":
+        x["S0"][0, :, 3, 4], x["S0"][0, :, 5, 6] = float("inf"), float("nan")
+    else:
+        p[where][5, 0, :, 3] = float("inf")
+    S = torch.empty_like(x["S0"])
+    o = handle.linear_attention(**p, scale=0.2, initial_state=x["S0"], final_state=S)
+    with np.errstate(invalid="ignore"):
+        ref, refS = oracle.linear_attention(**{m: host(y) for m, y in p.items()}, scale=0.2, S0=host(x["S0"]))
+    check_kinds(o, ref)
+    check_kinds(S, refS)
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("T", [40, 192, 500, 700, 2500])
+@pytest.mark.parametrize("where", ["q", "k", "v", "do", "S0", "dS1"])
+def test_gradients_of_infinities_follow_the_recurrence(handle, type, T, where):  # noqa: F811
+    H = len(DECAYS)
+    p, x = attention_problem(11, type, T, 1, H, H, 16, 16, decay=DECAYS)
+    if where in ("S0", "dS1"):
+        x[where][0, :, 3, 4] = float("inf")
+    else:
+        (p if where in p else x)[where][T - 5 if where in ("q", "do") else 5, 0, :, 3] = float("inf")
+    dS0 = torch.empty_like(x["S0"])
+    grads = handle.linear_attention_backward(**p, grad_out=x["do"], scale=0.2, initial_state=x["S0"],
+                                             grad_final_state=x["dS1"], grad_initial_state=dS0)
+    with np.errstate(invalid="ignore"):
+        ref = oracle.linear_attention_backward(**{m: host(y) for m, y in p.items()}, do=host(x["do"]), scale=0.2,
+                                               S0=host(x["S0"]), dS1=host(x["dS1"]))
+    for got, want in zip((*grads, dS0), ref):
+        check_kinds(got, want)
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("T", [192, 700])
+def test_growth_leaves_zeros_alone(handle, type, T):  # noqa: F811
+    """Decays above 1 whose power over a segment is infinite: rows of the state
+    that are zero stay zero."""
+    p, _ = attention_problem(12, type, T, 1, 2, 2, 16, 16, decay=[1.5, 2.0])
+    p["k"][..., 4:] = 0
+    S = torch.full((1, 2, 16, 16), float("nan"), device="cuda")
+    handle.linear_attention(**p, scale=0.2, final_state=S)
+    assert not S[:, :, 4:].any() and torch.isinf(S[:, :, :4]).any()
