@@ -642,6 +642,7 @@ prnnStatus_t prnn_linear_attention_step(prnnHandle_t handle, const prnnAttention
  * BAD_PARAM: NULL handle, x or y (M > 0); M < 0, N < 1, ld < N; eps < 0 or NaN;
  * unknown or unsupported types; misaligned pointers; y overlapping x (unless
  * equal), weight or bias; mean or rstd overlapping any other buffer.
+ * NOT_SUPPORTED: M above 2^31 - 1, N above 2^31 - 1024.
  * M == 0 does nothing. */
 prnnStatus_t prnn_layer_norm(prnnHandle_t handle, int64_t M, int N, prnnDataType_t type, const void* x, int64_t ldx,
                              prnnDataType_t param_type, const void* weight, const void* bias, float eps, void* y,

@@ -178,35 +178,37 @@ __global__ void __launch_bounds__(BLOCK) norm_kernel(NormArgs a) {
   }
 }
 
-// Rows wider than the registers of a workgroup: three reads of the row, the
-// later two from the caches.
+// Rows wider than the registers of a workgroup (or narrower than a vector): three
+// reads of the row, the later two from the caches.  A workgroup takes rows r, r +
+// grid, ...
 template <class E, class P>
 __global__ void __launch_bounds__(1024) norm_wide_kernel(NormArgs a) {
   typedef typename E::raw raw;
   __shared__ float slots[16];
-  const int64_t m = blockIdx.x;
-  const raw* x = static_cast<const raw*>(a.x) + m * a.ldx;
-  raw* y = static_cast<raw*>(a.y) + m * a.ldy;
-  float s[1] = {0.f};
-  for (int n = threadIdx.x; n < a.N; n += 1024) s[0] += E::get(x[n]);
-  row_sums<1024>(s, slots);
-  const float mean = s[0] / (float)a.N;
-  s[0] = 0.f;
-  for (int n = threadIdx.x; n < a.N; n += 1024) {
-    const float c = E::get(x[n]) - mean;
-    s[0] = __builtin_fmaf(c, c, s[0]);
-  }
-  row_sums<1024>(s, slots);
-  const float rstd = 1.f / sqrtf(s[0] / (float)a.N + a.eps);
-  for (int n = threadIdx.x; n < a.N; n += 1024) {
-    float w[1], b[1];
-    load_param<P, 1, false>(a.weight, n, true, 1.f, w);
-    load_param<P, 1, false>(a.bias, n, true, 0.f, b);
-    y[n] = E::put(__builtin_fmaf((E::get(x[n]) - mean) * rstd, w[0], b[0]));
-  }
-  if (threadIdx.x == 0) {
-    if (a.mean != nullptr) a.mean[m] = mean;
-    if (a.rstd != nullptr) a.rstd[m] = rstd;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+    const raw* x = static_cast<const raw*>(a.x) + m * a.ldx;
+    raw* y = static_cast<raw*>(a.y) + m * a.ldy;
+    float s[1] = {0.f};
+    for (int n = threadIdx.x; n < a.N; n += 1024) s[0] += E::get(x[n]);
+    row_sums<1024>(s, slots);
+    const float mean = s[0] / (float)a.N;
+    s[0] = 0.f;
+    for (int n = threadIdx.x; n < a.N; n += 1024) {
+      const float c = E::get(x[n]) - mean;
+      s[0] = __builtin_fmaf(c, c, s[0]);
+    }
+    row_sums<1024>(s, slots);
+    const float rstd = 1.f / sqrtf(s[0] / (float)a.N + a.eps);
+    for (int n = threadIdx.x; n < a.N; n += 1024) {
+      float w[1], b[1];
+      load_param<P, 1, false>(a.weight, n, true, 1.f, w);
+      load_param<P, 1, false>(a.bias, n, true, 0.f, b);
+      y[n] = E::put(__builtin_fmaf((E::get(x[n]) - mean) * rstd, w[0], b[0]));
+    }
+    if (threadIdx.x == 0) {
+      if (a.mean != nullptr) a.mean[m] = mean;
+      if (a.rstd != nullptr) a.rstd[m] = rstd;
+    }
   }
 }
 
@@ -319,26 +321,27 @@ template <class E, class P>
 __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(NormArgs a) {
   typedef typename E::raw raw;
   __shared__ float slots[32];
-  const int64_t m = blockIdx.x;
-  const raw* x = static_cast<const raw*>(a.x) + m * a.ldx;
-  const raw* dy = static_cast<const raw*>(a.dy) + m * a.lddy;
-  raw* dx = static_cast<raw*>(a.y) + m * a.ldy;
-  const float mean = a.mean_in[m], rstd = a.rstd_in[m];
-  float s[2] = {0.f, 0.f};
-  for (int n = threadIdx.x; n < a.N; n += 1024) {
-    float w[1];
-    load_param<P, 1, false>(a.weight, n, true, 1.f, w);
-    const float g = E::get(dy[n]) * w[0];
-    s[0] += g;
-    s[1] = __builtin_fmaf(g, (E::get(x[n]) - mean) * rstd, s[1]);
-  }
-  row_sums<1024>(s, slots);
-  const float g0 = s[0] / (float)a.N, g1 = s[1] / (float)a.N;
-  for (int n = threadIdx.x; n < a.N; n += 1024) {
-    float w[1];
-    load_param<P, 1, false>(a.weight, n, true, 1.f, w);
-    const float c = (E::get(x[n]) - mean) * rstd, g = E::get(dy[n]) * w[0];
-    dx[n] = E::put(rstd * (g - g0 - c * g1));
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+    const raw* x = static_cast<const raw*>(a.x) + m * a.ldx;
+    const raw* dy = static_cast<const raw*>(a.dy) + m * a.lddy;
+    raw* dx = static_cast<raw*>(a.y) + m * a.ldy;
+    const float mean = a.mean_in[m], rstd = a.rstd_in[m];
+    float s[2] = {0.f, 0.f};
+    for (int n = threadIdx.x; n < a.N; n += 1024) {
+      float w[1];
+      load_param<P, 1, false>(a.weight, n, true, 1.f, w);
+      const float g = E::get(dy[n]) * w[0];
+      s[0] += g;
+      s[1] = __builtin_fmaf(g, (E::get(x[n]) - mean) * rstd, s[1]);
+    }
+    row_sums<1024>(s, slots);
+    const float g0 = s[0] / (float)a.N, g1 = s[1] / (float)a.N;
+    for (int n = threadIdx.x; n < a.N; n += 1024) {
+      float w[1];
+      load_param<P, 1, false>(a.weight, n, true, 1.f, w);
+      const float c = (E::get(x[n]) - mean) * rstd, g = E::get(dy[n]) * w[0];
+      dx[n] = E::put(rstd * (g - g0 - c * g1));
+    }
   }
 }
 
@@ -369,29 +372,33 @@ __global__ void __launch_bounds__(1024) norm_params_kernel(const float* partial,
   typedef typename P::raw raw;
   __shared__ float part[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  float s = 0.f;
-  if (c < 2ll * N) {
-    constexpr int kAhead = 8;
-    for (int g0 = w; g0 < count; g0 += 16 * kAhead) {
-      float x[kAhead];
+  for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < 2ll * N; c0 += (int64_t)gridDim.x * 64) {
+    const int64_t c = c0 + lane;
+    float s = 0.f;
+    if (c < 2ll * N) {
+      constexpr int kAhead = 8;
+      for (int g0 = w; g0 < count; g0 += 16 * kAhead) {
+        float x[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int g = g0 + 16 * i;
-        x[i] = g < count ? partial[(size_t)g * 2 * N + c] : 0.f;
+        for (int i = 0; i < kAhead; ++i) {
+          const int g = g0 + 16 * i;
+          x[i] = g < count ? partial[(size_t)g * 2 * N + c] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) s += x[i];
       }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) s += x[i];
     }
-  }
-  part[w][lane] = s;
-  __syncthreads();
-  if (w != 0 || c >= 2ll * N) return;
-  s = 0.f;
+    part[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && c < 2ll * N) {
+      s = 0.f;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) s += part[j][lane];
-  raw* out = static_cast<raw*>(c < N ? dweight : dbias);
-  if (out != nullptr) out[c < N ? c : c - N] = P::put(s);
+      for (int j = 0; j < 16; ++j) s += part[j][lane];
+      raw* out = static_cast<raw*>(c < N ? dweight : dbias);
+      if (out != nullptr) out[c < N ? c : c - N] = P::put(s);
+    }
+    __syncthreads();  // before the next columns' sums
+  }
 }
 
 // Threads a row (TPR) and vectors a thread (NV) for rows of N: the fewest
@@ -410,6 +417,9 @@ Shape shape_of(int N, int elems, bool odd, int columns) {
     if (p[0] * p[1] >= units && p[1] * elems <= columns) return {odd, p[0], p[1]};
   return {odd, 0, 0};
 }
+
+// Workgroups of 1024 threads for `tasks`: a launch counts threads in 32 bits.
+unsigned workgroups(int64_t tasks) { return (unsigned)(tasks < 1 << 20 ? tasks : 1 << 20); }
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
@@ -477,7 +487,7 @@ hipError_t launch_layer_norm(const NormArgs& a, prnnDataType_t type, prnnDataTyp
       const int64_t most = 4ll * a.compute_units, grid = sets < most ? sets : most;
       norm_kernel<E, P, C::v, C::odd, C::tpr, C::nv, C::block><<<(unsigned)grid, C::block, 0, stream>>>(a);
     });
-    if (!fits) norm_wide_kernel<E, P><<<(unsigned)a.M, 1024, 0, stream>>>(a);
+    if (!fits) norm_wide_kernel<E, P><<<workgroups(a.M), 1024, 0, stream>>>(a);
     return hipGetLastError();
   });
 }
@@ -511,11 +521,11 @@ hipError_t launch_layer_norm_backward(const NormArgs& a, prnnDataType_t type, pr
       if (!fits) {
         // the columns first: dx may be written over x or dy
         if (a.partial != nullptr) norm_columns_kernel<E><<<dim3((a.N + 255) / 256, grid), 256, 0, stream>>>(a);
-        if (a.y != nullptr) norm_backward_wide_kernel<E, P><<<(unsigned)a.M, 1024, 0, stream>>>(a);
+        if (a.y != nullptr) norm_backward_wide_kernel<E, P><<<workgroups(a.M), 1024, 0, stream>>>(a);
       }
     }
     if (a.dweight != nullptr || a.dbias != nullptr)
-      norm_params_kernel<P><<<(unsigned)((2ll * a.N + 63) / 64), 1024, 0, stream>>>(a.partial, grid, a.N, a.dweight,
+      norm_params_kernel<P><<<workgroups((2ll * a.N + 63) / 64), 1024, 0, stream>>>(a.partial, grid, a.N, a.dweight,
                                                                                    a.dbias);
     return hipGetLastError();
   });

@@ -424,7 +424,8 @@ static prnnStatus_t check_norm(prnnContext* h, int64_t M, int N, prnnDataType_t 
   if (handle_failed(h)) return PRNN_STATUS_EXECUTION_FAILED;
   if (M < 0 || N < 1 || !known(type) || !known(ptype)) return PRNN_STATUS_BAD_PARAM;
   if (ptype != PRNN_DATA_FLOAT && ptype != type) return PRNN_STATUS_BAD_PARAM;
-  return M > 0x7fffffffll ? PRNN_STATUS_NOT_SUPPORTED : PRNN_STATUS_SUCCESS;
+  // (columns are counted in 31 bits, in steps of up to 1024)
+  return M > 0x7fffffffll || N > 0x7fffffff - 1023 ? PRNN_STATUS_NOT_SUPPORTED : PRNN_STATUS_SUCCESS;
 }
 
 static bool ld_ok(int64_t ld, int N) { return ld >= N && ld <= kMaxStride; }

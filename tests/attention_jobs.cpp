@@ -285,12 +285,26 @@ static void packed_workspace() {
       }
 }
 
+// Layer norm counts columns in 31 bits.
+static void wide_norms() {
+  prnnContext h;
+  float *x = Problem::state(0), *y = Problem::state(1), *m = Problem::state(2), *w = Problem::state(3);
+  const prnnDataType_t f = PRNN_DATA_FLOAT;
+  for (int N : {1, 12345, 0x7fffffff - 1023, 0x7fffffff - 1022, 0x7fffffff - 255, 0x7fffffff}) {
+    const prnnStatus_t want = N > 0x7fffffff - 1023 ? PRNN_STATUS_NOT_SUPPORTED : PRNN_STATUS_SUCCESS;
+    CHECK(prnn_layer_norm(&h, 1, N, f, x, N, f, nullptr, nullptr, 0.f, y, N, nullptr, nullptr, nullptr) == want, "%d columns", N);
+    CHECK(prnn_layer_norm_backward(&h, 1, N, f, y, N, x, N, m, m + 1, f, nullptr, w, N, nullptr, nullptr, nullptr) == want,
+          "%d columns", N);
+  }
+}
+
 int main(int argc, char** argv) {
   const char* const which = argc > 1 ? argv[1] : "";
   if (!std::strcmp(which, "long sequences")) long_sequences();
   else if (!std::strcmp(which, "gradients in place")) gradients_in_place();
   else if (!std::strcmp(which, "shared heads")) shared_heads();
   else if (!std::strcmp(which, "packed workspace")) packed_workspace();
+  else if (!std::strcmp(which, "wide norms")) wide_norms();
   else ++failures;
   if (failures == 0) std::printf("all checks passed\n");
   return failures == 0 ? 0 : 1;

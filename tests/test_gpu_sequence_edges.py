@@ -9,7 +9,8 @@ import torch
 
 import oracle
 from persistent_rnn_fwd_amd import Handle
-from test_gpu_sequence import TYPES, attention_problem, check_backward, check_forward, handle, host  # noqa: F401
+from test_gpu_sequence import TYPES, attention_problem, check_backward, check_forward, check_norm, check_norm_backward, \
+    handle, host, norm_problem  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -271,3 +272,36 @@ def test_growth_leaves_zeros_alone(handle, type, T):  # noqa: F811
     S = torch.full((1, 2, 16, 16), float("nan"), device="cuda")
     handle.linear_attention(**p, scale=0.2, final_state=S)
     assert not S[:, :, 4:].any() and torch.isinf(S[:, :, :4]).any()
+
+
+# -- layer norm of many rows and of wide ones --------------------------------------------------------------------
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("M, N", [((1 << 22) + 5, 3), (1, (1 << 27) + 5)], ids=["rows", "columns"])
+def test_norm_past_what_one_launch_counts(handle, type, M, N):  # noqa: F811
+    """Rows that no vector covers take a workgroup each, the sums of the parameters'
+    gradients one for 32 columns."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dt = TYPES[type]
+    x, dy = (torch.randn((M, N), generator=g, device="cuda").to(dt) for _ in range(2))
+    w = torch.randn(N, generator=g, device="cuda").to(dt)
+    mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    y = handle.layer_norm(x, w, mean=mean, rstd=rstd)
+    dx, dw, db = handle.layer_norm_backward(dy, x, mean, rstd, w)
+    if M > 1:
+        some = torch.cat([torch.arange(5), torch.tensor([1 << 20, (1 << 22) - 1, 1 << 22, M - 1])]).cuda()
+        check_norm(y[some], mean[some], rstd[some], x[some], w, None)
+        check_norm_backward(dx[some], None, None, dy[some], x[some], w, mean[some], rstd[some])
+        n = (x.double() - mean[:, None]) * rstd[:, None]
+        want = (dy.double() * n).sum(0), dy.double().sum(0), (dy.double() * n).abs().sum(0)
+        for got, ref in ((dw, want[0]), (db, want[1])):  # 2^16 rows in turn at most, of 2^-24 each, and a rounding
+            assert ((got.double() - ref).abs() <= 2.0 ** -8 * want[2] + torch.finfo(dt).eps / 2 * ref.abs()).all()
+    else:
+        # every column of the one row: statistics to the roundings of 2^17 columns a thread
+        n = (x.double() - x.double().mean()) * (x.double().var(correction=0) + 1e-5).rsqrt()
+        part = slice(N - 4096, None)
+        for got, ref in ((y, n * w.double()), (dw, dy.double() * n), (db, dy.double())):
+            got, ref = got.view(-1), ref.view(-1)
+            for s in (slice(0, 4096), part):
+                assert ((got[s].double() - ref[s]).abs() <= (2.0 ** -7 + torch.finfo(dt).eps) * (ref[s].abs() + 1)).all()
+        assert torch.isfinite(dx).all() and dx.view(-1)[part].any()
