@@ -207,7 +207,6 @@ hipError_t launch_attention_reduce(const AttnReduceArgs& args, prnnDataType_t ty
 
 hipError_t launch_attention_step(const AttnStepArgs& args, prnnDataType_t type, hipStream_t stream) {
   AttnStepArgs a = args;
-  a.tiles = (a.Dv + 31) / 32;
   a.by_tiles = inverse_of(a.tiles);
   a.by_heads = inverse_of(a.H);
   for (AttnOperand* x : {&a.q, &a.k, &a.v}) x->inverse = inverse_of(x->group);

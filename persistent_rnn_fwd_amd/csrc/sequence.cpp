@@ -401,6 +401,8 @@ prnnStatus_t prnn_linear_attention_step(prnnHandle_t h, const prnnAttention_t* d
   const int group = d->H / d->Hkv;
   AttnStepArgs a;
   std::memset(&a, 0, sizeof(a));
+  a.tiles = (d->Dv + 31) / 32;
+  if ((int64_t)a.tiles * d->B * d->H > kMaxWorkgroups) return PRNN_STATUS_NOT_SUPPORTED;
   a.q = operand(q, 1);
   a.k = operand(k, group);
   a.v = operand(v, group);

@@ -127,8 +127,8 @@ struct AttnStepArgs {
   const float* s_in;
   float* s_out;
   int B, H, Dk, Dv;
-  int tiles;  // tiles of 32 columns (set by the launch)
-  uint32_t by_tiles, by_heads;
+  int tiles;  // tiles of 32 columns
+  uint32_t by_tiles, by_heads;  // inverses of tiles and H (set by the launch)
   float scale;
 };
 hipError_t launch_attention_step(const AttnStepArgs& a, prnnDataType_t type, hipStream_t stream);

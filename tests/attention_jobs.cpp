@@ -14,7 +14,7 @@ static const uintptr_t kWork = 0x700000000000ull;
 static size_t workspace = 0;  // bytes asked for by the last call
 static prnn::AttnArgs args;   // of the last launch
 static prnn::AttnReduceArgs reduced;
-static int launches = 0, reductions = 0;
+static int launches = 0, steps = 0, reductions = 0;
 
 namespace prnn {
 bool handle_failed(prnnContext*) { return false; }
@@ -35,7 +35,10 @@ hipError_t launch_attention_reduce(const AttnReduceArgs& a, prnnDataType_t, hipS
   ++reductions;
   return hipSuccess;
 }
-hipError_t launch_attention_step(const AttnStepArgs&, prnnDataType_t, hipStream_t) { return hipSuccess; }
+hipError_t launch_attention_step(const AttnStepArgs&, prnnDataType_t, hipStream_t) {
+  ++steps;
+  return hipSuccess;
+}
 hipError_t launch_layer_norm(const NormArgs&, prnnDataType_t, prnnDataType_t, hipStream_t) { return hipSuccess; }
 int layer_norm_backward_grid(const NormArgs&, prnnDataType_t, int) { return 0; }
 hipError_t launch_layer_norm_backward(const NormArgs&, prnnDataType_t, prnnDataType_t, int, hipStream_t) { return hipSuccess; }
@@ -285,6 +288,27 @@ static void packed_workspace() {
       }
 }
 
+// Launches of more threads than 32 bits count are refused.
+static void grids() {
+  const struct {
+    int B, H, Dk, Dv;
+    bool step, whole;
+  } shapes[] = {{64, 32, 128, 128, true, true},      {1 << 18, 63, 1, 1, true, true}, {1 << 19, 32, 1, 32, false, false},
+                {1 << 18, 32, 1, 33, false, true},   {1 << 19, 15, 1, 64, true, true}, {1 << 19, 16, 1, 64, false, true},
+                {1 << 16, 256, 1, 1, false, false},  {1 << 15, 255, 1, 256, false, true}};
+  for (const auto& s : shapes) {
+    Problem p(s.B, 1, s.H, s.H, s.Dk, s.Dv, PRNN_DATA_BFLOAT, true);
+    p.S0 = Problem::state(0);
+    p.S1 = Problem::state(1);
+    launches = steps = 0;
+    const bool step = prnn_linear_attention_step(&p.h, &p.d, &p.q, &p.k, &p.v, p.S0, &p.o, p.S1, nullptr) == PRNN_STATUS_SUCCESS;
+    CHECK(step == s.step && steps == (s.step ? 1 : 0), "a step of %d x %d heads of %d", s.B, s.H, s.Dv);
+    const prnnStatus_t st = p.forward();
+    CHECK(st == (s.whole ? PRNN_STATUS_SUCCESS : PRNN_STATUS_NOT_SUPPORTED) && launches == (s.whole ? 1 : 0),
+          "%d x %d heads of %d: %d", s.B, s.H, s.Dv, (int)st);
+  }
+}
+
 // Layer norm counts columns in 31 bits.
 static void wide_norms() {
   prnnContext h;
@@ -305,6 +329,7 @@ int main(int argc, char** argv) {
   else if (!std::strcmp(which, "shared heads")) shared_heads();
   else if (!std::strcmp(which, "packed workspace")) packed_workspace();
   else if (!std::strcmp(which, "wide norms")) wide_norms();
+  else if (!std::strcmp(which, "grids")) grids();
   else ++failures;
   if (failures == 0) std::printf("all checks passed\n");
   return failures == 0 ? 0 : 1;
