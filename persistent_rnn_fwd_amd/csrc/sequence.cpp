@@ -24,9 +24,18 @@ struct Region {
   } axis[3] = {};
 };
 
+// `e` and the bytes from an axis' first row to its last.  No memory reaches
+// kFar: what does counts as that, so that the sums stay in 64 bits.
+constexpr uint64_t kFar = 1ull << 60;
+uint64_t along(uint64_t e, const Region::Axis& x) {
+  if (x.count <= 1) return e;
+  const unsigned __int128 far = (unsigned __int128)x.stride * (x.count - 1) + e;
+  return far < kFar ? (uint64_t)far : kFar;
+}
+
 uint64_t extent(const Region& r) {
   uint64_t e = r.row;
-  for (const auto& x : r.axis) e += x.stride * (x.count > 0 ? x.count - 1 : 0);
+  for (const auto& x : r.axis) e = along(e, x);
   return e;
 }
 
@@ -59,7 +68,7 @@ bool overlap(const Region& a, const Region& b) {
     for (const Region* r : {&a, &b}) {
       foot[i] = r->row;
       for (const auto& x : r->axis)
-        if (x.count > 1 && x.stride < pick.stride) foot[i] += x.stride * (x.count - 1);
+        if (x.stride < pick.stride) foot[i] = along(foot[i], x);
       ++i;
     }
     const uint64_t d = a.base <= b.base ? (b.base - a.base) % period : (period - (a.base - b.base) % period) % period;
@@ -76,7 +85,7 @@ bool distinct(const Region& r) {
   for (const auto& y : x) {
     if (y.count <= 1) continue;
     if (y.stride < e) return false;
-    e += y.stride * (y.count - 1);
+    e = along(e, y);
   }
   return true;
 }
@@ -94,7 +103,7 @@ Region rows_of(const void* p, int64_t M, int N, int64_t ld, size_t e) {
   return r;
 }
 
-// Strides beyond this cannot address memory; products of sizes stay in 64 bits.
+// Strides beyond this cannot address memory.
 constexpr int64_t kMaxStride = 1ll << 40;
 constexpr int64_t kMaxTokenStride = 1ll << 23;
 // Tokens of a sequence: the segments that cover them, and a chunk more, stay in

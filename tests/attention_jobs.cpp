@@ -309,6 +309,32 @@ static void grids() {
   }
 }
 
+// Spans past 64 bits do not wrap into small ones: an output in the place of a far
+// row of an input, or the other way round, is refused.
+static void spans() {
+  const int B = (1 << 23) + 1;
+  const int64_t stride = 1ll << 40;  // (B - 1) strides are 2^64 bytes
+  for (int which = 0; which < 3; ++which) {
+    Problem p(B, 1, 1, 1, 8, 8, PRNN_DATA_HALF, true);
+    p.S0 = Problem::state(0);
+    p.S1 = Problem::state(1);
+    prnnSequence_t *far = which == 0 ? &p.q : which == 1 ? &p.v : &p.o, *near = which == 2 ? &p.k : &p.o;
+    far->batch = stride;
+    far->data = reinterpret_cast<void*>(0x10000);
+    near->data = static_cast<char*>(far->data) + 5 * 2 * stride;
+    CHECK(p.forward() == PRNN_STATUS_BAD_PARAM, "forward %d", which);
+    CHECK(prnn_linear_attention_step(&p.h, &p.d, &p.q, &p.k, &p.v, p.S0, &p.o, p.S1, nullptr) == PRNN_STATUS_BAD_PARAM,
+          "step %d", which);
+  }
+  prnnContext h;
+  float *x = reinterpret_cast<float*>(0x10000), *y = x + 5 * stride;
+  for (const int M : {4, 6, (1 << 22) + 1}) {
+    const prnnStatus_t want = M > 5 ? PRNN_STATUS_BAD_PARAM : PRNN_STATUS_SUCCESS;
+    CHECK(prnn_layer_norm(&h, M, 4, PRNN_DATA_FLOAT, x, stride, PRNN_DATA_FLOAT, nullptr, nullptr, 0.f, y, 4, nullptr, nullptr,
+                          nullptr) == want, "%d rows", M);
+  }
+}
+
 // Layer norm counts columns in 31 bits.
 static void wide_norms() {
   prnnContext h;
@@ -330,6 +356,7 @@ int main(int argc, char** argv) {
   else if (!std::strcmp(which, "packed workspace")) packed_workspace();
   else if (!std::strcmp(which, "wide norms")) wide_norms();
   else if (!std::strcmp(which, "grids")) grids();
+  else if (!std::strcmp(which, "spans")) spans();
   else ++failures;
   if (failures == 0) std::printf("all checks passed\n");
   return failures == 0 ? 0 : 1;

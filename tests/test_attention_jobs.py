@@ -28,7 +28,7 @@ def driver(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("what", ["long sequences", "gradients in place", "shared heads", "packed workspace", "wide norms", "grids"])
+@pytest.mark.parametrize("what", ["long sequences", "gradients in place", "shared heads", "packed workspace", "wide norms", "grids", "spans"])
 def test_launches(driver, what):
     r = subprocess.run([driver, what], capture_output=True, text=True, env={**os.environ, "ASAN_OPTIONS": "detect_leaks=0"})
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
