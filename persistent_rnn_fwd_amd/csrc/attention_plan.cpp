@@ -51,7 +51,7 @@ size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
   a->seg_tokens = std::max(64, (int)(((a->T + segments - 1) / segments + 63) / 64 * 64));
   a->segments = std::max(1, (int)(((int64_t)a->T + a->seg_tokens - 1) / a->seg_tokens));
   // (every sequence gets the longest one's workgroups, whatever its length)
-  if (a->segments > 1 && (int64_t)a->tiles * a->B * a->H * a->segments > kMaxWorkgroups) {
+  if (!grid_fits(*a)) {
     a->segments = 1;
     a->seg_tokens = (a->T + 63) / 64 * 64;
   }

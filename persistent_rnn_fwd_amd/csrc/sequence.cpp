@@ -182,13 +182,6 @@ AttnArgs base_args(const Problem& p, int jobs) {
   return a;
 }
 
-// Workgroups of the widest launch: the segments', or where they are summed ahead
-// (from 9 on) up to 16 for a state.
-bool grid_fits(const AttnArgs& a) {
-  const int64_t states = (int64_t)a.tiles * a.B * a.H;
-  return states * (a.segments > 1 ? std::max(a.segments, 16) : 1) <= kMaxWorkgroups;
-}
-
 uint64_t state_bytes(const prnnAttention_t& d) { return 4ull * d.B * d.H * d.Dk * d.Dv; }
 
 // A state output may be the state input itself, nothing else.

@@ -96,6 +96,13 @@ inline int64_t slots(const AttnArgs& a) {
 // Workgroups of 256 threads that a launch takes (it counts threads in 32 bits).
 constexpr int64_t kMaxWorkgroups = (1ll << 24) - 1;
 
+// Whether the widest launch of a plan fits that: the segments', or where their
+// states are summed ahead (from 9 on) up to 16 workgroups for a state.
+inline bool grid_fits(const AttnArgs& a) {
+  const int64_t each = a.segments <= 1 ? 1 : a.segments > 16 ? a.segments : 16;
+  return (int64_t)a.tiles * a.B * a.H * each <= kMaxWorkgroups;
+}
+
 // Chooses the instance and the split, and returns the floats of workspace
 // that each job needs for AttnJob::segments (0: none).
 size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units);

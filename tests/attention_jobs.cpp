@@ -240,7 +240,7 @@ static void packed_workspace() {
     int max_len, H, Hkv, D;
   } shapes[] = {{512, 32768, 32768, 16, 16, 128}, {512, 32768, 16384, 16, 16, 128}, {4096, 4096, 4096, 16, 4, 128},
                 {4096, 4096, 1, 16, 16, 128},     {100000, 100000, 100000, 1, 1, 64}, {7, 3001, 1200, 16, 4, 64},
-                {60, 60000, 60000, 4, 2, 256},    {1 << 22, 1 << 22, 1 << 22, 1, 1, 16}, {3, 130, 130, 2, 2, 200}};
+                {60, 60000, 60000, 4, 2, 256},    {1 << 22, 1 << 22, 1 << 22, 1, 1, 16}, {1 << 20, 900, 900, 1, 1, 64}, {3, 130, 130, 2, 2, 200}};
   for (const auto& s : shapes)
     for (bool states : {false, true})
       for (int call = 0; call < 2; ++call) {
