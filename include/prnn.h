@@ -57,19 +57,21 @@
  *    outside the fp16 range where a path needs it) is sticky: the failing
  *    kernel marks a host-visible copy of the handle's status (pinned host
  *    memory), and the next call on the handle that enqueues work (forward,
- *    layer, stack, projection or floor), prnn_synchronize() or prnn_destroy(),
- *    whichever comes first, returns PRNN_STATUS_EXECUTION_FAILED without
- *    waiting for the GPU; that call enqueues nothing.  The failure is
+ *    layer, stack, projection, floor, linear attention or layer norm),
+ *    prnn_synchronize() or prnn_destroy(), whichever comes first, returns
+ *    PRNN_STATUS_EXECUTION_FAILED without waiting for the GPU; that call
+ *    enqueues nothing.  The failure is
  *    reported once; the handle is then usable again (its exchange ring is
  *    reset before the next launch).  Calls enqueued after the failing one but
  *    before the failure reached the host (made while it was still running)
  *    return SUCCESS and do nothing: their kernels see the failure at entry and
- *    leave H as it was.  A call that enqueues several launches (layer and
+ *    leave H as it was (linear attention and layer norm, which cannot fail in
+ *    this way, run as ever).  A call that enqueues several launches (layer and
  *    stack calls) and fails after the first leaves its outputs undefined.
  *  - One forward call may be in flight per handle at a time (the handle owns
- *    the exchange ring).  Use one handle per concurrently used stream.  A
- *    handle is not thread-safe.  Every call must be made with the handle's
- *    device current.
+ *    the exchange ring, and the workspace of linear attention and layer norm).
+ *    Use one handle per concurrently used stream.  A handle is not
+ *    thread-safe.  Every call must be made with the handle's device current.
  *  - No C++ exception crosses this interface.
  */
 #ifndef PRNN_H_

@@ -32,14 +32,16 @@
 // sequence (fewer are added by whoever needs them), and the main kernel starts
 // each segment from its sum.
 //
-// What bounds it.  Large calls in 16 bits: the loads, at the pattern's own rate
-// (the main kernel without its products moves 4.2 TB/s, with them 3.9: rows of
-// 256 bytes, read and written), and the extra read of k and v.  Measured:
-// 32768 bf16 tokens of 32 heads of 128 399 us (main 277, states 112, sum 11),
-// backward of 8 x 2048 tokens of 16 bf16 heads 194 us (221 TFLOP/s of the
-// recurrence's own operations; a chunk takes 6.5 us with one or two workgroups on
-// a unit, of it 2 us of MFMA issue).  fp32: the issue of its six products a
-// product and of the splitting, 5.3 us a chunk of 32 tokens alone on a unit.
+// What bounds it.  Large calls in 16 bits: what they move, which is more than they
+// have to.  k and v are read once more for the segments' states, the three jobs of
+// a backward pass read nine operands where four exist, and o's rows are written
+// in pieces of 64 bytes that cost 30 to 38 % more than o.  Measured, operands not
+// in the caches: 32768 bf16 tokens of 32 heads of 128, 1.79 GB moved (1.07 needed),
+// 437 us (4.1 TB/s); backward of 8 x 2048 tokens of 16 bf16 heads of 128, 844 MB
+// moved (470 needed), 247 us (3.4 TB/s): there the products are in issue for 38 %
+// of the time as well, and half the units have two workgroups, half one.  fp32: the
+// issue of its six products a product and of the splitting, 5.3 us a chunk of 32
+// tokens alone on a unit.
 // Small calls: launches and first loads, 3 us a kernel before its first product.
 //
 // Precision.  Operands are split into bf16 parts, high part first, each the
@@ -50,8 +52,8 @@
 // or more are left out: at most 2^-21 of the product, 2^-25 on average, where
 // both operands have them (a bf16 operand has one part, so none are missing, and
 // fp16 scores have all four).  Two parts between the products of 16-bit types
-// would take 204 us instead of 251 for the backward of 8 x 2048 tokens of 16 bf16
-// heads of 128, and 409 instead of 441 for 32768 tokens of 32, but where terms
+// would take 204 us instead of 247 for the backward of 8 x 2048 tokens of 16 bf16
+// heads of 128, and 409 instead of 437 for 32768 tokens of 32, but where terms
 // cancel the result is off by up to 2^-17 of them, and 2^-14 for fp16 scores.
 // bf16 parts have fp32's range, so large fp16 scores and states do not overflow.
 // Sums are fp32.
@@ -797,7 +799,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) attention_state_kernel(AttnArgs
 
 // Turns the segments' own states into the sequence's states after them, 4
 // elements a thread, the loads of 8 slots ahead (15 slots of 32 heads of 128 x
-// 128, 62 MB, 11 us).  grid: tiles x B H x (DKP DVT /
+// 128, 62 MB, 12 us).  grid: tiles x B H x (DKP DVT /
 // 1024) workgroups, jobs.  (Slots that a sequence does not reach stay as they are:
 // no one reads them.)
 template <int DKP, int NT, int WAVES>
@@ -830,9 +832,11 @@ __global__ void __launch_bounds__(256) attention_scan_kernel(AttnArgs a) {
 }
 
 // Stores the chunk's rows of o, element type or fp32: a lane has 4 NT
-// neighbouring columns of token 16 t + l.  Nontemporal: no one here reads o, and
-// the caches keep q, k and v instead (backward of 8 x 2048 tokens of 16 bf16
-// heads of 128: 207 us with plain stores, 194).
+// neighbouring columns of token 16 t + l.  Nontemporal, so that the caches keep q,
+// k and v: backward of 8 x 2048 tokens of 16 bf16 heads of 128, operands not in the
+// caches, 247 us, 251 with plain stores; with heads that share k and v in fours,
+// whose fp32 rows the next launch reads, 316 and 319; the forward pass and the norm
+// of each head after it, which reads o, 148 and 147.
 constexpr int kStream = 2;
 template <class E, int IT, int NT, bool WIDE>
 __device__ __forceinline__ void put_rows(const Out& x, const Where& w, const f32x4 (&O)[IT][NT], int64_t t0, int n,

@@ -33,18 +33,19 @@ size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
   const int64_t heads = std::max<int64_t>(1, sequences * a->H * a->jobs);
   // 32 columns a wave share its reads of q and k, 16 make twice the workgroups:
   // the narrow form where pieces of 64 tokens of the wide one would not fill the
-  // chip.  Measured (32 / 16 columns): 14 heads of 128, 300 tokens fp32 41 / 32
-  // us, 56 heads, 256 tokens 31 / 29; 128 heads, 1024 tokens 116 / 124.
+  // chip.  Measured (32 / 16 columns), fp32 and bf16: 14 heads of 128, 300 tokens
+  // 42 / 33 and 26 / 22 us, 56 heads, 256 tokens 30 / 29 and 22 / 21; 128 heads,
+  // 1024 tokens 116 / 128 and 65 / 70.
   const int64_t wide = heads * ((dv + 127) / 128) * ((a->T + 63) / 64);
   a->nt = dv > 64 && a->dkp < 256 && wide >= 2 * compute_units ? 2 : 1;
   const int cols = 64 * a->nt;
   a->tiles = (dv + cols - 1) / cols;
   // Segments: as many as give each compute unit 2 workgroups (states of 64 x 64:
   // 3), of at least 128 tokens, or 64 where those would leave units idle.
-  // Measured at 32 heads, 64 / 128 tokens: 1024 tokens of 128 x 128 fp32 56 / 50
-  // us, bf16 39 / 30, of 64 x 64 bf16 24 / 17.  A split in 2 or 3 costs a short
-  // sequence more than it gains: 56 x 3 jobs of 256 tokens fp32 50 whole, 53 in 2;
-  // 160 heads of 4096 tokens bf16 346 whole, 312 in 2, 243 in 3.
+  // Measured at 32 heads, 64 / 128 tokens: 1024 tokens of 128 x 128 fp32 54 / 49
+  // us, bf16 41 / 32, of 64 x 64 bf16 26 / 19.  A split in 2 or 3 costs a short
+  // sequence more than it gains: 56 x 3 jobs of 256 tokens of 128 fp32 49 whole, 53
+  // in 2; 160 heads of 4096 tokens bf16 383 whole, 347 in 2, 266 in 3.
   const int64_t groups = heads * a->tiles, want = compute_units * (a->dkp == 64 && a->nt == 1 ? 3 : 2) / groups;
   const int64_t least = groups * (a->T / 128) >= compute_units ? 128 : 64;
   const int64_t segments = want < 4 && a->T < 512 ? 1 : std::max<int64_t>(1, std::min<int64_t>(want, a->T / least));

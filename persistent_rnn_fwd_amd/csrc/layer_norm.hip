@@ -179,8 +179,10 @@ __global__ void __launch_bounds__(BLOCK) norm_kernel(NormArgs a) {
 }
 
 // Rows wider than the registers of a workgroup (or narrower than a vector): three
-// reads of the row, the later two from the caches.  A workgroup takes rows r, r +
-// grid, ...
+// reads of the row, the later two from the caches, element by element: 4096 x 16392
+// bf16 takes 117 us (2.3 TB/s; x 16384, in registers, 46), and a row of 4 columns a
+// workgroup of its own, 2^20 rows 3.3 ms (of 8 columns, in registers, 63 us).  A
+// workgroup takes rows r, r + grid, ...
 template <class E, class P>
 __global__ void __launch_bounds__(1024) norm_wide_kernel(NormArgs a) {
   typedef typename E::raw raw;
@@ -316,7 +318,9 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(NormArgs a) {
   }
 }
 
-// dx of rows wider than the registers of a workgroup.
+// dx of rows wider than the registers of a workgroup, or narrower than a vector; with
+// the parameters' sums x and dy are read three times (4096 x 12296 bf16 148 us, 2.0
+// TB/s; x 12288 67 us, 4.5 TB/s).
 template <class E, class P>
 __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(NormArgs a) {
   typedef typename E::raw raw;

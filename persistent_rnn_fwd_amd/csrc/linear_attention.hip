@@ -78,9 +78,10 @@ __global__ void __launch_bounds__(256) attention_keep_kernel(const float* from, 
 // has too, it stores none (they may be written already where the state is
 // updated in place).
 //
-// Measured: 64 sequences of 32 heads of 128 x 128, 270 MB, 43 us over and over on
-// the same states (46 with plain stores, which leave the new state in caches
-// that it does not fit), 53 us with cold ones (5.0 TB/s).
+// Measured, stores past the caches (and plain ones): 64 sequences of 32 heads of 128
+// x 128, 270 MB, into another state 43 us over and over (46), 53 with cold ones
+// (57; 5.0 TB/s); in place, a replayed loop of steps, 45.3 (44.7), 8 such layers 58.6
+// each (58.8), 16 sequences 12.5 (11.7), 4 sequences or 14 heads of one the same.
 template <class E, int W, bool ODD>
 __global__ void __launch_bounds__(256) attention_step_kernel(AttnStepArgs a) {
   typedef typename E::raw raw;
