@@ -571,9 +571,9 @@ typedef struct {
    *  offsets: int32 [B + 1], device: packed sequences, b the rows offsets[b] ..
    *    offsets[b + 1] - 1 of the token axis (batch strides are not used);
    *    `rows` is the length of that axis.  Offsets are clamped to [0, rows]
-   *    and lengths to [0, T] (where they decrease, what sequences with rows in
-   *    common get is undefined); rows of the outputs that no sequence covers
-   *    are not written. */
+   *    and lengths to [0, T] (they must not decrease: where they do, what is
+   *    written to the outputs is undefined); rows of the outputs that no
+   *    sequence covers are not written. */
   const int32_t* lengths;
   const int32_t* offsets;
   int64_t rows;

@@ -588,8 +588,7 @@ class Handle:
         log_decay fp32 [H]; scale None: Dk ** -0.5.  Sequences of unequal length:
         ``lengths`` int32 [B] (rows of o past them are zeros), or packed
         sequences, the tensors [rows, heads, D], with ``offsets`` int32 [B + 1]
-        and max_len the longest sequence's tokens (None: rows, at the cost of
-        workgroups for sequences as long as that).
+        and max_len the longest sequence's tokens (None: rows, at some cost).
         initial_state (None: zeros) and final_state (written, may be the
         initial one) are fp32 [B, H, Dk, Dv]."""
         (out,), state = self._attention(q, k, v, log_decay, scale, offsets, lengths, max_len, False,

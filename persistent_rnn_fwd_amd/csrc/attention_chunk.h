@@ -424,6 +424,32 @@ struct Where {
   int initial;            // the slot of the initial state, or -1
 };
 
+// The sequence and segment of a unit (see `pieces`): the last sequence whose first
+// unit is not past it, by 64 offsets at a time.  False where there is none.  Offsets
+// that decrease give any of them.
+__device__ __forceinline__ bool find_unit(const AttnArgs& a, uint32_t unit, int& b, int& seg) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = a.B;
+  for (;;) {
+    const int step = (n + 63) >> 6, probe = lo + lane * step;
+    uint32_t own = ~0u;
+    if (lane * step < n) {
+      const int64_t first = a.offsets[probe];
+      own = divide((uint32_t)(first < 0 ? 0 : first > a.rows ? a.rows : first), a.seg_tokens, a.by_seg) + probe;
+    }
+    const uint64_t before = __ballot(own <= unit);
+    if (before == 0) return false;
+    const int last = 63 - __builtin_clzll(before);
+    lo += last * step;
+    n = min(step, n - last * step);
+    if (step == 1) {
+      b = lo;
+      seg = (int)(unit - (uint32_t)__builtin_amdgcn_readlane(own, last));
+      return true;
+    }
+  }
+}
+
 template <class E, int DKP, int NT, int WAVES>
 __device__ __forceinline__ bool where(const AttnArgs& a, const AttnJob& job, int segments, Where& w) {
   typedef typename E::raw raw;
@@ -438,14 +464,22 @@ __device__ __forceinline__ bool where(const AttnArgs& a, const AttnJob& job, int
                "s"(a.B), "s"(a.T), "s"(a.H), "s"(a.tiles), "s"(a.seg_tokens), "s"(a.by_tiles), "s"(a.by_seg), "s"(job.Dv),
                "s"(job.o.p), "s"(job.s_out), "s"(job.reverse));
   const uint32_t id = blockIdx.x, state = divide(id, a.tiles, a.by_tiles), tile = id - state * a.tiles;
-  const uint32_t states = (uint32_t)a.B * a.H, seg = divide(state, states, a.by_states), bh = state - seg * states;
   w.col0 = (int)tile * DVT;
-  w.seg = (int)seg;
-  w.b = (int)divide(bh, a.H, a.by_heads);
-  w.h = (int)bh - w.b * a.H;
   w.cols = job.Dv - w.col0;
   if (w.cols <= 0) return false;
-  w.s = span_of(a, w.b);
+  if (a.units > 0) {
+    const uint32_t unit = divide(state, a.H, a.by_heads);
+    w.h = (int)(state - unit * a.H);
+    if (!find_unit(a, unit, w.b, w.seg)) return false;
+    w.s = span_of(a, w.b);
+    if (w.seg > 0 && (int64_t)w.seg * a.seg_tokens >= w.s.len) return false;
+  } else {
+    const uint32_t states = (uint32_t)a.B * a.H, seg = divide(state, states, a.by_states), bh = state - seg * states;
+    w.seg = (int)seg;
+    w.b = (int)divide(bh, a.H, a.by_heads);
+    w.h = (int)bh - w.b * a.H;
+    w.s = span_of(a, w.b);
+  }
   w.q = static_cast<const char*>(q.p) + base_of(q, a, w.s, w.b, w.h) * (int64_t)sizeof(raw);
   w.k = static_cast<const char*>(k.p) + base_of(k, a, w.s, w.b, w.h) * (int64_t)sizeof(raw);
   w.v = static_cast<const char*>(v.p) + (base_of(v, a, w.s, w.b, w.h) + w.col0) * (int64_t)sizeof(raw);
@@ -654,7 +688,6 @@ template <int KT, int NT>
 __device__ __forceinline__ f32x4* slot_at(const Where& w, int slot, int wave, int lane) {
   return reinterpret_cast<f32x4*>(w.states + slot * w.slot) + wave * (KT * NT * 64) + lane;
 }
-constexpr int kScanFrom = 9;  // segments from which a scan between the launches costs less than every segment's own sum
 
 // The state a segment starts from.
 template <int DKP, int NT>
@@ -700,7 +733,7 @@ __device__ __forceinline__ void last_state(const f32x4 (&S)[DKP / 16][NT], const
   }
 }
 
-// The slots of every segment but the last: grid tiles x B H x (segments - 1), jobs.  The chunks
+// The slots of every segment but the last: grid tiles x H x pieces (without the last segments), jobs.  The chunks
 // are taken from a segment's last to its first, each weighted for the tokens
 // behind it: the state itself is not touched between products, and the main
 // kernel, which starts where this one ends, finds the tokens it reads first in
@@ -883,7 +916,7 @@ __device__ __forceinline__ void put_rows(const Out& x, const Where& w, const f32
     }
 }
 
-// The attention: grid tiles x B H x segments, jobs.
+// The attention: grid tiles x H x pieces, jobs.
 template <class E, int DKP, int NT, int WAVES, bool VEC>
 __global__ void __launch_bounds__(64 * WAVES, 2) attention_chunk_kernel(AttnArgs a) {
   typedef Shape<E, DKP, NT, WAVES> Sh;
@@ -1128,17 +1161,18 @@ hipError_t launch_wide(K kernel, dim3 grid, int threads, int lds, const AttnArgs
 template <class E, int DKP, int NT, int WAVES, bool VEC>
 hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
   typedef Shape<E, DKP, NT, WAVES> Sh;
-  const unsigned states = (unsigned)a.tiles * a.B * a.H;
+  const unsigned columns = (unsigned)a.tiles * a.H, states = columns * a.B;
   if (a.segments > 1) {
-    hipError_t e = launch_wide(attention_state_kernel<E, DKP, NT, WAVES, VEC>, dim3(states * (a.segments - 1), a.jobs),
-                               64 * WAVES, Sh::kLdsState, a, stream);
+    const unsigned inner = a.units > 0 ? a.units : a.B * (a.segments - 1);  // (by number: the last segments, too)
+    hipError_t e = launch_wide(attention_state_kernel<E, DKP, NT, WAVES, VEC>, dim3(columns * inner, a.jobs), 64 * WAVES,
+                               Sh::kLdsState, a, stream);
     if (e != hipSuccess) return e;
     if (a.segments >= kScanFrom) {
       e = launch_wide(attention_scan_kernel<DKP, NT, WAVES>, dim3(states * (DKP * Sh::DVT / 1024), a.jobs), 256, 0, a, stream);
       if (e != hipSuccess) return e;
     }
   }
-  const dim3 grid(states * a.segments, a.jobs);
+  const dim3 grid(columns * (unsigned)pieces(a), a.jobs);
   return launch_wide(attention_chunk_kernel<E, DKP, NT, WAVES, VEC>, grid, 64 * WAVES, Sh::kLds, a, stream);
 }
 

@@ -51,10 +51,12 @@ size_t plan_attention(AttnArgs* a, prnnDataType_t type, int compute_units) {
   const int64_t segments = want < 4 && a->T < 512 ? 1 : std::max<int64_t>(1, std::min<int64_t>(want, a->T / least));
   a->seg_tokens = std::max(64, (int)(((a->T + segments - 1) / segments + 63) / 64 * 64));
   a->segments = std::max(1, (int)(((int64_t)a->T + a->seg_tokens - 1) / a->seg_tokens));
-  // (every sequence gets the longest one's workgroups, whatever its length)
-  if (!grid_fits(*a)) {
+  a->units = 0;
+  if (a->offsets != nullptr && a->segments > 1 && pieces(*a) > 4 * units_of(*a)) a->units = (int)units_of(*a);
+  if (a->segments > 1 && !grid_fits(*a)) {
     a->segments = 1;
     a->seg_tokens = (a->T + 63) / 64 * 64;
+    a->units = 0;
   }
   a->by_tiles = inverse_of(a->tiles);
   a->by_heads = inverse_of(a->H);

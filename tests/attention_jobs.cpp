@@ -260,13 +260,16 @@ static void packed_workspace() {
         const double wide = call == 1 && s.H != s.Hkv ? 4.0 * s.rows * s.H * s.D * 2 + 512 : 0;
         CHECK(workspace - wide <= 8 * operands + 4096, "%d sequences of %lld rows: workspace of %zu bytes for %.0f", s.B,
               (long long)s.rows, workspace, operands);
-        CHECK((int64_t)args.tiles * s.B * s.H * args.segments < 1ll << 24, "%d sequences: %d segments", s.B, args.segments);
+        CHECK((int64_t)args.tiles * s.H * prnn::pieces(args) < 1ll << 24, "%d sequences: %d segments", s.B, args.segments);
         if (args.segments == 1) continue;
+        // workgroups for a small multiple of the segments there can be
+        CHECK(prnn::pieces(args) <= 4 * (s.rows / args.seg_tokens + s.B), "%d sequences: %lld pieces of %lld rows in segments of %d",
+              s.B, (long long)prnn::pieces(args), (long long)s.rows, args.seg_tokens);
         // slots of sequences of any lengths that add up to the rows: apart, and inside
         for (int pattern = 0; pattern < 4; ++pattern)
           for (int i = 0; i < args.jobs; ++i) {
             const prnn::AttnJob& job = args.job[i];
-            int64_t first = 0, next = 0;
+            int64_t first = 0, next = 0, next_unit = 0;
             uint32_t seed = 1;
             for (int b = 0; b < s.B; ++b) {
               seed = seed * 1664525u + 1013904223u;
@@ -280,6 +283,12 @@ static void packed_workspace() {
               CHECK(used == 0 || (at >= next && at + used <= prnn::slots(args)), "slots %lld + %lld of sequence %d",
                     (long long)at, (long long)used, b);
               if (used > 0) next = at + used;
+              // found by their number, every segment has one of its own
+              if (args.units > 0 && i == 0) {
+                const int64_t unit = first / args.seg_tokens + b;
+                CHECK(unit >= next_unit && unit + std::max<int64_t>(count, 1) <= args.units, "sequence %d", b);
+                next_unit = unit + std::max<int64_t>(count, 1);
+              }
               first += len;
             }
           }
