@@ -558,7 +558,8 @@ prnnStatus_t prnn_debug_jitter(prnnHandle_t handle, uint32_t seed, int span);
  * later token, whatever that holds (infinities and NaN included). */
 typedef struct {
   int B;                    /* sequences                                        */
-  int T;                    /* tokens of the longest sequence (packed: or any number above, `rows` counts then) */
+  int T;                    /* tokens of the longest sequence (packed: more count
+                               as `rows`)                                       */
   int H, Hkv;               /* heads; key-value heads, H a multiple of Hkv      */
   int Dk, Dv;               /* head sizes, 1 .. PRNN_ATTENTION_MAX_D            */
   prnnDataType_t type;      /* of q, k, v, o and their gradients                */
