@@ -57,7 +57,7 @@
  *    outside the fp16 range where a path needs it) is sticky: the failing
  *    kernel marks a host-visible copy of the handle's status (pinned host
  *    memory), and the next call on the handle that enqueues work (forward,
- *    layer, stack, projection, floor, linear attention or layer norm),
+ *    layer, stack, projection, floor, linear attention, gated delta rule or norm),
  *    prnn_synchronize() or prnn_destroy(), whichever comes first, returns
  *    PRNN_STATUS_EXECUTION_FAILED without waiting for the GPU; that call
  *    enqueues nothing.  The failure is
@@ -65,11 +65,12 @@
  *    reset before the next launch).  Calls enqueued after the failing one but
  *    before the failure reached the host (made while it was still running)
  *    return SUCCESS and do nothing: their kernels see the failure at entry and
- *    leave H as it was (linear attention and layer norm, which cannot fail in
- *    this way, run as ever).  A call that enqueues several launches (layer and
+ *    leave H as it was (linear attention, the gated delta rule and the norms,
+ *    which cannot fail in this way, run as ever).  A call that enqueues several launches (layer and
  *    stack calls) and fails after the first leaves its outputs undefined.
  *  - One forward call may be in flight per handle at a time (the handle owns
- *    the exchange ring, and the workspace of linear attention and layer norm).
+ *    the exchange ring, and the workspace of linear attention, the gated delta
+ *    rule and the norms).
  *    Use one handle per concurrently used stream.  A handle is not
  *    thread-safe.  Every call must be made with the handle's device current.
  *  - No C++ exception crosses this interface.
@@ -99,7 +100,8 @@ typedef enum {
 typedef enum {
   PRNN_DATA_FLOAT = 0, /* fp32 */
   PRNN_DATA_HALF = 1,  /* fp16 (IEEE binary16); products and sums are taken in fp32 */
-  PRNN_DATA_BFLOAT = 2, /* bfloat16: linear attention and layer norm only (BAD_PARAM elsewhere) */
+  PRNN_DATA_BFLOAT = 2, /* bfloat16: linear attention, the gated delta rule and norms only (BAD_PARAM elsewhere) */
+  PRNN_DATA_E4M3 = 3,   /* OCP 8-bit float, 4 exponent and 3 mantissa bits: the output of rms norm only */
   PRNN_DATA_MAX_ENUM = 0x7FFFFFFF  /* not a value: keeps every int in the type's range */
 } prnnDataType_t;
 
@@ -666,6 +668,121 @@ prnnStatus_t prnn_layer_norm_backward(prnnHandle_t handle, int64_t M, int N, prn
                                       int64_t lddy, const void* x, int64_t ldx, const float* mean, const float* rstd,
                                       prnnDataType_t param_type, const void* weight, void* dx, int64_t lddx,
                                       void* dweight, void* dbias, hipStream_t stream);
+
+/* The gated delta rule: linear attention whose state is corrected.  Each token
+ * takes out what the decayed state already holds for its key, by the share
+ * beta:
+ *
+ *     Sd = exp(log_decay[t]) S[t-1],   S[-1] = S0 or zeros
+ *     S[t] = Sd + beta[t] k[t] (v[t] - Sd^T k[t])^T
+ *     o[t] = scale * S[t]^T q[t]
+ *
+ * log_decay and beta are fp32 values for every token and head (log_decay may be
+ * absent: no decay; minus infinity forgets everything before the token).  Head
+ * h of v, o, log_decay, beta and the state uses head h / (H / Hk) of q and k.
+ * Keys of unit length and 0 <= beta <= 2 keep the state bounded; any values are
+ * taken as they are.  States are fp32 and dense, [B][H][Dk][Dv]; sums, states
+ * and all that lies between the products are fp32 for every type.  A row of o
+ * depends on no later token, whatever that holds (infinities and NaN included);
+ * from a value that is not finite on, the columns of the state that it reaches
+ * are not finite either (infinite or NaN).  */
+typedef struct {
+  int B;                    /* sequences                                        */
+  int T;                    /* tokens of the longest sequence (packed: more count
+                               as `rows`)                                       */
+  int H, Hk;                /* heads; heads of q and k, H a multiple of Hk      */
+  int Dk, Dv;               /* head sizes, 1 .. PRNN_ATTENTION_MAX_D            */
+  prnnDataType_t type;      /* of q, k, v, o and their gradients                */
+  float scale;
+  const int32_t* lengths;   /* sequences of unequal length: as in               */
+  const int32_t* offsets;   /* prnnAttention_t                                  */
+  int64_t rows;
+} prnnDeltaRule_t;
+
+/* The whole of a prompt, in chunks of tokens on the matrix cores.  log_decay
+ * (or NULL) and beta: one fp32 element a token and head, at data[t * token + b *
+ * batch + head * head].  S0: initial states or NULL; S1: receives the states
+ * after each sequence's last token, or NULL; S1 may be S0.  A sequence of no
+ * tokens leaves S1 = S0 (zeros).  The handle keeps the workspace (about 13 KiB
+ * for every 32 tokens of a head, and for long sequences of few heads their
+ * segments' states; grown outside stream capture: NOT_SUPPORTED where it would
+ * have to grow while capturing).
+ * BAD_PARAM: as prnn_linear_attention, with Hk in the place of Hkv and the
+ * buffers of this call.  NOT_SUPPORTED: a token stride above 2^23 elements; a
+ * sequence above 2^31 - 2^17 tokens, or 2^31 - 1 rows; more workgroups than a
+ * grid holds.  B == 0 does nothing; T == 0 only passes the states on. */
+prnnStatus_t prnn_gated_delta_rule(prnnHandle_t handle, const prnnDeltaRule_t* rule, const prnnSequence_t* q,
+                                   const prnnSequence_t* k, const prnnSequence_t* v, const prnnSequence_t* log_decay,
+                                   const prnnSequence_t* beta, const float* S0, const prnnSequence_t* o, float* S1,
+                                   hipStream_t stream);
+
+/* Gradients of prnn_gated_delta_rule: do_ the gradient of o, dS1 that of S1 (or
+ * NULL), the inputs as they were; writes dq and dk [..][Hk][Dk] (sums over a
+ * shared head's group, added in fp32 in a fixed order), dv [..][H][Dv],
+ * dlog_decay (or NULL) and dbeta [..][H] and, unless NULL, dS0 (which may be
+ * dS1).  Without S0 the first token's decay acts on nothing: its gradient is 0.
+ * The workspace also holds the states of every chunk and their gradients (8 Dk
+ * Dv bytes for 32 tokens of a head), x and w (8 Dv bytes a token and head) and,
+ * for shared heads, every head's dq and dk in fp32.  A value that is not finite
+ * may make every gradient of its sequence and head NaN.  Errors as
+ * prnn_gated_delta_rule. */
+prnnStatus_t prnn_gated_delta_rule_backward(prnnHandle_t handle, const prnnDeltaRule_t* rule, const prnnSequence_t* q,
+                                            const prnnSequence_t* k, const prnnSequence_t* v,
+                                            const prnnSequence_t* log_decay, const prnnSequence_t* beta,
+                                            const float* S0, const prnnSequence_t* do_, const float* dS1,
+                                            const prnnSequence_t* dq, const prnnSequence_t* dk,
+                                            const prnnSequence_t* dv, const prnnSequence_t* dlog_decay,
+                                            const prnnSequence_t* dbeta, float* dS0, hipStream_t stream);
+
+/* One new token of every sequence.  T, lengths, offsets, rows and the token
+ * strides are not used.  S1 may be S0 (the usual form: the state is updated in
+ * place).  Errors as prnn_gated_delta_rule; S0 and S1 must not be NULL. */
+prnnStatus_t prnn_gated_delta_rule_step(prnnHandle_t handle, const prnnDeltaRule_t* rule, const prnnSequence_t* q,
+                                        const prnnSequence_t* k, const prnnSequence_t* v,
+                                        const prnnSequence_t* log_decay, const prnnSequence_t* beta, const float* S0,
+                                        const prnnSequence_t* o, float* S1, hipStream_t stream);
+
+/* Rms norm over the last axis of M rows of N, with the residual's addition:
+ *
+ *     s[m][n] = x[m][n] + residual[m][n]
+ *     y[m][n] = s[m][n] * rstd[m] * weight[n],   rstd[m] = 1 / sqrt(mean_n(s[m][n]^2) + eps)
+ *
+ * x, residual (or NULL: zeros) and sum (or NULL: not wanted) of `type`, rows ldx,
+ * ldr and lds elements apart (>= N); weight [N] of `param_type` (PRNN_DATA_FLOAT
+ * or `type`) or NULL (ones); rstd [M] fp32, or NULL.  s is fp32 throughout and
+ * rounded where it is stored; sums are fp32.  y_type `type`: y in that type,
+ * scales NULL and group 0.  y_type PRNN_DATA_E4M3: 8 bits with scales,
+ *
+ *     scale = max(max |y| / 448, 2^-126),   y / scale rounded to e4m3
+ *
+ * over each row (group 0, scales [M]) or each 128 columns of it, the last fewer
+ * (group 128, scales [M][ceil(N / 128)]); NaN in y stays NaN and does not count
+ * for its scale.  sum may be x or residual, and so may a y of `type` (same ld, in
+ * place), but not both the same.
+ * BAD_PARAM: NULL handle, x or y (M > 0); M < 0, N < 1, ld < N; eps < 0 or NaN;
+ * unknown or unsupported types or group; scales NULL with E4M3 or given without;
+ * misaligned pointers; an output overlapping an input (unless in place) or
+ * another output.  NOT_SUPPORTED: M above 2^31 - 1, N above 2^31 - 1024.
+ * M == 0 does nothing. */
+prnnStatus_t prnn_rms_norm(prnnHandle_t handle, int64_t M, int N, prnnDataType_t type, const void* x, int64_t ldx,
+                           const void* residual, int64_t ldr, prnnDataType_t param_type, const void* weight, float eps,
+                           void* sum, int64_t lds, prnnDataType_t y_type, void* y, int64_t ldy, float* scales,
+                           int group, float* rstd, hipStream_t stream);
+
+/* Gradients of prnn_rms_norm, x being the sum s that it stored (or its x, without
+ * a residual) and rstd what it left, with n = x rstd and g = dy weight:
+ *
+ *     dx = rstd (g - n mean_n(g n)) + dsum,   dweight = sum_m dy n
+ *
+ * dsum (or NULL: zeros) is the gradient that reaches the sum itself.  dx, the
+ * gradient of x and of the residual, may be dy, x or dsum (same ld), or NULL;
+ * dweight [N] of param_type, or NULL; weight NULL means ones.  The sums over the
+ * rows are fp32 in a fixed order (partial sums in the handle's workspace).
+ * M == 0 writes zeros to dweight.  Errors as prnn_rms_norm, for these buffers. */
+prnnStatus_t prnn_rms_norm_backward(prnnHandle_t handle, int64_t M, int N, prnnDataType_t type, const void* dy,
+                                    int64_t lddy, const void* x, int64_t ldx, const float* rstd,
+                                    prnnDataType_t param_type, const void* weight, const void* dsum, int64_t ldds,
+                                    void* dx, int64_t lddx, void* dweight, hipStream_t stream);
 
 /* For callers that cannot allocate device memory: code under HIP graph
  * capture, tight serving loops, harnesses that forbid allocation.

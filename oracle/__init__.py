@@ -34,3 +34,10 @@ from .sequence import (  # noqa: F401
     linear_attention,
     linear_attention_backward,
 )
+from .delta import (  # noqa: F401
+    e4m3_values,
+    gated_delta_rule,
+    gated_delta_rule_backward,
+    rms_norm,
+    rms_norm_backward,
+)

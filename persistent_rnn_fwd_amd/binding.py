@@ -26,7 +26,7 @@ STATUS_NAMES = {
     5: "PRNN_STATUS_INTERNAL_ERROR",
 }
 SUCCESS, BAD_PARAM, NOT_SUPPORTED, ALLOC_FAILED, EXECUTION_FAILED, INTERNAL_ERROR = range(6)
-DATA_FLOAT, DATA_HALF, DATA_BFLOAT = 0, 1, 2
+DATA_FLOAT, DATA_HALF, DATA_BFLOAT, DATA_E4M3 = 0, 1, 2, 3
 EXCHANGE_AUTO, EXCHANGE_DIRECT, EXCHANGE_RELAY = 0, 1, 2
 LAYOUT_AUTO, LAYOUT_SPREAD, LAYOUT_TEAM = 0, 1, 2
 MATH_AUTO, MATH_EXACT, MATH_SPLIT, MATH_HALF = 0, 1, 2, 3
@@ -73,15 +73,22 @@ SIGNATURES = {
     "prnn_linear_attention_step": (_I, [_H, _P, _P, _P, _P, _P, _P, _P, _P]),
     "prnn_layer_norm": (_I, [_H, _L, _I, _I, _P, _L, _I, _P, _P, ctypes.c_float, _P, _L, _P, _P, _P]),
     "prnn_layer_norm_backward": (_I, [_H, _L, _I, _I, _P, _L, _P, _L, _P, _P, _I, _P, _P, _L, _P, _P, _P]),
+    "prnn_gated_delta_rule": (_I, [_H, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "prnn_gated_delta_rule_backward": (_I, [_H, *[_P] * 16]),
+    "prnn_gated_delta_rule_step": (_I, [_H, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "prnn_rms_norm": (_I, [_H, _L, _I, _I, _P, _L, _P, _L, _I, _P, ctypes.c_float, _P, _L, _I, _P, _L, _P, _I, _P, _P]),
+    "prnn_rms_norm_backward": (_I, [_H, _L, _I, _I, _P, _L, _P, _L, _P, _I, _P, _P, _L, _P, _L, _P, _P]),
 }
 
 ATTENTION_MAX_D = 256  # PRNN_ATTENTION_MAX_D
 SEQUENCE_TYPES = {torch.float32: DATA_FLOAT, torch.float16: DATA_HALF, torch.bfloat16: DATA_BFLOAT}
 
 
-# prnnAttention_t, and prnnSequence_t: data, token, batch, head
+# prnnAttention_t, prnnDeltaRule_t, and prnnSequence_t: data, token, batch, head
 _ATTENTION = struct.Struct("@7if3Pq")
+_DELTA_RULE = struct.Struct("@7if2Pq")
 _SEQUENCE = struct.Struct("@P3q")
+RMS_GROUP = 128  # columns that share a scale of rms_norm_e4m3's groups
 
 
 class PlanInfo(ctypes.Structure):
@@ -195,9 +202,9 @@ class Handle:
         self._h = h
         self.device = torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
-        # descriptors of one call (an attention and up to 7 sequences); the
-        # library reads them before it returns
-        self._desc = ctypes.create_string_buffer(_ATTENTION.size + 7 * _SEQUENCE.size)
+        # descriptors of one call (an attention and up to 7 sequences, or a delta
+        # rule and up to 11); the library reads them before it returns
+        self._desc = ctypes.create_string_buffer(_ATTENTION.size + 11 * _SEQUENCE.size)
         self._desc_at = ctypes.addressof(self._desc)
 
     # -- lifetime ---------------------------------------------------------
@@ -643,6 +650,147 @@ class Handle:
             self._h, a, s, s + 32, s + 64, s0, s + 96, s1, self._stream(stream)))
         return out
 
+    # -- the gated delta rule -----------------------------------------------
+    def _delta_rule(self, q, k, v, log_decay, beta, scale, offsets, lengths, max_len, step, more):
+        """As _attention: writes the descriptors of the rule, of q, k, v, log_decay
+        and beta and of the sequences in `more`, and returns those tensors, the
+        shape of the states and whether there is a log_decay."""
+        lead = 1 if step or offsets is not None else 2
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor) or t.dim() != lead + 2:
+                raise ValueError(f"{name} must have {lead + 2} axes")
+        if not isinstance(beta, torch.Tensor):
+            raise TypeError("beta must be a torch tensor")
+        dtype = q.dtype
+        code = SEQUENCE_TYPES.get(dtype)
+        if code is None:
+            raise TypeError(f"q must have dtype in {tuple(SEQUENCE_TYPES)}, got {dtype}")
+        *rows, Hk, Dk = q.shape
+        H, Dv = v.shape[-2:]
+        rows = tuple(rows)
+        total, at_lengths, at_offsets = 0, None, None
+        if step:
+            B, T, axes = rows[0], 1, (None, 0)
+        elif offsets is not None:
+            if lengths is not None:
+                raise ValueError("give offsets (packed sequences) or lengths, not both")
+            if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
+                raise ValueError("offsets must be [B + 1]")
+            B, total, axes = offsets.shape[0] - 1, rows[0], (0, None)
+            T = total if max_len is None else max(-1, min(int(max_len), total))  # (longer than the rows: as long)
+            at_offsets = self._dense(offsets, "offsets", torch.int32, (B + 1,))
+        else:
+            (T, B), axes = rows, (0, 1)
+            if lengths is not None:
+                at_lengths = self._dense(lengths, "lengths", torch.int32, (B,))
+        _DELTA_RULE.pack_into(self._desc, 0, B, min(T, 0x7fffffff), H, Hk, Dk, Dv, code, Dk ** -0.5 if scale is None else scale,
+                              at_lengths or 0, at_offsets or 0, total)
+        at = _DELTA_RULE.size
+        outs = []
+        token, batch = axes
+        shapes = {"H": H, "Hk": Hk, "Dk": Dk, "Dv": Dv}
+        for t, name, heads, size, stream in (
+                (q, "q", "Hk", "Dk", 0), (k, "k", "Hk", "Dk", 0), (v, "v", "H", "Dv", 0),
+                (log_decay, "log_decay", "H", None, -1), (beta, "beta", "H", None, 0), *more):
+            scalar = size is None
+            shape = (*rows, shapes[heads]) if scalar else (*rows, shapes[heads], shapes[size])
+            if t is None and stream == -1:  # (absent)
+                outs.append(None)
+                at += _SEQUENCE.size
+                continue
+            if t is None:
+                t = _empty(q, shape, torch.float32 if scalar else dtype, stream)
+                strides = t.stride()
+            elif scalar:
+                # (one value a token and head: any strides)
+                if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != shape
+                        or t.get_device() != self._index):
+                    _need_strided(t, name, self.device, (torch.float32,), shape)
+                strides = t.stride()
+            else:
+                strides = self._strided(t, name, dtype, shape)
+            heads_at = -1 if scalar else -2
+            _SEQUENCE.pack_into(self._desc, at, t.data_ptr(),
+                                strides[token] if token is not None and shape[token] > 1 else 0,
+                                strides[batch] if batch is not None and shape[batch] > 1 else 0,
+                                strides[heads_at] if shape[heads_at] > 1 else 0)
+            at += _SEQUENCE.size
+            outs.append(t)
+        return outs[5:], (B, H, Dk, Dv), log_decay is not None
+
+    def gated_delta_rule(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: Optional[torch.Tensor],
+                         beta: torch.Tensor, *, scale: Optional[float] = None,
+                         initial_state: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+                         offsets: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                         max_len: Optional[int] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Sd = exp(log_decay[t]) S[t-1], S[t] = Sd + beta[t] k[t] (v[t] - Sd^T k[t])^T, o[t] = scale S[t]^T q[t] for
+        whole sequences.
+
+        q and k [T, B, Hk, Dk], v [T, B, H, Dv] (fp32, fp16 or bf16; any strides
+        with a contiguous last axis), log_decay (or None: no decay) and beta
+        fp32 [T, B, H] (any strides) give o [T, B, H, Dv]; scale None: Dk **
+        -0.5.  Sequences of unequal length (offsets, lengths, max_len) and states
+        fp32 [B, H, Dk, Dv] as in linear_attention."""
+        (out,), state, decays = self._delta_rule(q, k, v, log_decay, beta, scale, offsets, lengths, max_len, False,
+                                                 ((out, "out", "H", "Dv", stream),))
+        a = self._desc_at
+        s = a + _DELTA_RULE.size
+        _check("prnn_gated_delta_rule", self._lib.prnn_gated_delta_rule(
+            self._h, a, s, s + 32, s + 64, s + 96 if decays else None, s + 128,
+            self._state(initial_state, "initial_state", state), s + 160,
+            self._state(final_state, "final_state", state), self._stream(stream)))
+        return out
+
+    def gated_delta_rule_backward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                  log_decay: Optional[torch.Tensor], beta: torch.Tensor, grad_out: torch.Tensor, *,
+                                  scale: Optional[float] = None, initial_state: Optional[torch.Tensor] = None,
+                                  grad_final_state: Optional[torch.Tensor] = None,
+                                  grad_initial_state: Optional[torch.Tensor] = None,
+                                  offsets: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                                  max_len: Optional[int] = None, grad_q: Optional[torch.Tensor] = None,
+                                  grad_k: Optional[torch.Tensor] = None, grad_v: Optional[torch.Tensor] = None,
+                                  grad_log_decay: Optional[torch.Tensor] = None,
+                                  grad_beta: Optional[torch.Tensor] = None, stream=None):
+        """Gradients of gated_delta_rule: (dq, dk, dv, dlog_decay, dbeta), and into
+        grad_initial_state where it is given.  The inputs are those of the
+        forward call; dlog_decay is None without a log_decay (unless
+        grad_log_decay is given)."""
+        if grad_out is None:
+            raise TypeError("grad_out must be a torch tensor")
+        (_, *grads), state, decays = self._delta_rule(
+            q, k, v, log_decay, beta, scale, offsets, lengths, max_len, False,
+            ((grad_out, "grad_out", "H", "Dv", None), (grad_q, "grad_q", "Hk", "Dk", stream),
+             (grad_k, "grad_k", "Hk", "Dk", stream), (grad_v, "grad_v", "H", "Dv", stream),
+             (grad_log_decay, "grad_log_decay", "H", None, stream if log_decay is not None else -1),
+             (grad_beta, "grad_beta", "H", None, stream)))
+        a = self._desc_at
+        s = a + _DELTA_RULE.size
+        _check("prnn_gated_delta_rule_backward", self._lib.prnn_gated_delta_rule_backward(
+            self._h, a, s, s + 32, s + 64, s + 96 if decays else None, s + 128,
+            self._state(initial_state, "initial_state", state), s + 160,
+            self._state(grad_final_state, "grad_final_state", state), s + 192, s + 224, s + 256,
+            s + 288 if grads[3] is not None else None, s + 320,
+            self._state(grad_initial_state, "grad_initial_state", state), self._stream(stream)))
+        return tuple(grads)
+
+    def gated_delta_rule_step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              log_decay: Optional[torch.Tensor], beta: torch.Tensor, state: torch.Tensor, *,
+                              scale: Optional[float] = None, new_state: Optional[torch.Tensor] = None,
+                              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """One new token of every sequence: q and k [B, Hk, Dk], v [B, H, Dv],
+        log_decay (or None) and beta [B, H] give o [B, H, Dv].  state fp32 [B, H,
+        Dk, Dv] is updated in place, or left as it is and the new one written
+        to new_state."""
+        (out,), shape, decays = self._delta_rule(q, k, v, log_decay, beta, scale, None, None, None, True,
+                                                 ((out, "out", "H", "Dv", stream),))
+        a = self._desc_at
+        s = a + _DELTA_RULE.size
+        s0 = self._dense(state, "state", torch.float32, shape)
+        s1 = s0 if new_state is None else self._dense(new_state, "new_state", torch.float32, shape)
+        _check("prnn_gated_delta_rule_step", self._lib.prnn_gated_delta_rule_step(
+            self._h, a, s, s + 32, s + 64, s + 96 if decays else None, s + 128, s0, s + 160, s1, self._stream(stream)))
+        return out
+
     # -- layer norm -------------------------------------------------------------
     def _norm_rows(self, t, name, dtype, shape):
         """The rows of t [..., N]: how many, and the elements from one to the next."""
@@ -726,6 +874,84 @@ class Handle:
             self._h, M, N, code, grad_out.data_ptr(), lddy, x.data_ptr(), ldx, m, r, pcode, w, grad_x.data_ptr(), lddx,
             dw, db, self._stream(stream)))
         return grad_x, grad_weight, grad_bias
+
+    # -- rms norm ---------------------------------------------------------------
+    def _rms_norm(self, x, weight, eps, residual, sum_out, rstd, out_type, out_code, out, scales, group, stream):
+        code, shape = self._norm_type(x), x.shape
+        M, ldx = self._norm_rows(x, "x", x.dtype, shape)
+        (w,), pcode = self._norm_params(((weight, "weight"),), x.dtype, shape[-1])
+        ldr = lds = 0
+        if residual is not None:
+            _, ldr = self._norm_rows(residual, "residual", x.dtype, shape)
+        if sum_out is not None:
+            _, lds = self._norm_rows(sum_out, "sum_out", x.dtype, shape)
+        r = None if rstd is None else self._dense(rstd, "rstd", torch.float32, shape[:-1])
+        if out is None:
+            out = _empty(x, shape, out_type, stream)
+            ldy = shape[-1]
+        else:
+            _, ldy = self._norm_rows(out, "out", out_type, shape)
+        _check("prnn_rms_norm", self._lib.prnn_rms_norm(
+            self._h, M, shape[-1], code, x.data_ptr(), ldx, _ptr(residual), ldr, pcode, w, eps, _ptr(sum_out), lds,
+            out_code if out_code is not None else code, out.data_ptr(), ldy, _ptr(scales), group, r, self._stream(stream)))
+        return out
+
+    def rms_norm(self, x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
+                 residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """s * rstd * weight with s = x + residual over the last axis of x (fp32, fp16
+        or bf16); weight [N], fp32 or x's dtype, or None.  sum_out (of x's shape
+        and dtype; may be x or residual) receives s, rstd (fp32, x's shape
+        without its last axis) is written for the backward pass; out may be x
+        or residual."""
+        return self._rms_norm(x, weight, eps, residual, sum_out, rstd, x.dtype if isinstance(x, torch.Tensor) else None,
+                              None, out, None, 0, stream)
+
+    def rms_norm_e4m3(self, x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
+                      residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                      group: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                      scales: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None, stream=None):
+        """rms_norm with an output in 8 bits: (out, scales), out torch.float8_e4m3fn
+        of x's shape, to be multiplied by scales fp32, one for each row (x's
+        shape without its last axis) or, with group=128, for each 128 columns (x's
+        leading axes, then ceil(N / 128))."""
+        if group not in (None, RMS_GROUP):
+            raise ValueError(f"group must be None or {RMS_GROUP}, got {group}")
+        self._norm_type(x)
+        shape = x.shape[:-1] if group is None else (*x.shape[:-1], -(-x.shape[-1] // RMS_GROUP))
+        if scales is None:
+            scales = _empty(x, shape, torch.float32, stream)
+        self._dense(scales, "scales", torch.float32, shape)
+        return self._rms_norm(x, weight, eps, residual, sum_out, rstd, torch.float8_e4m3fn, DATA_E4M3, out, scales,
+                              group or 0, stream), scales
+
+    def rms_norm_backward(self, grad_out: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor,
+                          weight: Optional[torch.Tensor] = None, *, grad_sum: Optional[torch.Tensor] = None,
+                          grad_x: Optional[torch.Tensor] = None, grad_weight: Optional[torch.Tensor] = None,
+                          stream=None):
+        """Gradients of rms_norm: (dx, dweight).  x is the sum that it stored (its x,
+        without a residual), grad_sum the gradient that reaches that sum itself;
+        dx is the gradient of x and of the residual.  dweight has weight's
+        dtype; without a weight it is computed only into the buffer given, and
+        is None otherwise."""
+        code, shape = self._norm_type(x), x.shape
+        N = shape[-1]
+        M, ldx = self._norm_rows(x, "x", x.dtype, shape)
+        _, lddy = self._norm_rows(grad_out, "grad_out", x.dtype, shape)
+        ldds = self._norm_rows(grad_sum, "grad_sum", x.dtype, shape)[1] if grad_sum is not None else 0
+        r = self._dense(rstd, "rstd", torch.float32, shape[:-1])
+        if weight is not None and grad_weight is None:
+            grad_weight = _empty(x, (N,), weight.dtype, stream)
+        (w, dw), pcode = self._norm_params(((weight, "weight"), (grad_weight, "grad_weight")), x.dtype, N)
+        if grad_x is None:
+            grad_x = _empty(x, shape, x.dtype, stream)
+            lddx = N
+        else:
+            _, lddx = self._norm_rows(grad_x, "grad_x", x.dtype, shape)
+        _check("prnn_rms_norm_backward", self._lib.prnn_rms_norm_backward(
+            self._h, M, N, code, grad_out.data_ptr(), lddy, x.data_ptr(), ldx, r, pcode, w, _ptr(grad_sum), ldds,
+            grad_x.data_ptr(), lddx, dw, self._stream(stream)))
+        return grad_x, grad_weight
 
     def sync_floor(self, N: int, B: int, T: int, out: Optional[torch.Tensor] = None,
                    stream=None) -> torch.Tensor:

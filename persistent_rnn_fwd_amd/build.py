@@ -20,8 +20,9 @@ LIB = os.path.join(PKG, "libprnn.so")
 RESOURCES = os.path.join(BUILD, "kernel_resources.json")  # per-kernel registers, scratch, LDS, occupancy
 SOURCES = ["dense_f16.hip", "dense_f32.hip", "sparse_f16.hip", "sparse_f32.hip", "team_f16.hip", "team_f32.hip", "team_half.hip",
            "team_split.hip", "team_rows.hip", "project.hip", "stack.hip", "noalloc.hip", "linear_attention.hip",
-           "attention_f32.hip", "attention_f16.hip", "attention_bf16.hip", "layer_norm.hip", "prnn.cpp", "sequence.cpp",
-           "attention_plan.cpp"]
+           "attention_f32.hip", "attention_f16.hip", "attention_bf16.hip", "layer_norm.hip", "delta_rule.hip", "delta_f32.hip",
+           "delta_f16.hip", "delta_bf16.hip", "rms_norm.hip", "prnn.cpp", "sequence.cpp", "attention_plan.cpp",
+           "delta_calls.cpp", "rms_calls.cpp"]
 
 # -packed-fp32-ops: no v_pk_{add,mul,fma}_f32 in device code.
 FLAGS = [

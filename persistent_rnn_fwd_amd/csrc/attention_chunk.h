@@ -427,7 +427,8 @@ struct Where {
 // The sequence and segment of a unit (see `pieces`): the last sequence whose first
 // unit is not past it, by 64 offsets at a time.  False where there is none.  Offsets
 // that decrease give any of them.
-__device__ __forceinline__ bool find_unit(const AttnArgs& a, uint32_t unit, int& b, int& seg) {
+template <class A>
+__device__ __forceinline__ bool find_unit(const A& a, uint32_t unit, int& b, int& seg) {
   const int lane = threadIdx.x & 63;
   int lo = 0, n = a.B;
   for (;;) {

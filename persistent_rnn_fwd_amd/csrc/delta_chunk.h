@@ -1,0 +1,1189 @@
+// The gated delta rule in chunks of 32 tokens on the matrix cores.
+//
+//   S[t] = a S[t-1] + beta k (v - a S[t-1]^T k)^T,  o[t] = scale S[t]^T q,  a = exp(g[t])
+//
+// With i, j tokens of one chunk, S the state it starts from, G the sums of g
+// inside the chunk, d_ij = exp(G_i - G_j), up_i = exp(G_i), down_j = d_Cj
+// (C the chunk's last token):
+//
+//   A'_ij = d_ij (k_i.k_j) beta_j  (j < i),   T' = (I + A')^-1
+//   x = T' (v - up o (K S)),   P'_ij = scale d_ij (q_i.k_j) beta_j  (j <= i)
+//   o = scale up o (Q S) + P' x,   S <- up_C S + K^T (down beta o x)
+//
+// x_i is what token i's key finds missing of its value; beta x enters the state.
+// Nothing is divided by beta, which may be 0.  Backward, with R the gradient
+// of the state behind the chunk and dO that of o:
+//
+//   w = T'^T (P'^T dO + down beta o (K R))                        (= dv)
+//   R <- up_C R + Q^T (scale up o dO) - K^T (up o w)
+//   Y_ij = scale d_ij dO_i.x_j  (j <= i),   Z_ij = d_ij w_i.x_j  (j < i)
+//   dq = scale up o (dO S^T) + (Y beta) K,   row = -up o (w S^T) - (Z beta) K
+//   col = down o (x R^T) + Y^T Q - Z^T K,    dk = row + beta o col
+//   dbeta_i = k_i.col_i,   dG_i = q_i.dq_i + k_i.row_i - beta_i dbeta_i
+//   dg_t = up_C <R, S> + sum_j beta_j k_j.(down o x R^T)_j + sum_{i >= t} dG_i
+//
+// Launches.  T', P' and the factors depend on no state: a first launch, a wave
+// for each chunk and head, leaves them in the workspace (delta_prepare_kernel).
+// The walk along the sequence (delta_forward_kernel) has a workgroup of 4 waves
+// for 64 columns of one head's state; each wave keeps its DKP x 16 of the state
+// in registers.  The accumulators' layout (lane l: rows 4 (l / 16) + r, column l %
+// 16) is that of an operand whose rows are dealt to suit, so K S, x, o^T and the
+// state's update follow each other without a shuffle: two tiles of 16 tokens are
+// the operand whose element e of lane group g is token 16 (e / 4) + 4 g + e % 4, and
+// T' and P' are stored with their columns in that order.  The backward pass walks
+// forward for x and the states that chunks start from (kept in the workspace),
+// backwards for w and the gradients of those they end with, and a last launch, a
+// workgroup for each chunk and head, takes the gradients from these.
+//
+// Precision.  As linear attention's: operands in bf16 parts, exact (one for bf16,
+// two for fp16, three for fp32), what is fp32 between the products in three, sums
+// in fp32.  G is summed in fp64: decays of neighbouring tokens are then right
+// however far the chunk has decayed.
+//
+// Infinities and NaN.  A masked 0 times a later token's infinity is NaN, so a
+// wave whose outputs are not finite takes its columns again by the recurrence,
+// token by token (delta_tokens).  (Gradients: a value that is not finite may make
+// every gradient of its sequence and head NaN.)
+#pragma once
+
+#include "attention_chunk.h"
+#include "delta_rule.h"
+
+namespace prnn {
+namespace delta {
+
+using namespace attn;
+
+constexpr int C = kDeltaChunk;
+
+// Row and position of an element of a 32 x 32 matrix of bf16: rows of 64 bytes,
+// their 16-byte units swizzled, columns dealt as the operands' (position()).
+__host__ __device__ constexpr int delta_at(int row, int pos) {
+  return row * 64 + (((pos >> 3) ^ ((row >> 2) & 3)) << 4) + 2 * (pos & 7);
+}
+__host__ __device__ constexpr int position(int column) { return 8 * ((column & 15) >> 2) + 4 * (column >> 4) + (column & 3); }
+constexpr int kPart = 2048;  // bytes of a part of such a matrix
+
+// 16 rows from 16 t on as operands (row 16 t + l, positions 8 g .. + 7).
+template <int P>
+__device__ __forceinline__ void read_matrix(b16x8 (&x)[P], const char* m, int t, int lane) {
+  const int g = lane >> 4, l = lane & 15;
+#pragma unroll
+  for (int p = 0; p < P; ++p) x[p] = read_row(m, p * kPart + (16 * t + l) * 64 + ((g ^ (l >> 2)) << 4));
+}
+// ... and of the transpose: row 16 t + l is column 16 t + l, its elements the rows dealt as an operand's.
+template <int P>
+__device__ __forceinline__ void read_transposed(b16x8 (&x)[P], const char* m, int t, int lane) {
+  const int g = lane >> 4, l = lane & 15;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    u32x2 half[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      half[h] = read_columns(m, p * kPart + (16 * h + 4 * g + (l >> 2)) * 64 + (((l & 3) ^ g) << 4) + 8 * t);
+    const uint32_t words[4] = {half[0][0], half[0][1], half[1][0], half[1][1]};
+    x[p] = operand(words);
+  }
+}
+
+// 8 values of a row as an operand, zeros where the row or a column does not
+// exist.  row: its byte offset, or kOutside.
+template <class E, bool VEC>
+__device__ __forceinline__ void load_operand(b16x8 (&f)[Parts<E>::kIn], __amdgpu_buffer_rsrc_t r, uint32_t row, int col, int cols) {
+  typedef typename E::raw raw;
+  constexpr int IN = Parts<E>::kIn;
+  uint32_t w[IN == 3 ? 8 : 4];
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < (IN == 3 ? 2 : 1); ++i) {
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, col + 4 * i < cols ? row + (uint32_t)((col + 4 * i) * (int)sizeof(raw)) : kOutside, 0, kPlain);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[4 * i + e] = v[e];
+    }
+  } else {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t at = col + i < cols ? row + (uint32_t)((col + i) * (int)sizeof(raw)) : kOutside;
+      e[i] = sizeof(raw) == 4 ? __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, kPlain)
+                              : (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, kPlain);
+    }
+#pragma unroll
+    for (int i = 0; i < (IN == 3 ? 8 : 4); ++i) w[i] = IN == 3 ? e[i % 8] : e[2 * i % 8] | e[(2 * i + 1) % 8] << 16;
+  }
+  if constexpr (IN == 1) {
+    f[0] = operand(w);
+  } else {
+    float x[8];
+    if constexpr (IN == 2) {
+      typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+      const u32x4 v = {w[0], w[1], w[2], w[3]};
+      const f16x8 h = __builtin_bit_cast(f16x8, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = (float)h[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    }
+    uint32_t words[IN][4];
+    split<IN, 8>(x, words);
+#pragma unroll
+    for (int p = 0; p < IN; ++p) f[p] = operand(words[p]);
+  }
+}
+
+template <int P>
+__device__ __forceinline__ void split_operand(b16x8 (&f)[P], const float (&x)[8]) {
+  uint32_t words[P][4];
+  split<P, 8>(x, words);
+#pragma unroll
+  for (int p = 0; p < P; ++p) f[p] = operand(words[p]);
+}
+
+// exp of a difference of sums, its rounding to fp32 made good to first order.
+__device__ __forceinline__ float exp_sum(double d) {
+  const float x = (float)d;
+  if (x < -104.f) return 0.f;
+  const float e = expf(x);
+  return x > 89.f ? e : __builtin_fmaf(e, (float)(d - (double)x), e);
+}
+
+// A token's log decay as it is summed: minus infinity (and what else exp makes
+// 0) as a finite number, so that differences of sums stay what they are.
+__device__ __forceinline__ double summand(float g) { return g < -1e6f ? -1e6 : (double)g; }
+
+// LDS written by a wave is read by its other lanes.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// First chunk of a sequence in the workspace.
+__device__ __forceinline__ int64_t first_chunk(const DeltaArgs& a, const Span& s, int b) {
+  return a.offsets != nullptr ? s.first / C + b : (int64_t)b * a.chunks;
+}
+__device__ __forceinline__ bool chunk_of(const DeltaArgs& a, uint32_t slot, int& b, int& c) {
+  if (a.offsets != nullptr) return find_unit(a, slot, b, c);
+  b = (int)divide(slot, a.chunks, a.by_chunks);
+  c = (int)slot - b * a.chunks;
+  return true;
+}
+
+// -- what depends on no state ------------------------------------------------------------------
+
+// A wave for each chunk and head.  T' is inverted in fp32: its two diagonal blocks of 16 by
+// substitution, a column a lane, then T'_21 = -T'_22 A'_21 T'_11 on the matrix
+// cores.
+template <class E, int DKP, bool VEC, bool PAIRS>
+__global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
+  typedef typename E::raw raw;
+  constexpr int IN = Parts<E>::kIn, kRow = 36;
+  __shared__ float mem[4][2][C][kRow];
+  __shared__ double sums[4][C];
+  __shared__ float betas[4][C];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
+  const uint32_t id = blockIdx.x * 4 + wave;
+  const uint32_t slot = divide(id, a.H, a.by_heads);
+  const int h = (int)(id - slot * a.H);
+  int b, c;
+  if (slot >= (uint32_t)a.slots || !chunk_of(a, slot, b, c)) return;
+  const Span s = span_of(a, b);
+  const int n = min(C, s.len - c * C);
+  if (n <= 0) return;
+  float (&A)[C][kRow] = mem[wave][0], (&T)[C][kRow] = mem[wave][1];
+  char* const block = a.blocks + ((int64_t)slot * a.H + h) * kDeltaBlock;
+  const int64_t t0 = (int64_t)c * C;
+
+  // the decays' sums, and the factors
+  const int t = lane & 31;
+  double G = 0.;
+  float beta = 0.f;
+  if (t < n) {
+    if (a.g.p != nullptr) G = summand(static_cast<const float*>(a.g.p)[base_of(a.g, a, s, b, h) + (t0 + t) * a.g.token]);
+    beta = static_cast<const float*>(a.beta.p)[base_of(a.beta, a, s, b, h) + (t0 + t) * a.beta.token];
+  }
+#pragma unroll
+  for (int d = 1; d < C; d *= 2) {
+    const double y = __shfl_up(G, d, C);
+    if (t >= d) G += y;
+  }
+  if (lane < C) {
+    sums[wave][t] = G;
+    betas[wave][t] = beta;
+  }
+  wave_sync();
+  if (lane < C) {
+    const float up = exp_sum(G), down = exp_sum(sums[wave][C - 1] - G);
+    float* const f = reinterpret_cast<float*>(block + kDeltaVec) + t;
+    f[kUp * C] = up;
+    f[kScaledUp * C] = a.scale * up;
+    f[kInto * C] = down * beta;
+    f[kDown * C] = down;
+    f[kBeta * C] = beta;
+    reinterpret_cast<double*>(block + kDeltaSums)[t] = G;
+  }
+
+  // k k^T and q k^T as tiles (j, i): lane (g, l) has tokens j = 16 tj + 4 g + r of i = 16 ti + l
+  f32x4 kk[3], qk[3];  // (ti, tj) = (0, 0), (1, 0), (1, 1)
+#pragma unroll
+  for (int x = 0; x < 3; ++x) kk[x] = qk[x] = f32x4(0.f);
+  {
+    const uint32_t ks = (uint32_t)a.k.token * (uint32_t)sizeof(raw), qs = (uint32_t)a.q.token * (uint32_t)sizeof(raw);
+    const __amdgpu_buffer_rsrc_t rk = make_rsrc(
+        static_cast<const raw*>(a.k.p) + base_of(a.k, a, s, b, h) + t0 * a.k.token, (uint32_t)(n - 1) * ks + (uint32_t)(a.Dk * (int)sizeof(raw)));
+    const __amdgpu_buffer_rsrc_t rq = make_rsrc(
+        static_cast<const raw*>(a.q.p) + base_of(a.q, a, s, b, h) + t0 * a.q.token, (uint32_t)(n - 1) * qs + (uint32_t)(a.Dk * (int)sizeof(raw)));
+    for (int d = 0; d < a.Dk; d += 32) {
+      b16x8 K[2][IN], Q[2][IN];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int row = 16 * x + l;
+        load_operand<E, VEC>(K[x], rk, row < n ? row * ks : kOutside, d + 8 * g, a.Dk);
+        if (PAIRS) load_operand<E, VEC>(Q[x], rq, row < n ? row * qs : kOutside, d + 8 * g, a.Dk);
+      }
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        const int ti = (x + 1) / 2, tj = x / 2;
+        f32x4 y[1] = {kk[x]};
+        b16x8 Y[1][IN];
+#pragma unroll
+        for (int p = 0; p < IN; ++p) Y[0][p] = K[ti][p];
+        products<IN, IN, 1>(y, K[tj], Y);
+        kk[x] = y[0];
+        if (PAIRS) {
+          y[0] = qk[x];
+#pragma unroll
+          for (int p = 0; p < IN; ++p) Y[0][p] = Q[ti][p];
+          products<IN, IN, 1>(y, K[tj], Y);
+          qk[x] = y[0];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 3; ++x) {
+    const int ti = (x + 1) / 2, tj = x / 2, i = 16 * ti + l, j = 16 * tj + 4 * g;
+    f32x4 y;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float f = j + r <= i ? exp_sum(sums[wave][i] - sums[wave][j + r]) * betas[wave][j + r] : 0.f;
+      y[r] = j + r < i ? kk[x][r] * f : 0.f;
+      qk[x][r] = j + r <= i ? qk[x][r] * (a.scale * f) : 0.f;
+    }
+    *reinterpret_cast<f32x4*>(&A[i][j]) = y;
+  }
+  wave_sync();
+  // the diagonal blocks' inverses, column l of block g % 2
+  {
+    const int o = 16 * (g & 1);
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float y = i == l ? 1.f : 0.f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) y = __builtin_fmaf(-A[o + i][o + j], x[j], y);
+      x[i] = y;
+    }
+    if (g < 2) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) T[o + i][o + l] = x[i];
+    } else if (g == 2) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) T[i][16 + l] = 0.f;
+    }
+  }
+  wave_sync();
+  {
+    f32x4 x = f32x4(0.f);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) x = __builtin_amdgcn_mfma_f32_16x16x4f32(A[16 + l][4 * m + g], T[4 * m + g][l], x, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) A[4 * g + r][16 + l] = x[r];
+    wave_sync();
+    f32x4 y = f32x4(0.f);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) y = __builtin_amdgcn_mfma_f32_16x16x4f32(T[16 + l][16 + 4 * m + g], A[4 * m + g][16 + l], y, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) T[16 + 4 * g + r][l] = -y[r];
+  }
+  wave_sync();
+  // out in parts: a row and 16 positions a lane
+  auto put = [&](const float (&m)[C][kRow], int to) {
+    const int row = lane >> 1;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int unit = 2 * (lane & 1) + u;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = m[row][16 * (e / 4) + 4 * unit + e % 4];
+      uint32_t words[kFull][4];
+      split<kFull, 8>(x, words);
+#pragma unroll
+      for (int p = 0; p < kFull; ++p)
+        *reinterpret_cast<u32x4*>(block + to + p * kPart + delta_at(row, 8 * unit)) = u32x4{words[p][0], words[p][1], words[p][2], words[p][3]};
+    }
+  };
+  put(T, kDeltaT);
+  if constexpr (PAIRS) {
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      const int ti = (x + 1) / 2, tj = x / 2;
+      *reinterpret_cast<f32x4*>(&A[16 * ti + l][16 * tj + 4 * g]) = qk[x];
+    }
+    *reinterpret_cast<f32x4*>(&A[l][16 + 4 * g]) = f32x4(0.f);
+    wave_sync();
+    put(A, kDeltaP);
+  }
+}
+
+// -- the walk along a sequence --------------------------------------------------------------------
+
+template <class E, int DKP>
+struct Shape {
+  static constexpr int IN = Parts<E>::kIn, KT = DKP / 16, kTile = 2 * C * IN;  // bytes of a tile's column
+  static constexpr int kK = 0, kQ = kTile * DKP, kV = 2 * kTile * DKP, kM = kV + kTile * 64;
+  static constexpr int kVecs = kM + 2 * 3 * kPart, kLds = kVecs + 5 * 4 * C;
+};
+
+// What a workgroup works on: 64 columns of one head's state.
+struct Where {
+  int b, h, col0, cols;
+  Span s;
+  int chunks;
+  int64_t slot;
+};
+
+__device__ __forceinline__ bool where(const DeltaArgs& a, Where& w) {
+  const uint32_t id = blockIdx.x, state = divide(id, a.tiles, a.by_tiles);
+  w.col0 = 64 * (int)(id - state * a.tiles);
+  w.b = (int)divide(state, a.H, a.by_heads);
+  w.h = (int)(state - (uint32_t)w.b * a.H);
+  w.cols = min(64, a.Dv - w.col0);
+  w.s = span_of(a, w.b);
+  w.chunks = (w.s.len + C - 1) / C;
+  w.slot = first_chunk(a, w.s, w.b);
+  return true;
+}
+
+// A state in memory, [Dk][stride], as this lane's elements: row 32 (t / 2) + 8 g +
+// 4 (t % 2) + r of its column.
+struct StateAt {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int rows, first, step;
+  __device__ __forceinline__ StateAt(const float* p, int Dk, int stride, int col, bool exists, int lane)
+      : rsrc(make_rsrc(p, (uint32_t)(Dk * stride) * 4u)),
+        rows(exists ? Dk - 8 * (lane >> 4) : 0),
+        first(4 * (8 * (lane >> 4) * stride + col)),
+        step(4 * stride) {}
+  __device__ __forceinline__ uint32_t at(int t, int r) const {
+    const int row = 32 * (t / 2) + 4 * (t % 2) + r;
+    return row < rows ? (uint32_t)(first + row * step) : kOutside;
+  }
+};
+
+template <int KT>
+__device__ __forceinline__ void load_state(f32x4 (&S)[KT], const float* p, int Dk, int stride, int col, bool exists, int lane) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t) S[t] = f32x4(0.f);
+    return;
+  }
+  const StateAt x(p, Dk, stride, col, exists, lane);
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[t][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(x.rsrc, x.at(t, r), 0, kPlain));
+}
+template <int KT>
+__device__ __forceinline__ void store_state(const f32x4 (&S)[KT], float* p, int Dk, int stride, int col, bool exists, int lane) {
+  const StateAt x(p, Dk, stride, col, exists, lane);
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[t][r]), x.rsrc, x.at(t, r), 0, kPlain);
+}
+
+// The chunk's matrices and factors on their way from the workspace to LDS.
+struct Block {
+  u32x4 m[3], f;
+  __device__ __forceinline__ void load(const char* p) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) m[i] = reinterpret_cast<const u32x4*>(p)[i * 256 + threadIdx.x];
+    if (threadIdx.x < 5 * C / 4) f = reinterpret_cast<const u32x4*>(p + kDeltaVec)[threadIdx.x];
+  }
+  __device__ __forceinline__ void store(char* matrices, char* vecs) const {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) reinterpret_cast<u32x4*>(matrices)[i * 256 + threadIdx.x] = m[i];
+    if (threadIdx.x < 5 * C / 4) reinterpret_cast<u32x4*>(vecs)[threadIdx.x] = f;
+  }
+};
+
+// The factors of an operand's 8 tokens.
+__device__ __forceinline__ void factors(float (&f)[8], const char* vecs, int which, int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(vecs + 4 * (which * C + 16 * h + 4 * (lane >> 4)));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) f[4 * h + r] = x[r];
+  }
+}
+
+// The wave's 16 columns of a tile of W = 64, tokens as an operand's.
+template <class E>
+__device__ __forceinline__ void read_values(b16x8 (&V)[Parts<E>::kIn], const char* v, int wave, int lane) {
+  const int g = lane >> 4, l = lane & 15;
+  const int base = (row_at<64>(4 * g + (l >> 2)) ^ ((2 * wave + ((l & 3) >> 1)) << 4)) + 8 * (l & 1);
+#pragma unroll
+  for (int p = 0; p < Parts<E>::kIn; ++p) {
+    u32x2 half[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) half[h] = read_columns(v, base + p * (C * 64 * 2) + 16 * h * (2 * 64));
+    const uint32_t words[4] = {half[0][0], half[0][1], half[1][0], half[1][1]};
+    V[p] = operand(words);
+  }
+}
+template <int P>
+__device__ __forceinline__ void values_of(float (&x)[8], const b16x8 (&V)[P]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = (float)V[P - 1][e];
+#pragma unroll
+    for (int p = P - 2; p >= 0; --p) x[e] += (float)V[p][e];
+  }
+}
+
+// Rows 16 t .. (as the state deals them) of a tile's transpose, tokens as an operand's.
+template <class E, int DKP>
+__device__ __forceinline__ void read_keys(b16x8 (&K)[Parts<E>::kIn], const char* k, int lane, int t) {
+  const int g = lane >> 4, l = lane & 15;
+  const int base = row_at<DKP>(4 * g + (l >> 2)) ^ ((l & 3) << 4);
+#pragma unroll
+  for (int p = 0; p < Parts<E>::kIn; ++p) {
+    u32x2 half[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      half[h] = read_columns(k, (base ^ (64 * (t / 2))) + p * (C * DKP * 2) + 16 * h * (2 * DKP) + 8 * (t % 2));
+    const uint32_t words[4] = {half[0][0], half[0][1], half[1][0], half[1][1]};
+    K[p] = operand(words);
+  }
+}
+
+// acc += x y for single accumulators.
+template <int NX, int NY>
+__device__ __forceinline__ void product(f32x4& acc, const b16x8 (&x)[NX], const b16x8 (&y)[NY]) {
+#pragma unroll
+  for (int s = kFull - 1; s >= 0; --s)  // small terms first
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int j = s - i;
+      if (j < 0 || j >= NY) continue;
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[j], acc, 0, 0, 0);
+    }
+}
+
+template <int P>
+__device__ __forceinline__ void state_operand(b16x8 (&A)[P], const f32x4& lo, const f32x4& hi) {
+  const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  split_operand<P>(A, x);
+}
+
+// NaN from the first value on that is not finite.
+template <int N>
+__device__ __forceinline__ void watch(float& z, const f32x4 (&x)[N]) {
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) z = __builtin_fmaf(x[t][r], 0.f, z);
+}
+
+// Four neighbouring values of a row.
+template <class E>
+__device__ __forceinline__ void put4(void* p, int64_t at, const f32x4& x, int live, bool wide, bool vec) {
+  typedef typename E::raw raw;
+  if (live <= 0) return;
+  if (wide || sizeof(raw) == 4) {
+    float* const to = static_cast<float*>(p) + at;
+    if (vec) {
+      *reinterpret_cast<f32x4*>(to) = x;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < live) to[r] = x[r];
+    }
+    return;
+  }
+  raw* const to = static_cast<raw*>(p) + at;
+  typedef raw raw4 __attribute__((ext_vector_type(4)));
+  if (vec) {
+    raw4 y;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) y[r] = E::put(x[r]);
+    *reinterpret_cast<raw4*>(to) = y;
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (r < live) to[r] = E::put(x[r]);
+  }
+}
+
+// The recurrence over a whole sequence for this wave's columns, straight from
+// memory: the rows of o, and S.  Slow; see the file comment.
+template <class E, int DKP>
+__device__ __forceinline__ void delta_tokens(const DeltaArgs& a, const Where& w, int wave, int lane, f32x4 (&S)[DKP / 16]) {
+  typedef typename E::raw raw;
+  const int first = 8 * (lane >> 4), col = 16 * wave + (lane & 15);
+  const raw* q = static_cast<const raw*>(a.q.p) + base_of(a.q, a, w.s, w.b, w.h) + first;
+  const raw* k = static_cast<const raw*>(a.k.p) + base_of(a.k, a, w.s, w.b, w.h) + first;
+  const raw* v = static_cast<const raw*>(a.v.p) + base_of(a.v, a, w.s, w.b, w.h) + w.col0;
+  raw* o = static_cast<raw*>(const_cast<void*>(a.o.p)) + base_of(a.o, a, w.s, w.b, w.h) + w.col0;
+  const float* g = a.g.p != nullptr ? static_cast<const float*>(a.g.p) + base_of(a.g, a, w.s, w.b, w.h) : nullptr;
+  const float* beta = static_cast<const float*>(a.beta.p) + base_of(a.beta, a, w.s, w.b, w.h);
+  int rows = a.Dk - first;  // rows of the state from the lane's first one on
+  keep(rows);
+#pragma nounroll
+  for (int64_t t = 0; t < w.s.len; ++t) {
+    const float d = g != nullptr ? expf(g[t * a.g.token]) : 1.f;
+    float found = 0.f, out = 0.f;
+#pragma unroll
+    for (int x = 0; x < DKP / 16; ++x)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 32 * (x / 2) + 4 * (x % 2) + r;
+        if (row < rows) {
+          S[x][r] *= d;
+          found = __builtin_fmaf(E::get(k[t * a.k.token + row]), S[x][r], found);
+        }
+      }
+    found += __shfl_xor(found, 16);
+    found += __shfl_xor(found, 32);
+    const float u = beta[t * a.beta.token] * ((col < w.cols ? E::get(v[t * a.v.token + col]) : 0.f) - found);
+#pragma unroll
+    for (int x = 0; x < DKP / 16; ++x)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 32 * (x / 2) + 4 * (x % 2) + r;
+        if (row < rows) {
+          S[x][r] = __builtin_fmaf(E::get(k[t * a.k.token + row]), u, S[x][r]);
+          out = __builtin_fmaf(E::get(q[t * a.q.token + row]), S[x][r], out);
+        }
+      }
+    out += __shfl_xor(out, 16);
+    out += __shfl_xor(out, 32);
+    if (lane < 16 && col < w.cols) o[t * a.o.token + col] = E::put(out * a.scale);
+  }
+}
+
+// Forward: grid tiles x H x B.  SAVE: x and the chunks' first states into the
+// workspace instead of o and the final state.
+template <class E, int DKP, bool VEC, bool SAVE>
+__global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(DeltaArgs a) {
+  typedef Shape<E, DKP> Sh;
+  typedef typename E::raw raw;
+  constexpr int IN = Sh::IN, KT = Sh::KT;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char *const kt = lds + Sh::kK, *const qt = lds + Sh::kQ, *const vt = lds + Sh::kV, *const mt = lds + Sh::kM,
+              *const vecs = lds + Sh::kVecs;
+  Where w;
+  if (!where(a, w)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+  const int col = 16 * wave + l;
+  if (!SAVE && a.lengths != nullptr) {  // rows of padding are zeros
+    raw* const o = static_cast<raw*>(const_cast<void*>(a.o.p)) + base_of(a.o, a, w.s, w.b, w.h) + w.col0;
+    for (int64_t t = w.s.len; t < a.T; ++t)
+      if ((int)threadIdx.x < w.cols) o[t * a.o.token + threadIdx.x] = E::put(0.f);
+  }
+  const uint32_t qs = (uint32_t)a.q.token * (uint32_t)sizeof(raw), ks = (uint32_t)a.k.token * (uint32_t)sizeof(raw),
+                 vs = (uint32_t)a.v.token * (uint32_t)sizeof(raw);
+  const raw* const q = static_cast<const raw*>(a.q.p) + base_of(a.q, a, w.s, w.b, w.h);
+  const raw* const k = static_cast<const raw*>(a.k.p) + base_of(a.k, a, w.s, w.b, w.h);
+  const raw* const v = static_cast<const raw*>(a.v.p) + base_of(a.v, a, w.s, w.b, w.h) + w.col0;
+  Rows<E, C, DKP, 256, VEC> rq(qs, a.Dk, false), rk(ks, a.Dk, false);
+  Rows<E, C, 64, 256, VEC> rv(vs, w.cols, false);
+  Block block;
+  auto fetch = [&](int c) {
+    const int n = max(0, min(C, w.s.len - c * C));
+    const int64_t t0 = n == 0 ? 0 : (int64_t)c * C;
+    rk.load(k, t0, n, ks, a.Dk, false);
+    if (!SAVE) rq.load(q, t0, n, qs, a.Dk, false);
+    rv.load(v, t0, n, vs, w.cols, false);
+    if (n > 0) block.load(a.blocks + ((w.slot + c) * a.H + w.h) * kDeltaBlock);
+  };
+  fetch(0);
+  const size_t head = (size_t)w.b * a.H + w.h;
+  const float* const s_in = a.s_in != nullptr ? a.s_in + head * a.Dk * a.Dv : nullptr;
+  const int pitch = (a.Dv + 3) & ~3;
+  f32x4 S[KT];
+  load_state<KT>(S, s_in, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+  bool broken = false;
+
+  for (int c = 0; c < w.chunks; ++c) {
+    const int n = min(C, w.s.len - c * C);
+    rk.store(kt);
+    if (!SAVE) rq.store(qt);
+    rv.store(vt);
+    block.store(mt, vecs);
+    __syncthreads();
+    fetch(c + 1);
+    const float whole = *reinterpret_cast<const float*>(vecs + 4 * (kUp * C + C - 1));
+    if constexpr (SAVE)
+      store_state<KT>(S, a.S + (((w.slot + c) * a.H + w.h) * a.Dk) * pitch, a.Dk, pitch, w.col0 + col, w.col0 + col < pitch, lane);
+
+    // K S and (Q S)^T
+    const int rows = row_at<DKP>(l) ^ (g << 4);  // row l of a tile of 16, unit g
+    f32x4 x[2], O[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) x[t] = O[t] = f32x4(0.f);
+#pragma unroll
+    for (int s = 0; s < DKP / 32; ++s) {
+      b16x8 A[kFull];
+      state_operand<kFull>(A, S[2 * s], S[2 * s + 1]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        b16x8 K[IN], Q[IN];
+#pragma unroll
+        for (int p = 0; p < IN; ++p) {
+          K[p] = read_row(kt, (rows ^ (64 * s)) + p * (C * DKP * 2) + t * (32 * DKP));
+          if (!SAVE) Q[p] = read_row(qt, (rows ^ (64 * s)) + p * (C * DKP * 2) + t * (32 * DKP));
+        }
+        product(x[t], K, A);
+        if (!SAVE) product(O[t], A, Q);
+      }
+    }
+    // x = T' (v - up K S)
+    float y[8], f[8];
+    {
+      b16x8 V[IN], Y[kFull];
+      read_values<E>(V, vt, wave, lane);
+      values_of(y, V);
+      factors(f, vecs, kUp, lane);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(-f[e], x[e / 4][e % 4], y[e]);
+      split_operand<kFull>(Y, y);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        b16x8 T[kFull];
+        read_matrix<kFull>(T, mt, t, lane);
+        x[t] = f32x4(0.f);
+        product(x[t], T, Y);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x[e / 4][e % 4];
+    if constexpr (SAVE) {
+      float* const to = a.x + (((w.slot + c) * a.H + w.h) * C) * pitch + w.col0 + col;
+      if (w.col0 + col < pitch)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to[(16 * (e / 4) + 4 * g + e % 4) * pitch] = y[e];
+    } else {
+      // o^T = scale up (Q S)^T + x^T P'^T
+      b16x8 Y[kFull];
+      split_operand<kFull>(Y, y);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        b16x8 P[kFull];
+        read_matrix<kFull>(P, mt + kDeltaP, t, lane);
+        O[t] *= *reinterpret_cast<const float*>(vecs + 4 * (kScaledUp * C + 16 * t + l));
+        product(O[t], Y, P);
+      }
+    }
+    // S = up_C S + K^T (down beta x)
+    factors(f, vecs, kInto, lane);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= f[e];
+    b16x8 D[kFull];
+    split_operand<kFull>(D, y);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      b16x8 K[IN];
+      read_keys<E, DKP>(K, kt, lane, t);
+      S[t] *= whole;
+      product(S[t], K, D);
+    }
+    if constexpr (!SAVE) {
+      float z = 0.f;
+      watch(z, O);
+      broken = broken || wave_any(z != 0.f);
+      raw* const o = static_cast<raw*>(const_cast<void*>(a.o.p));
+      const int64_t at = base_of(a.o, a, w.s, w.b, w.h) + (int64_t)c * C * a.o.token + w.col0 + 16 * wave + 4 * g;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (16 * t + l < n) put4<E>(o, at + (16 * t + l) * a.o.token, O[t], w.cols - 16 * wave - 4 * g, false, (a.vec & 2) != 0);
+    }
+    __syncthreads();
+  }
+  if constexpr (!SAVE) {
+    float z = 0.f;
+    watch(z, S);
+    if (broken || wave_any(z != 0.f)) {
+      load_state<KT>(S, s_in, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+      delta_tokens<E, DKP>(a, w, wave, lane, S);
+    }
+    if (a.s_out != nullptr) store_state<KT>(S, a.s_out + head * a.Dk * a.Dv, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+  }
+}
+
+// Backwards: grid as forward; leaves w and the gradients of the states behind
+// the chunks, and that of the initial state.
+template <class E, int DKP, bool VEC>
+__global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(DeltaArgs a) {
+  typedef Shape<E, DKP> Sh;
+  typedef typename E::raw raw;
+  constexpr int IN = Sh::IN, KT = Sh::KT;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char *const kt = lds + Sh::kK, *const qt = lds + Sh::kQ, *const vt = lds + Sh::kV, *const mt = lds + Sh::kM,
+              *const vecs = lds + Sh::kVecs;
+  Where w;
+  if (!where(a, w)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+  const int col = 16 * wave + l;
+  const uint32_t qs = (uint32_t)a.q.token * (uint32_t)sizeof(raw), ks = (uint32_t)a.k.token * (uint32_t)sizeof(raw),
+                 os = (uint32_t)a.o.token * (uint32_t)sizeof(raw);
+  const raw* const q = static_cast<const raw*>(a.q.p) + base_of(a.q, a, w.s, w.b, w.h);
+  const raw* const k = static_cast<const raw*>(a.k.p) + base_of(a.k, a, w.s, w.b, w.h);
+  const raw* const o = static_cast<const raw*>(a.o.p) + base_of(a.o, a, w.s, w.b, w.h) + w.col0;
+  Rows<E, C, DKP, 256, VEC> rq(qs, a.Dk, false), rk(ks, a.Dk, false);
+  Rows<E, C, 64, 256, VEC> ro(os, w.cols, false);
+  Block block;
+  auto fetch = [&](int c) {
+    const int n = c < 0 ? 0 : min(C, w.s.len - c * C);
+    const int64_t t0 = n <= 0 ? 0 : (int64_t)c * C;
+    rk.load(k, t0, n, ks, a.Dk, false);
+    rq.load(q, t0, n, qs, a.Dk, false);
+    ro.load(o, t0, n, os, w.cols, false);
+    if (n > 0) block.load(a.blocks + ((w.slot + c) * a.H + w.h) * kDeltaBlock);
+  };
+  fetch(w.chunks - 1);
+  const size_t head = (size_t)w.b * a.H + w.h;
+  const int pitch = (a.Dv + 3) & ~3;
+  const bool kept = w.col0 + col < pitch;
+  f32x4 R[KT];
+  load_state<KT>(R, a.ds_in != nullptr ? a.ds_in + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+
+  for (int c = w.chunks - 1; c >= 0; --c) {
+    rk.store(kt);
+    rq.store(qt);
+    ro.store(vt);
+    block.store(mt, vecs);
+    __syncthreads();
+    fetch(c - 1);
+    const float whole = *reinterpret_cast<const float*>(vecs + 4 * (kUp * C + C - 1));
+    const int64_t at = (w.slot + c) * a.H + w.h;
+    store_state<KT>(R, a.R + at * a.Dk * pitch, a.Dk, pitch, w.col0 + col, kept, lane);
+
+    // K R
+    const int rows = row_at<DKP>(l) ^ (g << 4);
+    f32x4 x[2], u[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) x[t] = u[t] = f32x4(0.f);
+#pragma unroll
+    for (int s = 0; s < DKP / 32; ++s) {
+      b16x8 A[kFull];
+      state_operand<kFull>(A, R[2 * s], R[2 * s + 1]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        b16x8 K[IN];
+#pragma unroll
+        for (int p = 0; p < IN; ++p) K[p] = read_row(kt, (rows ^ (64 * s)) + p * (C * DKP * 2) + t * (32 * DKP));
+        product(x[t], K, A);
+      }
+    }
+    // w = T'^T (P'^T dO + down beta K R)
+    float y[8], f[8];
+    b16x8 D[IN];
+    read_values<E>(D, vt, wave, lane);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      b16x8 P[kFull];
+      read_transposed<kFull>(P, mt + kDeltaP, t, lane);
+      product(u[t], P, D);
+    }
+    factors(f, vecs, kInto, lane);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(f[e], x[e / 4][e % 4], u[e / 4][e % 4]);
+    b16x8 Y[kFull];
+    split_operand<kFull>(Y, y);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      b16x8 T[kFull];
+      read_transposed<kFull>(T, mt, t, lane);
+      x[t] = f32x4(0.f);
+      product(x[t], T, Y);
+    }
+    {
+      float* const to = a.w + at * C * pitch + w.col0 + col;
+      if (kept)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to[(16 * (e / 4) + 4 * g + e % 4) * pitch] = x[e / 4][e % 4];
+    }
+    // R = up_C R + Q^T (scale up dO) - K^T (up w)
+    b16x8 M[2][kFull];
+    values_of(y, D);
+    factors(f, vecs, kScaledUp, lane);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= f[e];
+    split_operand<kFull>(M[0], y);
+    factors(f, vecs, kUp, lane);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = -f[e] * x[e / 4][e % 4];
+    split_operand<kFull>(M[1], y);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      b16x8 K[IN], Q[IN];
+      read_keys<E, DKP>(Q, qt, lane, t);
+      read_keys<E, DKP>(K, kt, lane, t);
+      R[t] *= whole;
+      product(R[t], Q, M[0]);
+      product(R[t], K, M[1]);
+    }
+    __syncthreads();
+  }
+  if (a.ds_out != nullptr) store_state<KT>(R, a.ds_out + head * a.Dk * a.Dv, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+}
+
+// -- the gradients of a chunk ----------------------------------------------------------------------
+
+template <class E, int DKP>
+struct GradShape {
+  static constexpr int IN = Parts<E>::kIn, KT = DKP / 64;  // tiles of 16 rows of the state a wave
+  static constexpr int kK = 0, kQ = 2 * C * IN * DKP, kO = 2 * kQ, kX = kO + 2 * C * IN * 64, kW = kX + 2 * C * 3 * 64,
+                       kScores = kW + 2 * C * 3 * 64, kVecs = kScores + 4 * 3 * kPart, kSums = kVecs + 5 * 4 * C,
+                       kDots = kSums + 8 * C, kLds = kDots + 4 * 4 * 4 * C + 64;
+};
+
+// Grid slots x H.  The columns of the state are taken 64 at a time; a wave has DKP
+// / 4 of its rows.
+template <class E, int DKP, bool VEC>
+__global__ void __launch_bounds__(256) delta_grad_kernel(DeltaArgs a) {
+  typedef GradShape<E, DKP> Sh;
+  typedef typename E::raw raw;
+  constexpr int IN = Sh::IN, KT = Sh::KT;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char *const kt = lds + Sh::kK, *const qt = lds + Sh::kQ, *const ot = lds + Sh::kO, *const xt = lds + Sh::kX,
+              *const wt = lds + Sh::kW, *const scores = lds + Sh::kScores, *const vecs = lds + Sh::kVecs;
+  double* const sums = reinterpret_cast<double*>(lds + Sh::kSums);
+  float* const dots = reinterpret_cast<float*>(lds + Sh::kDots);  // [4 waves][4][32], then <R, S> of each wave
+  const uint32_t slot = divide(blockIdx.x, a.H, a.by_heads);
+  const int h = (int)(blockIdx.x - slot * a.H);
+  int b, c;
+  if (!chunk_of(a, slot, b, c)) return;
+  const Span s = span_of(a, b);
+  const int n = max(0, min(C, s.len - c * C));
+  const int all = a.lengths != nullptr ? min(C, a.T - c * C) : n;  // rows to write: padding as zeros
+  if (all <= 0) return;
+  const int64_t t0 = (int64_t)c * C;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+  const int64_t at = (int64_t)slot * a.H + h;
+  const int pitch = (a.Dv + 3) & ~3;
+  void* const dv = const_cast<void*>(a.dv.p);
+  const int64_t dv0 = base_of(a.dv, a, s, b, h) + t0 * a.dv.token;
+  if (n == 0) {
+    for (int i = threadIdx.x; i < all * a.Dv; i += 256) static_cast<raw*>(dv)[dv0 + (i / a.Dv) * a.dv.token + i % a.Dv] = E::put(0.f);
+  }
+
+  const uint32_t qs = (uint32_t)a.q.token * (uint32_t)sizeof(raw), ks = (uint32_t)a.k.token * (uint32_t)sizeof(raw),
+                 os = (uint32_t)a.o.token * (uint32_t)sizeof(raw);
+  typedef Rows<E, C, 64, 256, VEC> Values;
+  typedef Rows<F32, C, 64, 256, true> Wide;
+  Values ro(os, 64, false);
+  Wide rx((uint32_t)pitch * 4u, 64, false), rw((uint32_t)pitch * 4u, 64, false);
+  const raw* const o = static_cast<const raw*>(a.o.p) + base_of(a.o, a, s, b, h);
+  const float *const xs = a.x + at * C * pitch, *const ws = a.w + at * C * pitch;
+  auto fetch = [&](int col) {
+    const int m = col < a.Dv ? n : 0;
+    const int64_t first = m == 0 ? 0 : t0;
+    ro.whole = Values(os, a.Dv - col, false).whole;  // (the last columns are fewer)
+    rx.whole = Wide((uint32_t)pitch * 4u, pitch - col, false).whole;
+    rw.whole = rx.whole;
+    ro.load(o + col, first, m, os, min(64, a.Dv - col), false);
+    rx.load(xs + col, 0, m, (uint32_t)pitch * 4u, min(64, pitch - col), false);
+    rw.load(ws + col, 0, m, (uint32_t)pitch * 4u, min(64, pitch - col), false);
+  };
+  f32x4 dq[KT][2], row[KT][2], cl[KT][2], so[1], sw[1];
+  float inner = 0.f;  // <R, S>
+#pragma unroll
+  for (int i = 0; i < KT; ++i)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) dq[i][t] = row[i][t] = cl[i][t] = f32x4(0.f);
+  so[0] = sw[0] = f32x4(0.f);
+  if (n > 0) {
+    {
+      Rows<E, C, DKP, 256, VEC> rq(qs, a.Dk, false), rk(ks, a.Dk, false);
+      rq.load(static_cast<const raw*>(a.q.p) + base_of(a.q, a, s, b, h), t0, n, qs, a.Dk, false);
+      rk.load(static_cast<const raw*>(a.k.p) + base_of(a.k, a, s, b, h), t0, n, ks, a.Dk, false);
+      rq.store(qt);
+      rk.store(kt);
+      const char* const block = a.blocks + at * kDeltaBlock;
+      if (threadIdx.x < 5 * C) reinterpret_cast<float*>(vecs)[threadIdx.x] = reinterpret_cast<const float*>(block + kDeltaVec)[threadIdx.x];
+      if (threadIdx.x < C) sums[threadIdx.x] = reinterpret_cast<const double*>(block + kDeltaSums)[threadIdx.x];
+      for (int i = threadIdx.x; i < 4 * 3 * kPart / 16; i += 256) reinterpret_cast<u32x4*>(scores)[i] = u32x4{0u, 0u, 0u, 0u};
+    }
+    const __amdgpu_buffer_rsrc_t rS = make_rsrc(a.S + at * a.Dk * pitch, (uint32_t)(a.Dk * pitch) * 4u),
+                                 rR = make_rsrc(a.R + at * a.Dk * pitch, (uint32_t)(a.Dk * pitch) * 4u);
+    const int ti = (wave + 1) / 2, tj = wave / 2;  // the wave's tile of the scores (wave < 3)
+    fetch(0);
+    for (int col = 0; col < a.Dv; col += 64) {
+      ro.store(ot);
+      rx.store(xt);
+      rw.store(wt);
+      // dv, from the registers that w came in
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int v = (int)threadIdx.x + 256 * i, r = v / 16, d = col + 4 * (v % 16);
+        const u32x4 y = rw.v[i];
+        const f32x4 z = {__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]), __uint_as_float(y[3])};
+        if (r < n) put4<E>(dv, dv0 + r * a.dv.token + d, z, a.Dv - d, false, (a.vec & 4) != 0);
+        else if (r < all) put4<E>(dv, dv0 + r * a.dv.token + d, f32x4(0.f), a.Dv - d, false, (a.vec & 4) != 0);
+      }
+      __syncthreads();
+      fetch(col + 64);
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const int unit = row_at<64>(l) ^ (g << 4) ^ (64 * st);
+        b16x8 O[2][IN], X[2][kFull], W[2][kFull];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int p = 0; p < IN; ++p) O[t][p] = read_row(ot, unit + p * (C * 64 * 2) + t * (16 * 128));
+#pragma unroll
+          for (int p = 0; p < kFull; ++p) {
+            X[t][p] = read_row(xt, unit + p * (C * 64 * 2) + t * (16 * 128));
+            W[t][p] = read_row(wt, unit + p * (C * 64 * 2) + t * (16 * 128));
+          }
+        }
+        if (wave < 3) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int x = 0; x <= y; ++x)
+              if (y == ti && x == tj) {
+                product(so[0], O[y], X[x]);
+                product(sw[0], W[y], X[x]);
+              }
+        }
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+          const int dk = 16 * (wave * KT + i) + l, d = col + 32 * st + 8 * g;
+          float fs[8], fr[8];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t from = d + 4 * u < pitch && dk < a.Dk ? (uint32_t)(dk * pitch + d + 4 * u) * 4u : kOutside;
+            const u32x4 y = __builtin_amdgcn_raw_buffer_load_b128(rS, from, 0, kPlain), z = __builtin_amdgcn_raw_buffer_load_b128(rR, from, 0, kPlain);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              fs[4 * u + e] = __uint_as_float(y[e]);
+              fr[4 * u + e] = __uint_as_float(z[e]);
+              inner = __builtin_fmaf(fs[4 * u + e], fr[4 * u + e], inner);
+            }
+          }
+          b16x8 A[kFull];
+          split_operand<kFull>(A, fs);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            product(dq[i][t], A, O[t]);
+            product(row[i][t], A, W[t]);
+          }
+          split_operand<kFull>(A, fr);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) product(cl[i][t], A, X[t]);
+        }
+      }
+      __syncthreads();
+    }
+
+    // Y beta and -Z beta by rows i, Y and -Z by rows j
+    const float* const beta = reinterpret_cast<const float*>(vecs) + kBeta * C;
+    if (wave < 3) {
+      const int j = 16 * tj + l, i0 = 16 * ti + 4 * g;
+      float y[2][4], z[2][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = i0 + r;
+        const float d = j <= i ? exp_sum(sums[i] - sums[j]) : 0.f;
+        y[0][r] = j <= i ? so[0][r] * (a.scale * d) : 0.f;
+        y[1][r] = j < i ? -sw[0][r] * d : 0.f;
+        z[0][r] = y[0][r] * beta[j];
+        z[1][r] = y[1][r] * beta[j];
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        uint32_t words[kFull][2];
+        split<kFull, 4>(z[m], words);
+#pragma unroll
+        for (int p = 0; p < kFull; ++p)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            *reinterpret_cast<uint16_t*>(scores + (m * 3 + p) * kPart + delta_at(i0 + r, position(j))) = (uint16_t)(words[p][r / 2] >> (16 * (r % 2)));
+        split<kFull, 4>(y[m], words);
+#pragma unroll
+        for (int p = 0; p < kFull; ++p)
+          *reinterpret_cast<u32x2*>(scores + ((2 + m) * 3 + p) * kPart + delta_at(j, position(i0))) = u32x2{words[p][0], words[p][1]};
+      }
+    }
+    __syncthreads();
+  }
+
+  float sum[4][2];  // of tokens 16 t + l: k.(down x R^T), q.dq, k.row, k.col
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[i][0] = sum[i][1] = 0.f;
+#pragma unroll
+  for (int i = 0; i < KT; ++i) {
+    const int tile = wave * KT + i, d0 = 16 * tile + 4 * g;
+    if (n > 0) {
+      // rows 4 of the tile and tokens 16 t + l of q and k
+      float fq[2][4], fk[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        typedef __bf16 b16x4 __attribute__((ext_vector_type(4)));
+        const int from = (row_at<DKP>(l) ^ ((d0 >> 3) << 4)) + 2 * (d0 & 7) + t * (32 * DKP);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) fq[t][r] = fk[t][r] = 0.f;
+#pragma unroll
+        for (int p = IN - 1; p >= 0; --p) {
+          const b16x4 yq = *reinterpret_cast<const b16x4*>(qt + from + p * (C * DKP * 2)), yk = *reinterpret_cast<const b16x4*>(kt + from + p * (C * DKP * 2));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            fq[t][r] += (float)yq[r];
+            fk[t][r] += (float)yk[r];
+          }
+        }
+      }
+      // (the tile's rows are 16 tile + l here, as the products with S had them)
+      b16x8 K[IN], Q[IN];
+      {
+        const int base = row_at<DKP>(4 * g + (l >> 2)) ^ ((2 * tile + ((l & 3) >> 1)) << 4);
+#pragma unroll
+        for (int p = 0; p < IN; ++p) {
+          u32x2 yk[2], yq[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            yk[u] = read_columns(kt, base + 8 * (l & 1) + p * (C * DKP * 2) + 16 * u * (2 * DKP));
+            yq[u] = read_columns(qt, base + 8 * (l & 1) + p * (C * DKP * 2) + 16 * u * (2 * DKP));
+          }
+          const uint32_t wk[4] = {yk[0][0], yk[0][1], yk[1][0], yk[1][1]}, wq[4] = {yq[0][0], yq[0][1], yq[1][0], yq[1][1]};
+          K[p] = operand(wk);
+          Q[p] = operand(wq);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float* const f = reinterpret_cast<const float*>(vecs) + 16 * t + l;
+        dq[i][t] *= f[kScaledUp * C];
+        row[i][t] *= -f[kUp * C];
+        cl[i][t] *= f[kDown * C];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[0][t] = __builtin_fmaf(fk[t][r], cl[i][t][r], sum[0][t]);
+        b16x8 M[kFull];
+        read_matrix<kFull>(M, scores, t, lane);
+        product(dq[i][t], K, M);
+        read_matrix<kFull>(M, scores + 3 * kPart, t, lane);
+        product(row[i][t], K, M);
+        read_matrix<kFull>(M, scores + 6 * kPart, t, lane);
+        product(cl[i][t], Q, M);
+        read_matrix<kFull>(M, scores + 9 * kPart, t, lane);
+        product(cl[i][t], K, M);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sum[1][t] = __builtin_fmaf(fq[t][r], dq[i][t][r], sum[1][t]);
+          sum[2][t] = __builtin_fmaf(fk[t][r], row[i][t][r], sum[2][t]);
+          sum[3][t] = __builtin_fmaf(fk[t][r], cl[i][t][r], sum[3][t]);
+          row[i][t][r] = __builtin_fmaf(f[kBeta * C], cl[i][t][r], row[i][t][r]);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int token = 16 * t + l;
+      if (token < all) {
+        const bool in = token < n;
+        const int64_t atq = base_of(a.dq, a, s, b, h) + (t0 + token) * a.dq.token + d0, atk = base_of(a.dk, a, s, b, h) + (t0 + token) * a.dk.token + d0;
+        put4<E>(const_cast<void*>(a.dq.p), atq, in ? dq[i][t] : f32x4(0.f), a.Dk - d0, a.qk_f32 != 0, (a.vec & 8) != 0);
+        put4<E>(const_cast<void*>(a.dk.p), atk, in ? row[i][t] : f32x4(0.f), a.Dk - d0, a.qk_f32 != 0, (a.vec & 8) != 0);
+      }
+    }
+  }
+  // the scalars' gradients
+  if (n > 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        sum[i][t] += __shfl_xor(sum[i][t], 16);
+        sum[i][t] += __shfl_xor(sum[i][t], 32);
+        if (lane < 16) dots[(wave * 4 + i) * C + 16 * t + l] = sum[i][t];
+      }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) inner += __shfl_xor(inner, d);
+    if (lane == 0) dots[4 * 4 * C + wave] = inner;
+  }
+  __syncthreads();
+  if (threadIdx.x < C) {
+    const int t = threadIdx.x;
+    float dbeta = 0.f;
+    double dg = 0.;
+    if (n > 0) {
+      float y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = (dots[i * C + t] + dots[(4 + i) * C + t]) + (dots[(8 + i) * C + t] + dots[(12 + i) * C + t]);
+      const float* const f = reinterpret_cast<const float*>(vecs);
+      dbeta = y[3];
+      dg = t < n ? ((double)y[1] + (double)y[2]) - (double)(f[kBeta * C + t] * dbeta) : 0.;
+      double behind = t < n ? (double)(f[kBeta * C + t] * y[0]) : 0.;
+#pragma unroll
+      for (int d = 1; d < C; d *= 2) {
+        behind += __shfl_xor(behind, d, C);
+        const double z = __shfl_down(dg, d, C);
+        if (t + d < C) dg += z;
+      }
+      const float* const in = dots + 4 * 4 * C;
+      dg += behind + (double)f[kUp * C + C - 1] * (double)((in[0] + in[1]) + (in[2] + in[3]));
+      if (t == 0 && c == 0 && a.s_in == nullptr) dg = 0.;  // nothing there to decay before the first token
+    }
+    if (t < all) {
+      static_cast<float*>(const_cast<void*>(a.dbeta.p))[base_of(a.dbeta, a, s, b, h) + (t0 + t) * a.dbeta.token] = t < n ? dbeta : 0.f;
+      if (a.dg.p != nullptr)
+        static_cast<float*>(const_cast<void*>(a.dg.p))[base_of(a.dg, a, s, b, h) + (t0 + t) * a.dg.token] = t < n ? (float)dg : 0.f;
+    }
+  }
+}
+
+// -- launches of one element type ---------------------------------------------------------------------
+
+template <class K>
+hipError_t launch_kernel(K kernel, unsigned grid, int lds, const DeltaArgs& a, hipStream_t stream) {
+  const void* fn = reinterpret_cast<const void*>(kernel);
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  DeltaArgs args = a;
+  void* list[] = {&args};
+  return hipLaunchKernel(fn, dim3(grid), dim3(256), list, (size_t)lds, stream);
+}
+
+template <class E, int DKP, bool VEC>
+hipError_t launch_shape(const DeltaArgs& a, bool backward, hipStream_t stream) {
+  const unsigned blocks = (unsigned)(a.slots * a.H), states = (unsigned)((int64_t)a.tiles * a.B * a.H);
+  hipError_t e = hipSuccess;
+  if (blocks > 0) e = launch_kernel(delta_prepare_kernel<E, DKP, VEC, true>, (blocks + 3) / 4, 0, a, stream);
+  if (e != hipSuccess) return e;
+  if (!backward) return launch_kernel(delta_forward_kernel<E, DKP, VEC, false>, states, Shape<E, DKP>::kLds, a, stream);
+  if (blocks > 0) e = launch_kernel(delta_forward_kernel<E, DKP, VEC, true>, states, Shape<E, DKP>::kLds, a, stream);
+  if (e == hipSuccess) e = launch_kernel(delta_reverse_kernel<E, DKP, VEC>, states, Shape<E, DKP>::kLds, a, stream);
+  if (e == hipSuccess && blocks > 0) e = launch_kernel(delta_grad_kernel<E, DKP, VEC>, blocks, GradShape<E, DKP>::kLds, a, stream);
+  return e;
+}
+
+template <class E, bool VEC>
+hipError_t launch_vec(const DeltaArgs& a, bool backward, hipStream_t stream) {
+  if (a.dkp == 64) return launch_shape<E, 64, VEC>(a, backward, stream);
+  if (a.dkp == 128) return launch_shape<E, 128, VEC>(a, backward, stream);
+  return launch_shape<E, 256, VEC>(a, backward, stream);
+}
+
+template <class E>
+hipError_t launch_type(const DeltaArgs& a, bool backward, hipStream_t stream) {
+  return (a.vec & 1) != 0 ? launch_vec<E, true>(a, backward, stream) : launch_vec<E, false>(a, backward, stream);
+}
+
+}  // namespace delta
+}  // namespace prnn

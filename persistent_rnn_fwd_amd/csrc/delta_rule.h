@@ -1,0 +1,65 @@
+// The gated delta rule: kernel arguments and launches.
+#pragma once
+
+#include "sequence.h"
+
+namespace prnn {
+
+constexpr int kDeltaChunk = 32;  // tokens of a chunk
+
+// What the chunks' kernels need of a chunk and head besides q, k and v, left by
+// the first launch (delta_prepare_kernel), in bytes from the block's start.  T' and P' are three
+// bf16 parts of 32 x 32, in the order that delta_at() says.
+constexpr int kDeltaT = 0, kDeltaP = 3 * 2048, kDeltaVec = 6 * 2048;
+enum DeltaVec { kUp, kScaledUp, kInto, kDown, kBeta };  // 32 floats each
+constexpr int kDeltaSums = kDeltaVec + 5 * 128;         // 32 doubles: the decays' sums
+constexpr int kDeltaBlock = 13 * 1024;
+
+struct DeltaArgs {
+  AttnOperand q, k, v, o;  // o: the output, or its gradient
+  AttnOperand g, beta;     // fp32, one value a token and head; g.p null: no decay
+  AttnOperand dq, dk, dv, dg, dbeta;  // dg.p may be null
+  const float* s_in;       // or nullptr (zeros)
+  float* s_out;            // or nullptr
+  const float* ds_in;      // backward: of the final state, or nullptr
+  float* ds_out;           // ... and of the initial one, or nullptr
+  const int32_t* lengths;
+  const int32_t* offsets;
+  int64_t rows;
+  int B, T, H, Dk, Dv;
+  float scale;
+  int qk_f32;  // dq and dk are fp32 whatever the element type
+  // workspace, by chunk ("slot") and head
+  char* blocks;
+  float *x, *w;   // backward: [slot][H][32][Dv]
+  float *S, *R;   // backward: [slot][H][Dk][Dv], the states that chunks start from and the gradients of those they end with
+  // set by plan_delta
+  int64_t slots;
+  int chunks;  // of the longest sequence
+  int dkp, tiles, vec;
+  int seg_tokens;  // kDeltaChunk (find_unit)
+  uint32_t by_seg, by_tiles, by_heads, by_chunks;
+};
+
+// Chunks of all sequences: those of the longest one for each, or as many as
+// packed rows can fill (a sequence whose first row is n chunks and a rest has
+// the slots from n + b on).
+void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward);
+hipError_t launch_delta(const DeltaArgs& a, prnnDataType_t type, bool backward, hipStream_t stream);
+// ... of one element type (delta_f32.hip, delta_f16.hip, delta_bf16.hip)
+hipError_t launch_delta_f32(const DeltaArgs& a, bool backward, hipStream_t stream);
+hipError_t launch_delta_f16(const DeltaArgs& a, bool backward, hipStream_t stream);
+hipError_t launch_delta_bf16(const DeltaArgs& a, bool backward, hipStream_t stream);
+
+struct DeltaStepArgs {
+  AttnOperand q, k, v, o, g, beta;
+  const float* s_in;
+  float* s_out;
+  int B, H, Dk, Dv;
+  int tiles;  // tiles of 32 columns
+  uint32_t by_tiles, by_heads;
+  float scale;
+};
+hipError_t launch_delta_step(const DeltaStepArgs& a, prnnDataType_t type, hipStream_t stream);
+
+}  // namespace prnn
