@@ -140,7 +140,9 @@ DeltaArgs base_args(const Problem& p, const prnnSequence_t* q, const prnnSequenc
 bool grids_fit(const DeltaArgs& a, bool backward) {
   if ((double)a.slots * a.H > 4. * kMaxWorkgroups) return false;
   const int64_t blocks = a.slots * a.H;
-  return (backward ? blocks : (blocks + 3) / 4) <= kMaxWorkgroups && (int64_t)a.tiles * a.B * a.H <= kMaxWorkgroups;
+  const double pieces = a.units > 0 ? (double)a.units * a.H : (double)a.B * a.H * a.segments;
+  return (backward ? blocks : (blocks + 3) / 4) <= kMaxWorkgroups &&
+         pieces * (a.tiles + (a.segments > 1 ? a.move_tiles : 0)) <= kMaxWorkgroups && (a.segments < 3 || (double)a.B * a.H * ((a.pitch + 15) / 16) <= kMaxWorkgroups);
 }
 
 void log_call(const prnnContext* h, const char* what, const Problem& p) {
@@ -151,11 +153,23 @@ void log_call(const prnnContext* h, const char* what, const Problem& p) {
 
 size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
+// The workspace of split sequences, from `at` on (null: only its size).
+size_t segment_memory(DeltaArgs* a, char* at) {
+  const size_t parts = (size_t)a->seg_slots * a->H, states = rounded(parts * a->Dk * a->pitch * 4),
+               moves = rounded(parts * a->Dk * a->move_pitch * 4);
+  if (at != nullptr && parts > 0) {
+    a->ends = reinterpret_cast<float*>(at);
+    a->firsts = reinterpret_cast<float*>(at + states);
+    a->moves = reinterpret_cast<float*>(at + 2 * states);
+  }
+  return 2 * states + moves;
+}
+
 }  // namespace
 
 namespace prnn {
 
-void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward) {
+void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward, int compute_units) {
   const int e = type == PRNN_DATA_FLOAT ? 4 : 2;
   // whether every row starts at a multiple of `per` elements of `size` bytes and has a multiple of them
   auto vectors = [&](const AttnOperand& x, int D, int size, int per) {
@@ -173,11 +187,31 @@ void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward) {
   a->tiles = (a->Dv + 63) / 64;
   a->chunks = (int)(((int64_t)a->T + kDeltaChunk - 1) / kDeltaChunk);
   a->slots = a->T == 0 ? 0 : a->offsets != nullptr ? a->rows / kDeltaChunk + a->B : (int64_t)a->B * a->chunks;
-  a->seg_tokens = kDeltaChunk;
-  a->by_seg = inverse_of(kDeltaChunk);
+  a->pitch = (a->Dv + 3) / 4 * 4;
+  a->move_pitch = (a->Dk + 3) / 4 * 4;
+  a->move_tiles = (a->Dk + 63) / 64;
+  // Segments: as many as give each compute unit 2 workgroups, of at least 4 chunks,
+  // and no split in less than 3.
+  const int64_t sequences = a->offsets != nullptr && a->T > 0 ? std::max<int64_t>(1, std::min<int64_t>(a->B, a->rows / a->T)) : a->B;
+  const int64_t states = std::max<int64_t>(1, sequences * a->H * a->tiles);
+  int64_t segments = std::min<int64_t>(2 * compute_units / states, a->chunks / 4);
+  if (segments < 3) segments = 1;
+  a->seg_chunks = std::max(1, (int)((a->chunks + segments - 1) / segments));
+  a->segments = std::max(1, (a->chunks + a->seg_chunks - 1) / a->seg_chunks);
+  const int64_t tokens = (int64_t)a->seg_chunks * kDeltaChunk;
+  a->units = 0;
+  a->seg_slots = 0;
+  if (a->segments > 1) {
+    a->seg_slots = a->offsets != nullptr ? a->rows / tokens + 1 : (int64_t)a->B * a->segments;
+    if (a->offsets != nullptr) a->units = (int)(a->rows / tokens + a->B);
+  }
   a->by_tiles = inverse_of(a->tiles);
+  a->by_all_tiles = inverse_of(a->tiles + a->move_tiles);
   a->by_heads = inverse_of(a->H);
   a->by_chunks = inverse_of(std::max(1, a->chunks));
+  a->by_segments = inverse_of(a->segments);
+  a->by_seg_chunks = inverse_of(a->seg_chunks);
+  a->by_seg_tokens = inverse_of((int)tokens);
 }
 
 }  // namespace prnn
@@ -200,13 +234,15 @@ prnnStatus_t prnn_gated_delta_rule(prnnHandle_t h, const prnnDeltaRule_t* d, con
   DeltaArgs a = base_args(p, q, k, v, log_decay, beta, o);
   a.s_in = S0;
   a.s_out = S1;
-  plan_delta(&a, d->type, false);
+  plan_delta(&a, d->type, false, handle_compute_units(h));
   if (!grids_fit(a, false)) return PRNN_STATUS_NOT_SUPPORTED;
   if (a.slots > 0) {
     void* mem = nullptr;
-    st = handle_workspace(h, (size_t)a.slots * a.H * kDeltaBlock, stream, &mem);
+    const size_t blocks = rounded((size_t)a.slots * a.H * kDeltaBlock);
+    st = handle_workspace(h, blocks + segment_memory(&a, nullptr), stream, &mem);
     if (st != PRNN_STATUS_SUCCESS) return st;
     a.blocks = static_cast<char*>(mem);
+    segment_memory(&a, a.blocks + blocks);
   }
   st = launched(launch_delta(a, d->type, false, stream));
   if (st == PRNN_STATUS_SUCCESS) log_call(h, "gated delta rule", p);
@@ -254,13 +290,14 @@ prnnStatus_t prnn_gated_delta_rule_backward(prnnHandle_t h, const prnnDeltaRule_
     }
     a.qk_f32 = 1;
   }
-  plan_delta(&a, d->type, true);
+  plan_delta(&a, d->type, true, handle_compute_units(h));
   if (!grids_fit(a, true)) return PRNN_STATUS_NOT_SUPPORTED;
   if (a.slots > 0) {
-    const size_t blocks = (size_t)a.slots * a.H, pitch = (d->Dv + 3) / 4 * 4, tokens = rounded(blocks * kDeltaChunk * pitch * 4),
+    const size_t blocks = (size_t)a.slots * a.H, pitch = a.pitch, tokens = rounded(blocks * kDeltaChunk * pitch * 4),
                  states = rounded(blocks * d->Dk * pitch * 4);
     void* mem = nullptr;
-    st = handle_workspace(h, rounded(blocks * kDeltaBlock) + 2 * (tokens + states + heads), stream, &mem);
+    const size_t segments = segment_memory(&a, nullptr);
+    st = handle_workspace(h, rounded(blocks * kDeltaBlock) + 2 * (tokens + states + heads) + segments, stream, &mem);
     if (st != PRNN_STATUS_SUCCESS) return st;
     char* at = static_cast<char*>(mem);
     auto take = [&](size_t bytes) {
@@ -273,6 +310,7 @@ prnnStatus_t prnn_gated_delta_rule_backward(prnnHandle_t h, const prnnDeltaRule_
     a.w = reinterpret_cast<float*>(take(tokens));
     a.S = reinterpret_cast<float*>(take(states));
     a.R = reinterpret_cast<float*>(take(states));
+    segment_memory(&a, take(segments));
     if (group > 1) {
       a.dq.p = take(heads);
       a.dk.p = take(heads);

@@ -158,15 +158,25 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// First chunk of a sequence in the workspace.
+// First chunk of a sequence in the workspace, and a chunk's sequence and number in it.
 __device__ __forceinline__ int64_t first_chunk(const DeltaArgs& a, const Span& s, int b) {
   return a.offsets != nullptr ? s.first / C + b : (int64_t)b * a.chunks;
 }
 __device__ __forceinline__ bool chunk_of(const DeltaArgs& a, uint32_t slot, int& b, int& c) {
-  if (a.offsets != nullptr) return find_unit(a, slot, b, c);
+  if (a.offsets != nullptr) {
+    const Pieces p = {a.offsets, a.rows, a.B, C, 0xffffffffu / C + 1};
+    return find_unit(p, slot, b, c);
+  }
   b = (int)divide(slot, a.chunks, a.by_chunks);
   c = (int)slot - b * a.chunks;
   return true;
+}
+
+// Workgroups are dealt to the 8 XCDs in turn; those of neighbouring numbers, which
+// read the same rows, go to one of them, whose L2 then has them.
+__device__ __forceinline__ uint32_t near(uint32_t id, uint32_t count) {
+  const uint32_t whole = count / 8 * 8;
+  return id < whole ? id % 8 * (whole / 8) + id / 8 : id;
 }
 
 // -- what depends on no state ------------------------------------------------------------------
@@ -345,23 +355,42 @@ struct Shape {
   static constexpr int kVecs = kM + 2 * 3 * kPart, kLds = kVecs + 5 * 4 * C;
 };
 
-// What a workgroup works on: 64 columns of one head's state.
+// What a workgroup works on: 64 columns of one head's state, or of what a segment
+// makes of the identity (move), and one segment of a sequence.
 struct Where {
   int b, h, col0, cols;
+  bool move;
   Span s;
-  int chunks;
-  int64_t slot;
+  int seg, segments;  // its number, and the sequence's
+  int lo, hi;         // its chunks
+  int64_t chunk;      // the sequence's first chunk in the workspace
+  int64_t part;       // ... and first segment
 };
 
-__device__ __forceinline__ bool where(const DeltaArgs& a, Where& w) {
-  const uint32_t id = blockIdx.x, state = divide(id, a.tiles, a.by_tiles);
-  w.col0 = 64 * (int)(id - state * a.tiles);
-  w.b = (int)divide(state, a.H, a.by_heads);
-  w.h = (int)(state - (uint32_t)w.b * a.H);
-  w.cols = min(64, a.Dv - w.col0);
+// tiles: column tiles of a head; the launch has as many workgroups for every
+// head and segment.
+__device__ __forceinline__ bool where(const DeltaArgs& a, int tiles, uint32_t by_tiles, Where& w) {
+  const uint32_t id = near(blockIdx.x, gridDim.x), state = divide(id, tiles, by_tiles);
+  const int tile = (int)(id - state * tiles);
+  const uint32_t piece = divide(state, a.H, a.by_heads);
+  w.h = (int)(state - piece * a.H);
+  if (a.units > 0) {
+    const Pieces p = {a.offsets, a.rows, a.B, a.seg_chunks * C, a.by_seg_tokens};
+    if (!find_unit(p, piece, w.b, w.seg)) return false;
+  } else {
+    w.b = (int)divide(piece, a.segments, a.by_segments);
+    w.seg = (int)piece - w.b * a.segments;
+  }
+  w.move = tile >= a.tiles;
+  w.col0 = 64 * (w.move ? tile - a.tiles : tile);
+  w.cols = min(64, (w.move ? a.Dk : a.Dv) - w.col0);
   w.s = span_of(a, w.b);
-  w.chunks = (w.s.len + C - 1) / C;
-  w.slot = first_chunk(a, w.s, w.b);
+  const int chunks = (w.s.len + C - 1) / C;
+  w.segments = chunks > 0 ? (int)divide(chunks - 1, a.seg_chunks, a.by_seg_chunks) + 1 : 1;
+  w.lo = w.seg * a.seg_chunks;
+  w.hi = min(chunks, w.lo + a.seg_chunks);
+  w.chunk = first_chunk(a, w.s, w.b);
+  w.part = a.offsets != nullptr ? w.s.first / (a.seg_chunks * C) : (int64_t)w.b * a.segments;
   return true;
 }
 
@@ -526,8 +555,8 @@ __device__ __forceinline__ void put4(void* p, int64_t at, const f32x4& x, int li
   }
 }
 
-// The recurrence over a whole sequence for this wave's columns, straight from
-// memory: the rows of o, and S.  Slow; see the file comment.
+// The recurrence over a segment for this wave's columns, straight from memory:
+// the rows of o, and S.  Slow; see the file comment.
 template <class E, int DKP>
 __device__ __forceinline__ void delta_tokens(const DeltaArgs& a, const Where& w, int wave, int lane, f32x4 (&S)[DKP / 16]) {
   typedef typename E::raw raw;
@@ -541,7 +570,7 @@ __device__ __forceinline__ void delta_tokens(const DeltaArgs& a, const Where& w,
   int rows = a.Dk - first;  // rows of the state from the lane's first one on
   keep(rows);
 #pragma nounroll
-  for (int64_t t = 0; t < w.s.len; ++t) {
+  for (int64_t t = (int64_t)w.lo * C; t < min((int64_t)w.s.len, (int64_t)w.hi * C); ++t) {
     const float d = g != nullptr ? expf(g[t * a.g.token]) : 1.f;
     float found = 0.f, out = 0.f;
 #pragma unroll
@@ -573,60 +602,109 @@ __device__ __forceinline__ void delta_tokens(const DeltaArgs& a, const Where& w,
   }
 }
 
-// Forward: grid tiles x H x B.  SAVE: x and the chunks' first states into the
-// workspace instead of o and the final state.
-template <class E, int DKP, bool VEC, bool SAVE>
+// acc[t] += x[t] y and, with BOTH, other[t] += y z[t], the accumulators in turn.
+template <int IN, bool BOTH>
+__device__ __forceinline__ void state_products(f32x4 (&acc)[2], f32x4 (&other)[2], const b16x8 (&x)[2][IN],
+                                               const b16x8 (&z)[2][IN], const b16x8 (&y)[kFull]) {
+#pragma unroll
+  for (int s = kFull - 1; s >= 0; --s)  // small terms first
+#pragma unroll
+    for (int i = 0; i < IN; ++i) {
+      const int j = s - i;
+      if (j < 0) continue;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][i], y[j], acc[t], 0, 0, 0);
+      if (BOTH)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) other[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[j], z[t][i], other[t], 0, 0, 0);
+    }
+}
+
+// What the walk does: the outputs and the final state; x and the chunks' first
+// states for the gradients; or the segments' ends and moves.
+enum Walk { kOutputs, kKeep, kEnds };
+
+// Forward: grid tiles (kEnds: and move tiles) x H x segments.
+template <class E, int DKP, bool VEC, Walk WALK>
 __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(DeltaArgs a) {
   typedef Shape<E, DKP> Sh;
   typedef typename E::raw raw;
   constexpr int IN = Sh::IN, KT = Sh::KT;
+  constexpr bool OUT = WALK == kOutputs;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char *const kt = lds + Sh::kK, *const qt = lds + Sh::kQ, *const vt = lds + Sh::kV, *const mt = lds + Sh::kM,
               *const vecs = lds + Sh::kVecs;
   Where w;
-  if (!where(a, w)) return;
+  if (!where(a, WALK == kEnds ? a.tiles + a.move_tiles : a.tiles, WALK == kEnds ? a.by_all_tiles : a.by_tiles, w)) return;
+  // (the ends of the last segment are not needed, nor what the first one makes of any state but its own)
+  if (WALK == kEnds && (w.seg + 1 >= w.segments || (w.move && w.seg == 0))) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
   const int col = 16 * wave + l;
-  if (!SAVE && a.lengths != nullptr) {  // rows of padding are zeros
+  if (OUT && a.lengths != nullptr) {  // rows of padding are zeros
     raw* const o = static_cast<raw*>(const_cast<void*>(a.o.p)) + base_of(a.o, a, w.s, w.b, w.h) + w.col0;
-    for (int64_t t = w.s.len; t < a.T; ++t)
+    const int64_t end = min((int64_t)a.T, (int64_t)(w.seg + 1) * a.seg_chunks * C);
+    for (int64_t t = max((int64_t)w.s.len, (int64_t)w.lo * C); t < end; ++t)
       if ((int)threadIdx.x < w.cols) o[t * a.o.token + threadIdx.x] = E::put(0.f);
   }
+  if (w.seg >= w.segments) return;
   const uint32_t qs = (uint32_t)a.q.token * (uint32_t)sizeof(raw), ks = (uint32_t)a.k.token * (uint32_t)sizeof(raw),
                  vs = (uint32_t)a.v.token * (uint32_t)sizeof(raw);
   const raw* const q = static_cast<const raw*>(a.q.p) + base_of(a.q, a, w.s, w.b, w.h);
   const raw* const k = static_cast<const raw*>(a.k.p) + base_of(a.k, a, w.s, w.b, w.h);
-  const raw* const v = static_cast<const raw*>(a.v.p) + base_of(a.v, a, w.s, w.b, w.h) + w.col0;
+  const raw* const v = static_cast<const raw*>(a.v.p) + base_of(a.v, a, w.s, w.b, w.h) + (w.move ? 0 : w.col0);
+  const int vcols = w.move ? 0 : w.cols;  // (moves: values of zeros)
   Rows<E, C, DKP, 256, VEC> rq(qs, a.Dk, false), rk(ks, a.Dk, false);
-  Rows<E, C, 64, 256, VEC> rv(vs, w.cols, false);
+  Rows<E, C, 64, 256, VEC> rv(vs, vcols, false);
   Block block;
   auto fetch = [&](int c) {
-    const int n = max(0, min(C, w.s.len - c * C));
+    const int n = c < w.hi ? min(C, w.s.len - c * C) : 0;
     const int64_t t0 = n == 0 ? 0 : (int64_t)c * C;
     rk.load(k, t0, n, ks, a.Dk, false);
-    if (!SAVE) rq.load(q, t0, n, qs, a.Dk, false);
-    rv.load(v, t0, n, vs, w.cols, false);
-    if (n > 0) block.load(a.blocks + ((w.slot + c) * a.H + w.h) * kDeltaBlock);
+    if (OUT) rq.load(q, t0, n, qs, a.Dk, false);
+    rv.load(v, t0, n, vs, vcols, false);
+    if (n > 0) block.load(a.blocks + ((w.chunk + c) * a.H + w.h) * kDeltaBlock);
   };
-  fetch(0);
+  fetch(w.lo);
   const size_t head = (size_t)w.b * a.H + w.h;
-  const float* const s_in = a.s_in != nullptr ? a.s_in + head * a.Dk * a.Dv : nullptr;
-  const int pitch = (a.Dv + 3) & ~3;
+  const int64_t matrix = (int64_t)a.Dk * a.pitch;
+  const bool split = w.segments > 1;
+  // The state the segment starts from.  (A split sequence's own first state is
+  // kept in the workspace by the launch for the ends: another workgroup may write the
+  // final state in its place.)
+  auto start = [&](f32x4 (&S)[KT]) {
+    if (WALK == kEnds && w.move) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[t][r] = 32 * (t / 2) + 8 * g + 4 * (t % 2) + r == w.col0 + col ? 1.f : 0.f;
+    } else if (WALK == kEnds && w.seg > 0) {
+      load_state<KT>(S, nullptr, a.Dk, a.Dv, 0, false, lane);
+    } else if (WALK != kEnds && split && w.seg > 0) {
+      load_state<KT>(S, a.ends + ((w.part + w.seg - 1) * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, col < w.cols, lane);
+    } else if (WALK != kEnds && split && a.s_in != nullptr) {
+      load_state<KT>(S, a.firsts + (w.part * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, col < w.cols, lane);
+    } else {
+      load_state<KT>(S, a.s_in != nullptr ? a.s_in + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+    }
+  };
   f32x4 S[KT];
-  load_state<KT>(S, s_in, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+  start(S);
+  const bool kept = w.col0 + col < a.pitch;  // (columns of padding hold zeros)
+  if (WALK == kEnds && w.seg == 0 && a.s_in != nullptr)
+    store_state<KT>(S, a.firsts + (w.part * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
   bool broken = false;
 
-  for (int c = 0; c < w.chunks; ++c) {
+  for (int c = w.lo; c < w.hi; ++c) {
     const int n = min(C, w.s.len - c * C);
     rk.store(kt);
-    if (!SAVE) rq.store(qt);
+    if (OUT) rq.store(qt);
     rv.store(vt);
     block.store(mt, vecs);
     __syncthreads();
     fetch(c + 1);
     const float whole = *reinterpret_cast<const float*>(vecs + 4 * (kUp * C + C - 1));
-    if constexpr (SAVE)
-      store_state<KT>(S, a.S + (((w.slot + c) * a.H + w.h) * a.Dk) * pitch, a.Dk, pitch, w.col0 + col, w.col0 + col < pitch, lane);
+    const int64_t at = (w.chunk + c) * a.H + w.h;
+    if constexpr (WALK == kKeep) store_state<KT>(S, a.S + at * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
 
     // K S and (Q S)^T
     const int rows = row_at<DKP>(l) ^ (g << 4);  // row l of a tile of 16, unit g
@@ -635,96 +713,212 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(
     for (int t = 0; t < 2; ++t) x[t] = O[t] = f32x4(0.f);
 #pragma unroll
     for (int s = 0; s < DKP / 32; ++s) {
-      b16x8 A[kFull];
-      state_operand<kFull>(A, S[2 * s], S[2 * s + 1]);
+      b16x8 A[kFull], K[2][IN], Q[2][IN];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        b16x8 K[IN], Q[IN];
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int p = 0; p < IN; ++p) {
-          K[p] = read_row(kt, (rows ^ (64 * s)) + p * (C * DKP * 2) + t * (32 * DKP));
-          if (!SAVE) Q[p] = read_row(qt, (rows ^ (64 * s)) + p * (C * DKP * 2) + t * (32 * DKP));
+          K[t][p] = read_row(kt, (rows ^ (64 * s)) + p * (C * DKP * 2) + t * (32 * DKP));
+          if (OUT) Q[t][p] = read_row(qt, (rows ^ (64 * s)) + p * (C * DKP * 2) + t * (32 * DKP));
         }
-        product(x[t], K, A);
-        if (!SAVE) product(O[t], A, Q);
-      }
+      state_operand<kFull>(A, S[2 * s], S[2 * s + 1]);
+      state_products<IN, OUT>(x, O, K, Q, A);
     }
     // x = T' (v - up K S)
     float y[8], f[8];
     {
-      b16x8 V[IN], Y[kFull];
+      b16x8 V[IN], Y[kFull], T[2][kFull];
       read_values<E>(V, vt, wave, lane);
       values_of(y, V);
       factors(f, vecs, kUp, lane);
 #pragma unroll
+      for (int t = 0; t < 2; ++t) read_matrix<kFull>(T[t], mt, t, lane);
+#pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(-f[e], x[e / 4][e % 4], y[e]);
       split_operand<kFull>(Y, y);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        b16x8 T[kFull];
-        read_matrix<kFull>(T, mt, t, lane);
-        x[t] = f32x4(0.f);
-        product(x[t], T, Y);
-      }
+      x[0] = x[1] = f32x4(0.f);
+      products<kFull, kFull, 2>(x, T, Y);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = x[e / 4][e % 4];
-    if constexpr (SAVE) {
-      float* const to = a.x + (((w.slot + c) * a.H + w.h) * C) * pitch + w.col0 + col;
-      if (w.col0 + col < pitch)
+    if constexpr (WALK == kKeep) {
+      float* const to = a.x + at * C * a.pitch + w.col0 + col;
+      if (kept)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) to[(16 * (e / 4) + 4 * g + e % 4) * pitch] = y[e];
-    } else {
-      // o^T = scale up (Q S)^T + x^T P'^T
-      b16x8 Y[kFull];
-      split_operand<kFull>(Y, y);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        b16x8 P[kFull];
-        read_matrix<kFull>(P, mt + kDeltaP, t, lane);
-        O[t] *= *reinterpret_cast<const float*>(vecs + 4 * (kScaledUp * C + 16 * t + l));
-        product(O[t], Y, P);
-      }
+        for (int e = 0; e < 8; ++e) to[(16 * (e / 4) + 4 * g + e % 4) * a.pitch] = y[e];
     }
     // S = up_C S + K^T (down beta x)
-    factors(f, vecs, kInto, lane);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] *= f[e];
     b16x8 D[kFull];
-    split_operand<kFull>(D, y);
+    {
+      float z[8];
+      factors(f, vecs, kInto, lane);
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      b16x8 K[IN];
-      read_keys<E, DKP>(K, kt, lane, t);
-      S[t] *= whole;
-      product(S[t], K, D);
+      for (int e = 0; e < 8; ++e) z[e] = y[e] * f[e];
+      split_operand<kFull>(D, z);
     }
-    if constexpr (!SAVE) {
+    if constexpr (OUT) {
+      // o^T = scale up (Q S)^T + x^T P'^T
+      b16x8 Y[kFull], P[2][kFull];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        read_matrix<kFull>(P[t], mt + kDeltaP, t, lane);
+        O[t] *= *reinterpret_cast<const float*>(vecs + 4 * (kScaledUp * C + 16 * t + l));
+      }
+      split_operand<kFull>(Y, y);
+      products<kFull, kFull, 2>(O, Y, P);
+    }
+#pragma unroll
+    for (int t = 0; t < KT; t += 2) {
+      b16x8 K[2][IN];
+      f32x4 z[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        read_keys<E, DKP>(K[u], kt, lane, t + u);
+        z[u] = S[t + u] * whole;
+      }
+      products<IN, kFull, 2>(z, K, D);
+      S[t] = z[0];
+      S[t + 1] = z[1];
+    }
+    if constexpr (OUT) {
       float z = 0.f;
       watch(z, O);
       broken = broken || wave_any(z != 0.f);
       raw* const o = static_cast<raw*>(const_cast<void*>(a.o.p));
-      const int64_t at = base_of(a.o, a, w.s, w.b, w.h) + (int64_t)c * C * a.o.token + w.col0 + 16 * wave + 4 * g;
+      const int64_t to = base_of(a.o, a, w.s, w.b, w.h) + (int64_t)c * C * a.o.token + w.col0 + 16 * wave + 4 * g;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        if (16 * t + l < n) put4<E>(o, at + (16 * t + l) * a.o.token, O[t], w.cols - 16 * wave - 4 * g, false, (a.vec & 2) != 0);
+        if (16 * t + l < n) put4<E>(o, to + (16 * t + l) * a.o.token, O[t], w.cols - 16 * wave - 4 * g, false, (a.vec & 2) != 0);
     }
     __syncthreads();
   }
-  if constexpr (!SAVE) {
+  if constexpr (OUT) {
     float z = 0.f;
     watch(z, S);
     if (broken || wave_any(z != 0.f)) {
-      load_state<KT>(S, s_in, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+      start(S);
       delta_tokens<E, DKP>(a, w, wave, lane, S);
     }
-    if (a.s_out != nullptr) store_state<KT>(S, a.s_out + head * a.Dk * a.Dv, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+    if (a.s_out != nullptr && w.seg + 1 == w.segments)
+      store_state<KT>(S, a.s_out + head * a.Dk * a.Dv, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+  } else if constexpr (WALK == kEnds) {
+    const int64_t part = (w.part + w.seg) * a.H + w.h;
+    if (w.move)
+      store_state<KT>(S, a.moves + part * a.Dk * a.move_pitch, a.Dk, a.move_pitch, w.col0 + col, w.col0 + col < a.move_pitch, lane);
+    else
+      store_state<KT>(S, a.ends + part * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
   }
 }
 
-// Backwards: grid as forward; leaves w and the gradients of the states behind
-// the chunks, and that of the initial state.
-template <class E, int DKP, bool VEC>
+// The states that segments start from, along each split sequence: ends[i] +=
+// moves[i] ends[i - 1], or backwards ends[i - 1] += moves[i]^T ends[i] (ends[i - 1] holds the
+// gradient of the state that segment i starts from).  Grid tiles of 16 columns x H
+// x B.  A step is a chain of loads, product and store, so its rows are spread over the
+// waves, the state goes round through LDS, and the next step's matrix is on its
+// way meanwhile.
+template <int DKP, bool REVERSE>
+__global__ void __launch_bounds__(256) delta_scan_kernel(DeltaArgs a) {
+  constexpr int TILES = DKP / 64, STEPS = DKP / 32, kRow = DKP + 4;  // tiles of 16 rows a wave
+  constexpr bool kAhead = DKP <= 128;  // (registers)
+  __shared__ __attribute__((aligned(16))) float lds[16][kRow];
+  const uint32_t tiles = (uint32_t)(a.pitch + 15) / 16u, state = blockIdx.x / tiles;
+  const uint32_t b = divide(state, a.H, a.by_heads);
+  const int h = (int)(state - b * a.H), col0 = 16 * (int)(blockIdx.x - state * tiles);
+  const Span s = span_of(a, (int)b);
+  const int segments = (s.len + a.seg_chunks * C - 1) / (a.seg_chunks * C);
+  if (segments <= 2) return;
+  const int64_t part = a.offsets != nullptr ? s.first / (a.seg_chunks * C) : (int64_t)b * a.segments;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
+  const int64_t matrix = (int64_t)a.Dk * a.pitch;
+  // tile i of the wave: rows 16 (wave TILES + i) + l, columns 4 g .. + 3
+  auto at = [&](int i) {
+    const int row = 16 * (wave * TILES + i) + l, col = col0 + 4 * g;
+    return row < a.Dk && col < a.pitch ? (uint32_t)(row * a.pitch + col) * 4u : kOutside;
+  };
+  auto end_of = [&](int seg) {
+    return make_rsrc(a.ends + ((part + (REVERSE ? seg - 1 : seg)) * a.H + h) * matrix, (uint32_t)matrix * 4u);
+  };
+  u32x4 E[TILES];
+  float M[TILES][STEPS][8];
+  auto fetch_tile = [&](int seg, int i) {
+    const __amdgpu_buffer_rsrc_t m = make_rsrc(a.moves + ((part + seg) * a.H + h) * a.Dk * a.move_pitch, (uint32_t)(a.Dk * a.move_pitch) * 4u);
+    E[i] = __builtin_amdgcn_raw_buffer_load_b128(end_of(seg), at(i), 0, kPlain);
+    const int row = 16 * (wave * TILES + i) + l;
+#pragma unroll
+    for (int y = 0; y < STEPS; ++y) {
+      const int from = 32 * y + 8 * g;
+      if constexpr (REVERSE) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          M[i][y][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(m, row < a.Dk && from + e < a.Dk ? (uint32_t)((from + e) * a.move_pitch + row) * 4u : kOutside, 0, kPlain));
+      } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(m, row < a.Dk && from + 4 * u < a.move_pitch ? (uint32_t)(row * a.move_pitch + from + 4 * u) * 4u : kOutside, 0, kPlain);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) M[i][y][4 * u + e] = __uint_as_float(v[e]);
+        }
+      }
+    }
+  };
+  auto seg_of = [&](int i) { return REVERSE ? segments - 1 - i : i; };
+  {
+    const __amdgpu_buffer_rsrc_t first = end_of(REVERSE ? segments - 1 : 0);
+    u32x4 S[TILES];
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) S[i] = __builtin_amdgcn_raw_buffer_load_b128(first, at(i), 0, kPlain);
+    if (kAhead)
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) fetch_tile(seg_of(1), i);
+#pragma unroll
+    for (int i = 0; i < TILES; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) lds[4 * g + r][16 * (wave * TILES + i) + l] = __uint_as_float(S[i][r]);
+  }
+  for (int i = 1; i + 1 < segments; ++i) {
+    __syncthreads();
+    b16x8 S[STEPS][kFull];
+#pragma unroll
+    for (int y = 0; y < STEPS; ++y) {
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(&lds[l][32 * y + 8 * g + 4 * u]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * u + e] = v[e];
+      }
+      split_operand<kFull>(S[y], x);
+    }
+    f32x4 next[TILES];
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      if (!kAhead) fetch_tile(seg_of(i), t);
+      next[t] = __builtin_bit_cast(f32x4, E[t]);
+#pragma unroll
+      for (int y = 0; y < STEPS; ++y) {
+        b16x8 B[kFull];
+        split_operand<kFull>(B, M[t][y]);
+        product(next[t], S[y], B);  // (columns x rows)
+      }
+    }
+    if (kAhead && i + 2 < segments)
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) fetch_tile(seg_of(i + 1), t);
+    const __amdgpu_buffer_rsrc_t end = end_of(seg_of(i));
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) lds[4 * g + r][16 * (wave * TILES + t) + l] = next[t][r];
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, next[t]), end, at(t), 0, kPlain);
+    }
+  }
+}
+
+// Backwards: leaves w and the gradients of the states behind the chunks, and
+// that of the initial state; or (ENDS) the gradients of the states that segments
+// start from, by themselves.  Grid tiles x H x segments.
+template <class E, int DKP, bool VEC, bool ENDS>
 __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(DeltaArgs a) {
   typedef Shape<E, DKP> Sh;
   typedef typename E::raw raw;
@@ -733,7 +927,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
   char *const kt = lds + Sh::kK, *const qt = lds + Sh::kQ, *const vt = lds + Sh::kV, *const mt = lds + Sh::kM,
               *const vecs = lds + Sh::kVecs;
   Where w;
-  if (!where(a, w)) return;
+  if (!where(a, a.tiles, a.by_tiles, w) || w.seg >= w.segments || (ENDS && w.seg == 0)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
   const int col = 16 * wave + l;
   const uint32_t qs = (uint32_t)a.q.token * (uint32_t)sizeof(raw), ks = (uint32_t)a.k.token * (uint32_t)sizeof(raw),
@@ -745,21 +939,30 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
   Rows<E, C, 64, 256, VEC> ro(os, w.cols, false);
   Block block;
   auto fetch = [&](int c) {
-    const int n = c < 0 ? 0 : min(C, w.s.len - c * C);
+    const int n = c < w.lo ? 0 : min(C, w.s.len - c * C);
     const int64_t t0 = n <= 0 ? 0 : (int64_t)c * C;
     rk.load(k, t0, n, ks, a.Dk, false);
     rq.load(q, t0, n, qs, a.Dk, false);
     ro.load(o, t0, n, os, w.cols, false);
-    if (n > 0) block.load(a.blocks + ((w.slot + c) * a.H + w.h) * kDeltaBlock);
+    if (n > 0) block.load(a.blocks + ((w.chunk + c) * a.H + w.h) * kDeltaBlock);
   };
-  fetch(w.chunks - 1);
+  fetch(w.hi - 1);
   const size_t head = (size_t)w.b * a.H + w.h;
-  const int pitch = (a.Dv + 3) & ~3;
-  const bool kept = w.col0 + col < pitch;
+  const int64_t matrix = (int64_t)a.Dk * a.pitch;
+  const bool kept = w.col0 + col < a.pitch, last = w.seg + 1 == w.segments;
   f32x4 R[KT];
-  load_state<KT>(R, a.ds_in != nullptr ? a.ds_in + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+  if (ENDS && !last)
+    load_state<KT>(R, nullptr, a.Dk, a.Dv, 0, false, lane);
+  else if (!ENDS && !last)
+    load_state<KT>(R, a.ends + ((w.part + w.seg) * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, col < w.cols, lane);
+  else if (!ENDS && w.segments > 1 && a.ds_in != nullptr)
+    load_state<KT>(R, a.firsts + (w.part * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, col < w.cols, lane);
+  else
+    load_state<KT>(R, a.ds_in != nullptr ? a.ds_in + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+  if (ENDS && last && a.ds_in != nullptr)
+    store_state<KT>(R, a.firsts + (w.part * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
 
-  for (int c = w.chunks - 1; c >= 0; --c) {
+  for (int c = w.hi - 1; c >= w.lo; --c) {
     rk.store(kt);
     rq.store(qt);
     ro.store(vt);
@@ -767,8 +970,8 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
     __syncthreads();
     fetch(c - 1);
     const float whole = *reinterpret_cast<const float*>(vecs + 4 * (kUp * C + C - 1));
-    const int64_t at = (w.slot + c) * a.H + w.h;
-    store_state<KT>(R, a.R + at * a.Dk * pitch, a.Dk, pitch, w.col0 + col, kept, lane);
+    const int64_t at = (w.chunk + c) * a.H + w.h;
+    if (!ENDS) store_state<KT>(R, a.R + at * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
 
     // K R
     const int rows = row_at<DKP>(l) ^ (g << 4);
@@ -777,43 +980,37 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
     for (int t = 0; t < 2; ++t) x[t] = u[t] = f32x4(0.f);
 #pragma unroll
     for (int s = 0; s < DKP / 32; ++s) {
-      b16x8 A[kFull];
+      b16x8 A[kFull], K[2][IN];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int p = 0; p < IN; ++p) K[t][p] = read_row(kt, (rows ^ (64 * s)) + p * (C * DKP * 2) + t * (32 * DKP));
       state_operand<kFull>(A, R[2 * s], R[2 * s + 1]);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        b16x8 K[IN];
-#pragma unroll
-        for (int p = 0; p < IN; ++p) K[p] = read_row(kt, (rows ^ (64 * s)) + p * (C * DKP * 2) + t * (32 * DKP));
-        product(x[t], K, A);
-      }
+      state_products<IN, false>(x, u, K, K, A);
     }
     // w = T'^T (P'^T dO + down beta K R)
     float y[8], f[8];
     b16x8 D[IN];
     read_values<E>(D, vt, wave, lane);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      b16x8 P[kFull];
-      read_transposed<kFull>(P, mt + kDeltaP, t, lane);
-      product(u[t], P, D);
-    }
-    factors(f, vecs, kInto, lane);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(f[e], x[e / 4][e % 4], u[e / 4][e % 4]);
-    b16x8 Y[kFull];
-    split_operand<kFull>(Y, y);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      b16x8 T[kFull];
-      read_transposed<kFull>(T, mt, t, lane);
-      x[t] = f32x4(0.f);
-      product(x[t], T, Y);
-    }
     {
-      float* const to = a.w + at * C * pitch + w.col0 + col;
+      b16x8 P[2][kFull], T[2][kFull], Y[kFull];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) read_transposed<kFull>(P[t], mt + kDeltaP, t, lane);
+      products<kFull, IN, 2>(u, P, D);
+      factors(f, vecs, kInto, lane);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) read_transposed<kFull>(T[t], mt, t, lane);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(f[e], x[e / 4][e % 4], u[e / 4][e % 4]);
+      split_operand<kFull>(Y, y);
+      x[0] = x[1] = f32x4(0.f);
+      products<kFull, kFull, 2>(x, T, Y);
+    }
+    if (!ENDS) {
+      float* const to = a.w + at * C * a.pitch + w.col0 + col;
       if (kept)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) to[(16 * (e / 4) + 4 * g + e % 4) * pitch] = x[e / 4][e % 4];
+        for (int e = 0; e < 8; ++e) to[(16 * (e / 4) + 4 * g + e % 4) * a.pitch] = x[e / 4][e % 4];
     }
     // R = up_C R + Q^T (scale up dO) - K^T (up w)
     b16x8 M[2][kFull];
@@ -827,17 +1024,26 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
     for (int e = 0; e < 8; ++e) y[e] = -f[e] * x[e / 4][e % 4];
     split_operand<kFull>(M[1], y);
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      b16x8 K[IN], Q[IN];
-      read_keys<E, DKP>(Q, qt, lane, t);
-      read_keys<E, DKP>(K, kt, lane, t);
-      R[t] *= whole;
-      product(R[t], Q, M[0]);
-      product(R[t], K, M[1]);
+    for (int t = 0; t < KT; t += 2) {
+      b16x8 K[2][IN], Q[2][IN];
+      f32x4 z[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        read_keys<E, DKP>(Q[i], qt, lane, t + i);
+        read_keys<E, DKP>(K[i], kt, lane, t + i);
+        z[i] = R[t + i] * whole;
+      }
+      products<IN, kFull, 2>(z, Q, M[0]);
+      products<IN, kFull, 2>(z, K, M[1]);
+      R[t] = z[0];
+      R[t + 1] = z[1];
     }
     __syncthreads();
   }
-  if (a.ds_out != nullptr) store_state<KT>(R, a.ds_out + head * a.Dk * a.Dv, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
+  if (ENDS)
+    store_state<KT>(R, a.ends + ((w.part + w.seg - 1) * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
+  else if (a.ds_out != nullptr && w.seg == 0)
+    store_state<KT>(R, a.ds_out + head * a.Dk * a.Dv, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
 }
 
 // -- the gradients of a chunk ----------------------------------------------------------------------
@@ -862,8 +1068,8 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(DeltaArgs a) {
               *const wt = lds + Sh::kW, *const scores = lds + Sh::kScores, *const vecs = lds + Sh::kVecs;
   double* const sums = reinterpret_cast<double*>(lds + Sh::kSums);
   float* const dots = reinterpret_cast<float*>(lds + Sh::kDots);  // [4 waves][4][32], then <R, S> of each wave
-  const uint32_t slot = divide(blockIdx.x, a.H, a.by_heads);
-  const int h = (int)(blockIdx.x - slot * a.H);
+  const uint32_t id = near(blockIdx.x, gridDim.x), slot = divide(id, a.H, a.by_heads);
+  const int h = (int)(id - slot * a.H);
   int b, c;
   if (!chunk_of(a, slot, b, c)) return;
   const Span s = span_of(a, b);
@@ -873,7 +1079,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(DeltaArgs a) {
   const int64_t t0 = (int64_t)c * C;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
   const int64_t at = (int64_t)slot * a.H + h;
-  const int pitch = (a.Dv + 3) & ~3;
+  const int pitch = a.pitch;
   void* const dv = const_cast<void*>(a.dv.p);
   const int64_t dv0 = base_of(a.dv, a, s, b, h) + t0 * a.dv.token;
   if (n == 0) {
@@ -1162,13 +1368,25 @@ hipError_t launch_kernel(K kernel, unsigned grid, int lds, const DeltaArgs& a, h
 
 template <class E, int DKP, bool VEC>
 hipError_t launch_shape(const DeltaArgs& a, bool backward, hipStream_t stream) {
-  const unsigned blocks = (unsigned)(a.slots * a.H), states = (unsigned)((int64_t)a.tiles * a.B * a.H);
+  const unsigned blocks = (unsigned)(a.slots * a.H), heads = (unsigned)((int64_t)a.B * a.H),
+                 pieces = (unsigned)(a.units > 0 ? (int64_t)a.units * a.H : (int64_t)heads * a.segments);
+  const unsigned columns = (unsigned)(a.pitch + 15) / 16;  // (tiles of the scan)
+  constexpr int kLds = Shape<E, DKP>::kLds;
+  const bool split = a.seg_slots > 0;
   hipError_t e = hipSuccess;
   if (blocks > 0) e = launch_kernel(delta_prepare_kernel<E, DKP, VEC, true>, (blocks + 3) / 4, 0, a, stream);
+  if (e == hipSuccess && split) {
+    e = launch_kernel(delta_forward_kernel<E, DKP, VEC, kEnds>, pieces * (a.tiles + a.move_tiles), kLds, a, stream);
+    if (e == hipSuccess && a.segments > 2) e = launch_kernel(delta_scan_kernel<DKP, false>, heads * columns, 0, a, stream);
+  }
   if (e != hipSuccess) return e;
-  if (!backward) return launch_kernel(delta_forward_kernel<E, DKP, VEC, false>, states, Shape<E, DKP>::kLds, a, stream);
-  if (blocks > 0) e = launch_kernel(delta_forward_kernel<E, DKP, VEC, true>, states, Shape<E, DKP>::kLds, a, stream);
-  if (e == hipSuccess) e = launch_kernel(delta_reverse_kernel<E, DKP, VEC>, states, Shape<E, DKP>::kLds, a, stream);
+  if (!backward) return launch_kernel(delta_forward_kernel<E, DKP, VEC, kOutputs>, pieces * a.tiles, kLds, a, stream);
+  if (blocks > 0) e = launch_kernel(delta_forward_kernel<E, DKP, VEC, kKeep>, pieces * a.tiles, kLds, a, stream);
+  if (e == hipSuccess && split) {
+    e = launch_kernel(delta_reverse_kernel<E, DKP, VEC, true>, pieces * a.tiles, kLds, a, stream);
+    if (e == hipSuccess && a.segments > 2) e = launch_kernel(delta_scan_kernel<DKP, true>, heads * columns, 0, a, stream);
+  }
+  if (e == hipSuccess) e = launch_kernel(delta_reverse_kernel<E, DKP, VEC, false>, pieces * a.tiles, kLds, a, stream);
   if (e == hipSuccess && blocks > 0) e = launch_kernel(delta_grad_kernel<E, DKP, VEC>, blocks, GradShape<E, DKP>::kLds, a, stream);
   return e;
 }

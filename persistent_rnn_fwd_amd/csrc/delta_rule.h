@@ -33,18 +33,37 @@ struct DeltaArgs {
   char* blocks;
   float *x, *w;   // backward: [slot][H][32][Dv]
   float *S, *R;   // backward: [slot][H][Dk][Dv], the states that chunks start from and the gradients of those they end with
+  // ... and by segment of a split sequence (first_segment()) and head
+  float* ends;    // [Dk][pitch]: the state a segment leaves by itself, then the sequence's; backward then its gradient
+  float* firsts;  // [Dk][pitch]: the state, or gradient, that the sequence's first, or last, segment starts from
+  float* moves;   // [Dk][Dk], rows `move_pitch` apart: what a segment makes of the identity, without values
   // set by plan_delta
-  int64_t slots;
-  int chunks;  // of the longest sequence
-  int dkp, tiles, vec;
-  int seg_tokens;  // kDeltaChunk (find_unit)
-  uint32_t by_seg, by_tiles, by_heads, by_chunks;
+  int64_t slots;      // chunks in the workspace
+  int chunks;         // of the longest sequence
+  int64_t seg_slots;  // segments in the workspace, 0: no sequence is split
+  int segments;       // of the longest sequence
+  int seg_chunks;     // chunks of a segment
+  int units;          // packed: workgroups' sequences and segments are found by number (unit_of), or 0
+  int pitch, move_pitch;
+  int dkp, tiles, move_tiles, vec;
+  uint32_t by_tiles, by_all_tiles, by_heads, by_chunks, by_segments, by_seg_chunks, by_seg_tokens;
+};
+
+// Packed sequences as find_unit() takes them: in pieces of seg_tokens.
+struct Pieces {
+  const int32_t* offsets;
+  int64_t rows;
+  int B, seg_tokens;
+  uint32_t by_seg;
 };
 
 // Chunks of all sequences: those of the longest one for each, or as many as
 // packed rows can fill (a sequence whose first row is n chunks and a rest has
 // the slots from n + b on).
-void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward);
+// Long sequences of few heads are split into segments: what a segment makes of
+// the state that it starts from is ends + moves S, both computed for all segments
+// side by side, and a scan along the sequence gives the states they start from.
+void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward, int compute_units);
 hipError_t launch_delta(const DeltaArgs& a, prnnDataType_t type, bool backward, hipStream_t stream);
 // ... of one element type (delta_f32.hip, delta_f16.hip, delta_bf16.hip)
 hipError_t launch_delta_f32(const DeltaArgs& a, bool backward, hipStream_t stream);
