@@ -187,6 +187,9 @@ void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward, int compute_un
   a->tiles = (a->Dv + 63) / 64;
   a->chunks = (int)(((int64_t)a->T + kDeltaChunk - 1) / kDeltaChunk);
   a->slots = a->T == 0 ? 0 : a->offsets != nullptr ? a->rows / kDeltaChunk + a->B : (int64_t)a->B * a->chunks;
+  a->group = 1;  // (group_chunks)
+  a->groups = (a->chunks + a->group - 1) / a->group;
+  a->group_slots = a->T == 0 ? 0 : a->offsets != nullptr ? a->rows / (a->group * kDeltaChunk) + a->B : (int64_t)a->B * a->groups;
   a->pitch = (a->Dv + 3) / 4 * 4;
   a->move_pitch = (a->Dk + 3) / 4 * 4;
   a->move_tiles = (a->Dk + 63) / 64;
@@ -209,6 +212,8 @@ void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward, int compute_un
   a->by_all_tiles = inverse_of(a->tiles + a->move_tiles);
   a->by_heads = inverse_of(a->H);
   a->by_chunks = inverse_of(std::max(1, a->chunks));
+  a->by_groups = inverse_of(std::max(1, a->groups));
+  a->by_group_tokens = inverse_of(a->group * kDeltaChunk);
   a->by_segments = inverse_of(a->segments);
   a->by_seg_chunks = inverse_of(a->seg_chunks);
   a->by_seg_tokens = inverse_of((int)tokens);
@@ -293,8 +298,8 @@ prnnStatus_t prnn_gated_delta_rule_backward(prnnHandle_t h, const prnnDeltaRule_
   plan_delta(&a, d->type, true, handle_compute_units(h));
   if (!grids_fit(a, true)) return PRNN_STATUS_NOT_SUPPORTED;
   if (a.slots > 0) {
-    const size_t blocks = (size_t)a.slots * a.H, pitch = a.pitch, tokens = rounded(blocks * kDeltaChunk * pitch * 4),
-                 states = rounded(blocks * d->Dk * pitch * 4);
+    const size_t blocks = (size_t)a.slots * a.H, groups = (size_t)a.group_slots * a.H, pitch = a.pitch,
+                 tokens = rounded(groups * a.group * kDeltaChunk * pitch * 4), states = rounded(groups * d->Dk * pitch * 4);
     void* mem = nullptr;
     const size_t segments = segment_memory(&a, nullptr);
     st = handle_workspace(h, rounded(blocks * kDeltaBlock) + 2 * (tokens + states + heads) + segments, stream, &mem);

@@ -172,6 +172,26 @@ __device__ __forceinline__ bool chunk_of(const DeltaArgs& a, uint32_t slot, int&
   return true;
 }
 
+// Chunks that the gradients are taken of at once, and whose first state (and the
+// gradient of the last one) is kept: as many as LDS holds.
+template <class E, int DKP>
+__host__ __device__ constexpr int group_chunks() {
+  return 1;
+}
+// First group of a sequence in the workspace, and a group's sequence and number in it.
+__device__ __forceinline__ int64_t first_group(const DeltaArgs& a, const Span& s, int b) {
+  return a.offsets != nullptr ? s.first / (a.group * C) + b : (int64_t)b * a.groups;
+}
+__device__ __forceinline__ bool group_of(const DeltaArgs& a, uint32_t slot, int& b, int& c) {
+  if (a.offsets != nullptr) {
+    const Pieces p = {a.offsets, a.rows, a.B, a.group * C, a.by_group_tokens};
+    return find_unit(p, slot, b, c);
+  }
+  b = (int)divide(slot, a.groups, a.by_groups);
+  c = (int)slot - b * a.groups;
+  return true;
+}
+
 // Workgroups are dealt to the 8 XCDs in turn; those of neighbouring numbers, which
 // read the same rows, go to one of them, whose L2 then has them.
 __device__ __forceinline__ uint32_t near(uint32_t id, uint32_t count) {
@@ -363,8 +383,8 @@ struct Where {
   Span s;
   int seg, segments;  // its number, and the sequence's
   int lo, hi;         // its chunks
-  int64_t chunk;      // the sequence's first chunk in the workspace
-  int64_t part;       // ... and first segment
+  int chunks;         // of the sequence
+  int64_t chunk, group, part;  // the sequence's first chunk, group and segment in the workspace
 };
 
 // tiles: column tiles of a head; the launch has as many workgroups for every
@@ -385,11 +405,12 @@ __device__ __forceinline__ bool where(const DeltaArgs& a, int tiles, uint32_t by
   w.col0 = 64 * (w.move ? tile - a.tiles : tile);
   w.cols = min(64, (w.move ? a.Dk : a.Dv) - w.col0);
   w.s = span_of(a, w.b);
-  const int chunks = (w.s.len + C - 1) / C;
-  w.segments = chunks > 0 ? (int)divide(chunks - 1, a.seg_chunks, a.by_seg_chunks) + 1 : 1;
+  w.chunks = (w.s.len + C - 1) / C;
+  w.segments = w.chunks > 0 ? (int)divide(w.chunks - 1, a.seg_chunks, a.by_seg_chunks) + 1 : 1;
   w.lo = w.seg * a.seg_chunks;
-  w.hi = min(chunks, w.lo + a.seg_chunks);
+  w.hi = min(w.chunks, w.lo + a.seg_chunks);
   w.chunk = first_chunk(a, w.s, w.b);
+  w.group = first_group(a, w.s, w.b);
   w.part = a.offsets != nullptr ? w.s.first / (a.seg_chunks * C) : (int64_t)w.b * a.segments;
   return true;
 }
@@ -629,7 +650,7 @@ template <class E, int DKP, bool VEC, Walk WALK>
 __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(DeltaArgs a) {
   typedef Shape<E, DKP> Sh;
   typedef typename E::raw raw;
-  constexpr int IN = Sh::IN, KT = Sh::KT;
+  constexpr int IN = Sh::IN, KT = Sh::KT, GROUP = group_chunks<E, DKP>();
   constexpr bool OUT = WALK == kOutputs;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char *const kt = lds + Sh::kK, *const qt = lds + Sh::kQ, *const vt = lds + Sh::kV, *const mt = lds + Sh::kM,
@@ -703,8 +724,8 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(
     __syncthreads();
     fetch(c + 1);
     const float whole = *reinterpret_cast<const float*>(vecs + 4 * (kUp * C + C - 1));
-    const int64_t at = (w.chunk + c) * a.H + w.h;
-    if constexpr (WALK == kKeep) store_state<KT>(S, a.S + at * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
+    if constexpr (WALK == kKeep)
+      if (c % GROUP == 0) store_state<KT>(S, a.S + ((w.group + c / GROUP) * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
 
     // K S and (Q S)^T
     const int rows = row_at<DKP>(l) ^ (g << 4);  // row l of a tile of 16, unit g
@@ -742,7 +763,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = x[e / 4][e % 4];
     if constexpr (WALK == kKeep) {
-      float* const to = a.x + at * C * a.pitch + w.col0 + col;
+      float* const to = a.x + (((w.group + c / GROUP) * a.H + w.h) * GROUP + c % GROUP) * C * a.pitch + w.col0 + col;
       if (kept)
 #pragma unroll
         for (int e = 0; e < 8; ++e) to[(16 * (e / 4) + 4 * g + e % 4) * a.pitch] = y[e];
@@ -922,7 +943,7 @@ template <class E, int DKP, bool VEC, bool ENDS>
 __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(DeltaArgs a) {
   typedef Shape<E, DKP> Sh;
   typedef typename E::raw raw;
-  constexpr int IN = Sh::IN, KT = Sh::KT;
+  constexpr int IN = Sh::IN, KT = Sh::KT, GROUP = group_chunks<E, DKP>();
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char *const kt = lds + Sh::kK, *const qt = lds + Sh::kQ, *const vt = lds + Sh::kV, *const mt = lds + Sh::kM,
               *const vecs = lds + Sh::kVecs;
@@ -970,8 +991,8 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
     __syncthreads();
     fetch(c - 1);
     const float whole = *reinterpret_cast<const float*>(vecs + 4 * (kUp * C + C - 1));
-    const int64_t at = (w.chunk + c) * a.H + w.h;
-    if (!ENDS) store_state<KT>(R, a.R + at * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
+    if (!ENDS && (c % GROUP == GROUP - 1 || c + 1 == w.chunks))
+      store_state<KT>(R, a.R + ((w.group + c / GROUP) * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
 
     // K R
     const int rows = row_at<DKP>(l) ^ (g << 4);
@@ -1007,7 +1028,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
       products<kFull, kFull, 2>(x, T, Y);
     }
     if (!ENDS) {
-      float* const to = a.w + at * C * a.pitch + w.col0 + col;
+      float* const to = a.w + (((w.group + c / GROUP) * a.H + w.h) * GROUP + c % GROUP) * C * a.pitch + w.col0 + col;
       if (kept)
 #pragma unroll
         for (int e = 0; e < 8; ++e) to[(16 * (e / 4) + 4 * g + e % 4) * a.pitch] = x[e / 4][e % 4];
@@ -1046,54 +1067,74 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
     store_state<KT>(R, a.ds_out + head * a.Dk * a.Dv, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
 }
 
-// -- the gradients of a chunk ----------------------------------------------------------------------
+// -- the gradients of a group of chunks ------------------------------------------------------------
 
+// Tokens of a group: its formulas are a chunk's, of 64 tokens where LDS holds them:
+// states and their gradients are then kept, and split, for every second chunk only.
+// Nothing is moved across: reads of operands ahead would take the registers of the sums.
+__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
+
+template <int DKP>
+constexpr int grad_waves() {
+  return DKP <= 128 ? 4 : 8;
+}
 template <class E, int DKP>
 struct GradShape {
-  static constexpr int IN = Parts<E>::kIn, KT = DKP / 64;  // tiles of 16 rows of the state a wave
-  static constexpr int kK = 0, kQ = 2 * C * IN * DKP, kO = 2 * kQ, kX = kO + 2 * C * IN * 64, kW = kX + 2 * C * 3 * 64,
-                       kScores = kW + 2 * C * 3 * 64, kVecs = kScores + 4 * 3 * kPart, kSums = kVecs + 5 * 4 * C,
-                       kDots = kSums + 8 * C, kLds = kDots + 4 * 4 * 4 * C + 64;
+  static constexpr int IN = Parts<E>::kIn, TC = group_chunks<E, DKP>() * C, TT = TC / 16;
+  static constexpr int WAVES = grad_waves<DKP>(), KT = DKP / 16 / WAVES;  // tiles of 16 rows of the state a wave
+  static constexpr int kPart = 2 * TC * 64;         // a part of 64 columns of TC rows
+  // k, then q; dO, x and w of 64 columns, then two matrices of scores, then the sums of the waves
+  static constexpr int kK = 0, kA = 2 * TC * IN * DKP, kO = kA, kX = kO + IN * kPart, kW = kX + 3 * kPart,
+                       kVecs = kW + 3 * kPart, kSums = kVecs + 4 * 4 * TC, kLds = kSums + 8 * TC;
+  static constexpr int kScore = 3 * 128 * TC;  // bytes of a matrix of scores: rows of 128 bytes
+  static_assert(2 * kScore <= kVecs - kA && WAVES * 16 * TC + 64 <= kVecs - kA, "overlays");
 };
+enum GradVec { kGUp, kGScaledUp, kGDown, kGBeta };
 
-// Grid slots x H.  The columns of the state are taken 64 at a time; a wave has DKP
-// / 4 of its rows.
+// Grid groups x H.  The columns of the state are taken 64 at a time; a wave has KT
+// tiles of 16 of its rows.
 template <class E, int DKP, bool VEC>
-__global__ void __launch_bounds__(256) delta_grad_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(64 * grad_waves<DKP>(), 2) delta_grad_kernel(DeltaArgs a) {
   typedef GradShape<E, DKP> Sh;
   typedef typename E::raw raw;
-  constexpr int IN = Sh::IN, KT = Sh::KT;
+  constexpr int IN = Sh::IN, KT = Sh::KT, TC = Sh::TC, TT = Sh::TT, WAVES = Sh::WAVES, THREADS = 64 * WAVES;
+  // tiles (i, j) of the scores: those with j <= i, then those above the diagonal that the products read
+  constexpr bool kAhead = false;
+  constexpr int kTiles = TT * (TT + 1) / 2, kJobs = kTiles + TT / 2, kOwn = (kJobs + WAVES - 1) / WAVES;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  char *const kt = lds + Sh::kK, *const qt = lds + Sh::kQ, *const ot = lds + Sh::kO, *const xt = lds + Sh::kX,
-              *const wt = lds + Sh::kW, *const scores = lds + Sh::kScores, *const vecs = lds + Sh::kVecs;
+  char *const kt = lds + Sh::kK, *const ot = lds + Sh::kO, *const xt = lds + Sh::kX, *const wt = lds + Sh::kW,
+              *const scores = lds + Sh::kA;
+  float* const vecs = reinterpret_cast<float*>(lds + Sh::kVecs);
   double* const sums = reinterpret_cast<double*>(lds + Sh::kSums);
-  float* const dots = reinterpret_cast<float*>(lds + Sh::kDots);  // [4 waves][4][32], then <R, S> of each wave
+  float* const dots = reinterpret_cast<float*>(lds + Sh::kA);  // [waves][4][TC], then <R, S> of each wave
   const uint32_t id = near(blockIdx.x, gridDim.x), slot = divide(id, a.H, a.by_heads);
   const int h = (int)(id - slot * a.H);
   int b, c;
-  if (!chunk_of(a, slot, b, c)) return;
+  if (!group_of(a, slot, b, c)) return;
   const Span s = span_of(a, b);
-  const int n = max(0, min(C, s.len - c * C));
-  const int all = a.lengths != nullptr ? min(C, a.T - c * C) : n;  // rows to write: padding as zeros
+  const int64_t t0 = (int64_t)c * TC;
+  const int n = (int)max((int64_t)0, min((int64_t)TC, s.len - t0));
+  const int all = a.lengths != nullptr ? (int)min((int64_t)TC, a.T - t0) : n;  // rows to write: padding as zeros
   if (all <= 0) return;
-  const int64_t t0 = (int64_t)c * C;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
   const int64_t at = (int64_t)slot * a.H + h;
   const int pitch = a.pitch;
   void* const dv = const_cast<void*>(a.dv.p);
   const int64_t dv0 = base_of(a.dv, a, s, b, h) + t0 * a.dv.token;
   if (n == 0) {
-    for (int i = threadIdx.x; i < all * a.Dv; i += 256) static_cast<raw*>(dv)[dv0 + (i / a.Dv) * a.dv.token + i % a.Dv] = E::put(0.f);
+    for (int i = threadIdx.x; i < all * a.Dv; i += THREADS) static_cast<raw*>(dv)[dv0 + (i / a.Dv) * a.dv.token + i % a.Dv] = E::put(0.f);
   }
 
   const uint32_t qs = (uint32_t)a.q.token * (uint32_t)sizeof(raw), ks = (uint32_t)a.k.token * (uint32_t)sizeof(raw),
                  os = (uint32_t)a.o.token * (uint32_t)sizeof(raw);
-  typedef Rows<E, C, 64, 256, VEC> Values;
-  typedef Rows<F32, C, 64, 256, true> Wide;
+  typedef Rows<E, TC, 64, THREADS, VEC> Values;
+  typedef Rows<F32, TC, 64, THREADS, true> Wide;
+  typedef Rows<E, TC, DKP, THREADS, VEC> Keys;
   Values ro(os, 64, false);
   Wide rx((uint32_t)pitch * 4u, 64, false), rw((uint32_t)pitch * 4u, 64, false);
+  Keys rq(qs, a.Dk, false);
   const raw* const o = static_cast<const raw*>(a.o.p) + base_of(a.o, a, s, b, h);
-  const float *const xs = a.x + at * C * pitch, *const ws = a.w + at * C * pitch;
+  const float *const xs = a.x + at * TC * pitch, *const ws = a.w + at * TC * pitch;
   auto fetch = [&](int col) {
     const int m = col < a.Dv ? n : 0;
     const int64_t first = m == 0 ? 0 : t0;
@@ -1104,200 +1145,280 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(DeltaArgs a) {
     rx.load(xs + col, 0, m, (uint32_t)pitch * 4u, min(64, pitch - col), false);
     rw.load(ws + col, 0, m, (uint32_t)pitch * 4u, min(64, pitch - col), false);
   };
-  f32x4 dq[KT][2], row[KT][2], cl[KT][2], so[1], sw[1];
+  f32x4 dq[KT][TT], row[KT][TT], cl[KT][TT], so[kOwn], sw[kOwn];
   float inner = 0.f;  // <R, S>
 #pragma unroll
   for (int i = 0; i < KT; ++i)
 #pragma unroll
-    for (int t = 0; t < 2; ++t) dq[i][t] = row[i][t] = cl[i][t] = f32x4(0.f);
-  so[0] = sw[0] = f32x4(0.f);
+    for (int t = 0; t < TT; ++t) dq[i][t] = row[i][t] = cl[i][t] = f32x4(0.f);
+#pragma unroll
+  for (int m = 0; m < kOwn; ++m) so[m] = sw[m] = f32x4(0.f);
+  int ti[kOwn], tj[kOwn];
+#pragma unroll
+  for (int m = 0; m < kOwn; ++m) {
+    const int job = wave + WAVES * m;
+    ti[m] = job >= kTiles ? 2 * (job - kTiles) : job >= 6 ? 3 : job >= 3 ? 2 : job >= 1 ? 1 : 0;
+    tj[m] = job >= kTiles ? ti[m] + 1 : job - ti[m] * (ti[m] + 1) / 2;
+  }
+  float sum[4][TT];  // of tokens 16 t + l: k.(down x R^T), q.dq, k.row, k.col
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) sum[i][t] = 0.f;
   if (n > 0) {
+    fetch(0);
     {
-      Rows<E, C, DKP, 256, VEC> rq(qs, a.Dk, false), rk(ks, a.Dk, false);
-      rq.load(static_cast<const raw*>(a.q.p) + base_of(a.q, a, s, b, h), t0, n, qs, a.Dk, false);
+      Keys rk(ks, a.Dk, false);
       rk.load(static_cast<const raw*>(a.k.p) + base_of(a.k, a, s, b, h), t0, n, ks, a.Dk, false);
-      rq.store(qt);
+      // the sums and factors of the group, from its chunks'
+      if (threadIdx.x < TC) {
+        const int t = threadIdx.x;
+        const char* const block = a.blocks + ((first_chunk(a, s, b) + c * (TC / C)) * a.H + h) * kDeltaBlock;
+        double G = reinterpret_cast<const double*>(block + kDeltaSums)[t < C ? t : C - 1], end = reinterpret_cast<const double*>(block + kDeltaSums)[C - 1];
+        float beta = t < C ? reinterpret_cast<const float*>(block + kDeltaVec)[kBeta * C + t] : 0.f;
+        if (TC > C && n > C) {
+          const char* const second = block + (int64_t)a.H * kDeltaBlock;
+          const double* const more = reinterpret_cast<const double*>(second + kDeltaSums);
+          if (t >= C) {
+            G += more[t - C];
+            beta = reinterpret_cast<const float*>(second + kDeltaVec)[kBeta * C + t - C];
+          }
+          end += more[C - 1];
+        }
+        const float up = exp_sum(G);
+        sums[t] = G;
+        vecs[kGUp * TC + t] = up;
+        vecs[kGScaledUp * TC + t] = a.scale * up;
+        vecs[kGDown * TC + t] = exp_sum(end - G);
+        vecs[kGBeta * TC + t] = beta;
+      }
       rk.store(kt);
-      const char* const block = a.blocks + at * kDeltaBlock;
-      if (threadIdx.x < 5 * C) reinterpret_cast<float*>(vecs)[threadIdx.x] = reinterpret_cast<const float*>(block + kDeltaVec)[threadIdx.x];
-      if (threadIdx.x < C) sums[threadIdx.x] = reinterpret_cast<const double*>(block + kDeltaSums)[threadIdx.x];
-      for (int i = threadIdx.x; i < 4 * 3 * kPart / 16; i += 256) reinterpret_cast<u32x4*>(scores)[i] = u32x4{0u, 0u, 0u, 0u};
     }
     const __amdgpu_buffer_rsrc_t rS = make_rsrc(a.S + at * a.Dk * pitch, (uint32_t)(a.Dk * pitch) * 4u),
                                  rR = make_rsrc(a.R + at * a.Dk * pitch, (uint32_t)(a.Dk * pitch) * 4u);
-    const int ti = (wave + 1) / 2, tj = wave / 2;  // the wave's tile of the scores (wave < 3)
-    fetch(0);
+    u32x4 fs[KT][2], fr[KT][2];
+    auto fetch_states = [&](int col) {  // 32 columns
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int dk = 16 * (wave * KT + i) + l, d = col + 8 * g + 4 * u;
+          const uint32_t from = d < pitch && dk < a.Dk ? (uint32_t)(dk * pitch + d) * 4u : kOutside;
+          fs[i][u] = __builtin_amdgcn_raw_buffer_load_b128(rS, from, 0, kPlain);
+          fr[i][u] = __builtin_amdgcn_raw_buffer_load_b128(rR, from, 0, kPlain);
+        }
+    };
+    fetch_states(0);
     for (int col = 0; col < a.Dv; col += 64) {
       ro.store(ot);
       rx.store(xt);
       rw.store(wt);
       // dv, from the registers that w came in
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int v = (int)threadIdx.x + 256 * i, r = v / 16, d = col + 4 * (v % 16);
+      for (int i = 0; i < Wide::N; ++i) {
+        const int v = (int)threadIdx.x + THREADS * i, r = v / 16, d = col + 4 * (v % 16);
         const u32x4 y = rw.v[i];
         const f32x4 z = {__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]), __uint_as_float(y[3])};
-        if (r < n) put4<E>(dv, dv0 + r * a.dv.token + d, z, a.Dv - d, false, (a.vec & 4) != 0);
-        else if (r < all) put4<E>(dv, dv0 + r * a.dv.token + d, f32x4(0.f), a.Dv - d, false, (a.vec & 4) != 0);
+        if (r < all) put4<E>(dv, dv0 + r * a.dv.token + d, r < n ? z : f32x4(0.f), a.Dv - d, false, (a.vec & 4) != 0);
       }
       __syncthreads();
-      fetch(col + 64);
+      if (kAhead) fetch(col + 64);
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         const int unit = row_at<64>(l) ^ (g << 4) ^ (64 * st);
-        b16x8 O[2][IN], X[2][kFull], W[2][kFull];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-          for (int p = 0; p < IN; ++p) O[t][p] = read_row(ot, unit + p * (C * 64 * 2) + t * (16 * 128));
-#pragma unroll
-          for (int p = 0; p < kFull; ++p) {
-            X[t][p] = read_row(xt, unit + p * (C * 64 * 2) + t * (16 * 128));
-            W[t][p] = read_row(wt, unit + p * (C * 64 * 2) + t * (16 * 128));
-          }
-        }
-        if (wave < 3) {
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int x = 0; x <= y; ++x)
-              if (y == ti && x == tj) {
-                product(so[0], O[y], X[x]);
-                product(sw[0], W[y], X[x]);
-              }
-        }
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
-          const int dk = 16 * (wave * KT + i) + l, d = col + 32 * st + 8 * g;
-          float fs[8], fr[8];
+          b16x8 A[kFull], B[kFull];
+          {
+            float x[8], y[8];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t from = d + 4 * u < pitch && dk < a.Dk ? (uint32_t)(dk * pitch + d + 4 * u) * 4u : kOutside;
-            const u32x4 y = __builtin_amdgcn_raw_buffer_load_b128(rS, from, 0, kPlain), z = __builtin_amdgcn_raw_buffer_load_b128(rR, from, 0, kPlain);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              fs[4 * u + e] = __uint_as_float(y[e]);
-              fr[4 * u + e] = __uint_as_float(z[e]);
-              inner = __builtin_fmaf(fs[4 * u + e], fr[4 * u + e], inner);
+            for (int e = 0; e < 8; ++e) {
+              x[e] = __uint_as_float(fs[i][e / 4][e % 4]);
+              y[e] = __uint_as_float(fr[i][e / 4][e % 4]);
+              inner = __builtin_fmaf(x[e], y[e], inner);
             }
+            split_operand<kFull>(A, x);
+            split_operand<kFull>(B, y);
           }
-          b16x8 A[kFull];
-          split_operand<kFull>(A, fs);
+          if (i == KT - 1) fetch_states(col + 32 * st + 32);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            product(dq[i][t], A, O[t]);
-            product(row[i][t], A, W[t]);
+          for (int t = 0; t < TT; ++t) {
+            b16x8 O[IN], X[kFull], W[kFull];
+#pragma unroll
+            for (int p = 0; p < IN; ++p) O[p] = read_row(ot, unit + p * Sh::kPart + t * (16 * 128));
+#pragma unroll
+            for (int p = 0; p < kFull; ++p) {
+              X[p] = read_row(xt, unit + p * Sh::kPart + t * (16 * 128));
+              W[p] = read_row(wt, unit + p * Sh::kPart + t * (16 * 128));
+            }
+#pragma unroll
+            for (int z = kFull - 1; z >= 0; --z)
+#pragma unroll
+              for (int y = 0; y <= z; ++y) {
+                row[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[z - y], W[y], row[i][t], 0, 0, 0);
+                cl[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B[z - y], X[y], cl[i][t], 0, 0, 0);
+                if (y < IN) dq[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[z - y], O[y < IN ? y : 0], dq[i][t], 0, 0, 0);
+              }
+            hold();
           }
-          split_operand<kFull>(A, fr);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) product(cl[i][t], A, X[t]);
         }
+#pragma unroll
+        for (int m = 0; m < kOwn; ++m)
+          if (wave + WAVES * m < kTiles) {
+            b16x8 O[IN], X[kFull], W[kFull];
+#pragma unroll
+            for (int p = 0; p < IN; ++p) O[p] = read_row(ot, unit + p * Sh::kPart + ti[m] * (16 * 128));
+#pragma unroll
+            for (int p = 0; p < kFull; ++p) {
+              X[p] = read_row(xt, unit + p * Sh::kPart + tj[m] * (16 * 128));
+              W[p] = read_row(wt, unit + p * Sh::kPart + ti[m] * (16 * 128));
+            }
+            product(so[m], O, X);
+            product(sw[m], W, X);
+            hold();
+          }
       }
       __syncthreads();
+      if (!kAhead) fetch(col + 64);
     }
+    rq.load(static_cast<const raw*>(a.q.p) + base_of(a.q, a, s, b, h), t0, n, qs, a.Dk, false);
 
-    // Y beta and -Z beta by rows i, Y and -Z by rows j
-    const float* const beta = reinterpret_cast<const float*>(vecs) + kBeta * C;
-    if (wave < 3) {
-      const int j = 16 * tj + l, i0 = 16 * ti + 4 * g;
-      float y[2][4], z[2][4];
+    // The scores as matrices in parts: rows of tokens i, each with its factor of j (`by_rows`), or
+    // rows of tokens j.  Which: Y, or -Z.
+    float decays[kOwn][4];
+#pragma unroll
+    for (int m = 0; m < kOwn; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = i0 + r;
-        const float d = j <= i ? exp_sum(sums[i] - sums[j]) : 0.f;
-        y[0][r] = j <= i ? so[0][r] * (a.scale * d) : 0.f;
-        y[1][r] = j < i ? -sw[0][r] * d : 0.f;
-        z[0][r] = y[0][r] * beta[j];
-        z[1][r] = y[1][r] * beta[j];
+        const int i = 16 * ti[m] + 4 * g + r, j = 16 * tj[m] + l;
+        decays[m][r] = wave + WAVES * m < kTiles && j <= i ? exp_sum(sums[i] - sums[j]) : 0.f;
       }
+    auto put_scores = [&](char* to, const f32x4 (&x)[kOwn], bool minus, bool by_rows) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        uint32_t words[kFull][2];
-        split<kFull, 4>(z[m], words);
-#pragma unroll
-        for (int p = 0; p < kFull; ++p)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            *reinterpret_cast<uint16_t*>(scores + (m * 3 + p) * kPart + delta_at(i0 + r, position(j))) = (uint16_t)(words[p][r / 2] >> (16 * (r % 2)));
-        split<kFull, 4>(y[m], words);
-#pragma unroll
-        for (int p = 0; p < kFull; ++p)
-          *reinterpret_cast<u32x2*>(scores + ((2 + m) * 3 + p) * kPart + delta_at(j, position(i0))) = u32x2{words[p][0], words[p][1]};
-      }
-    }
-    __syncthreads();
-  }
-
-  float sum[4][2];  // of tokens 16 t + l: k.(down x R^T), q.dq, k.row, k.col
-#pragma unroll
-  for (int i = 0; i < 4; ++i) sum[i][0] = sum[i][1] = 0.f;
-#pragma unroll
-  for (int i = 0; i < KT; ++i) {
-    const int tile = wave * KT + i, d0 = 16 * tile + 4 * g;
-    if (n > 0) {
-      // rows 4 of the tile and tokens 16 t + l of q and k
-      float fq[2][4], fk[2][4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        typedef __bf16 b16x4 __attribute__((ext_vector_type(4)));
-        const int from = (row_at<DKP>(l) ^ ((d0 >> 3) << 4)) + 2 * (d0 & 7) + t * (32 * DKP);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) fq[t][r] = fk[t][r] = 0.f;
-#pragma unroll
-        for (int p = IN - 1; p >= 0; --p) {
-          const b16x4 yq = *reinterpret_cast<const b16x4*>(qt + from + p * (C * DKP * 2)), yk = *reinterpret_cast<const b16x4*>(kt + from + p * (C * DKP * 2));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            fq[t][r] += (float)yq[r];
-            fk[t][r] += (float)yk[r];
-          }
-        }
-      }
-      // (the tile's rows are 16 tile + l here, as the products with S had them)
-      b16x8 K[IN], Q[IN];
-      {
-        const int base = row_at<DKP>(4 * g + (l >> 2)) ^ ((2 * tile + ((l & 3) >> 1)) << 4);
-#pragma unroll
-        for (int p = 0; p < IN; ++p) {
-          u32x2 yk[2], yq[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            yk[u] = read_columns(kt, base + 8 * (l & 1) + p * (C * DKP * 2) + 16 * u * (2 * DKP));
-            yq[u] = read_columns(qt, base + 8 * (l & 1) + p * (C * DKP * 2) + 16 * u * (2 * DKP));
-          }
-          const uint32_t wk[4] = {yk[0][0], yk[0][1], yk[1][0], yk[1][1]}, wq[4] = {yq[0][0], yq[0][1], yq[1][0], yq[1][1]};
-          K[p] = operand(wk);
-          Q[p] = operand(wq);
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float* const f = reinterpret_cast<const float*>(vecs) + 16 * t + l;
-        dq[i][t] *= f[kScaledUp * C];
-        row[i][t] *= -f[kUp * C];
-        cl[i][t] *= f[kDown * C];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sum[0][t] = __builtin_fmaf(fk[t][r], cl[i][t][r], sum[0][t]);
-        b16x8 M[kFull];
-        read_matrix<kFull>(M, scores, t, lane);
-        product(dq[i][t], K, M);
-        read_matrix<kFull>(M, scores + 3 * kPart, t, lane);
-        product(row[i][t], K, M);
-        read_matrix<kFull>(M, scores + 6 * kPart, t, lane);
-        product(cl[i][t], Q, M);
-        read_matrix<kFull>(M, scores + 9 * kPart, t, lane);
-        product(cl[i][t], K, M);
+      for (int m = 0; m < kOwn; ++m) {
+        if (wave + WAVES * m >= kJobs) break;
+        const int j = 16 * tj[m] + l, i0 = 16 * ti[m] + 4 * g;
+        float y[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          sum[1][t] = __builtin_fmaf(fq[t][r], dq[i][t][r], sum[1][t]);
-          sum[2][t] = __builtin_fmaf(fk[t][r], row[i][t][r], sum[2][t]);
-          sum[3][t] = __builtin_fmaf(fk[t][r], cl[i][t][r], sum[3][t]);
-          row[i][t][r] = __builtin_fmaf(f[kBeta * C], cl[i][t][r], row[i][t][r]);
+          const int i = i0 + r;
+          const float d = decays[m][r] * ((minus ? -1.f : a.scale) * (by_rows ? vecs[kGBeta * TC + j] : 1.f));
+          y[r] = j < i || (!minus && j == i) ? x[m][r] * d : 0.f;
+        }
+        uint32_t words[kFull][2];
+        split<kFull, 4>(y, words);
+#pragma unroll
+        for (int p = 0; p < kFull; ++p) {
+          if (by_rows) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              *reinterpret_cast<uint16_t*>(to + p * (128 * TC) + (row_at<64>(i0 + r) ^ ((j >> 3) << 4)) + 2 * (j & 7)) = (uint16_t)(words[p][r / 2] >> (16 * (r % 2)));
+          } else {
+            *reinterpret_cast<u32x2*>(to + p * (128 * TC) + (row_at<64>(j) ^ ((i0 >> 3) << 4)) + 2 * (i0 & 7)) = u32x2{words[p][0], words[p][1]};
+          }
         }
       }
-    }
+    };
+    // acc[i][t] += keys^T scores for the wave's rows of the state; LOWER: scores by rows i (tokens j <= i), else by rows j.
+    auto take = [&](f32x4 (&acc)[KT][TT], const char* m, bool lower) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+      for (int y = 0; y < TC / 32; ++y) {
+        b16x8 K[KT][IN];
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+          const int base = row_at<DKP>(8 * g + (l >> 2)) ^ ((2 * (wave * KT + i) + ((l & 3) >> 1)) << 4);
+#pragma unroll
+          for (int p = 0; p < IN; ++p) {
+            u32x2 half[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              half[u] = read_columns(kt, (base ^ (16 * u)) + 8 * (l & 1) + p * (TC * DKP * 2) + (32 * y + 4 * u) * (2 * DKP));
+            const uint32_t words[4] = {half[0][0], half[0][1], half[1][0], half[1][1]};
+            K[i][p] = operand(words);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          if (lower ? y > t / 2 : y < t / 2) continue;
+          b16x8 M[kFull];
+#pragma unroll
+          for (int p = 0; p < kFull; ++p) M[p] = read_row(m, p * (128 * TC) + (row_at<64>(l) ^ (g << 4) ^ (64 * y)) + t * (16 * 128));
+#pragma unroll
+          for (int i = 0; i < KT; ++i) product(acc[i][t], K[i], M);
+          hold();
+        }
+      }
+    };
+    // the values of keys at the accumulators' places: tokens 16 t + l, 4 rows of the state
+    f32x4 keys[KT][TT];
+    auto read_values_of_keys = [&]() {
+      typedef __bf16 b16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+      for (int i = 0; i < KT; ++i) {
+        const int d0 = 16 * (wave * KT + i) + 4 * g;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          keys[i][t] = f32x4(0.f);
+#pragma unroll
+          for (int p = IN - 1; p >= 0; --p) {
+            const b16x4 x = *reinterpret_cast<const b16x4*>(kt + (row_at<DKP>(l) ^ ((d0 >> 3) << 4)) + 2 * (d0 & 7) + p * (TC * DKP * 2) + t * (32 * DKP));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) keys[i][t][r] += (float)x[r];
+          }
+        }
+      }
+    };
+    auto dot = [&](float (&to)[TT], const f32x4 (&acc)[KT][TT]) {
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) to[t] = __builtin_fmaf(keys[i][t][r], acc[i][t][r], to[t]);
+    };
+    read_values_of_keys();
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const float* const f = vecs + 16 * t + l;
+#pragma unroll
+      for (int i = 0; i < KT; ++i) {
+        dq[i][t] *= f[kGScaledUp * TC];
+        row[i][t] *= -f[kGUp * TC];
+        cl[i][t] *= f[kGDown * TC];
+      }
+    }
+    dot(sum[0], cl);
+    put_scores(scores, so, false, true);
+    put_scores(scores + Sh::kScore, sw, true, true);
+    __syncthreads();
+    take(dq, scores, true);
+    take(row, scores + Sh::kScore, true);
+    dot(sum[2], row);
+    __syncthreads();
+    put_scores(scores, so, false, false);
+    put_scores(scores + Sh::kScore, sw, true, false);
+    __syncthreads();
+    take(cl, scores + Sh::kScore, false);
+    __syncthreads();
+    rq.store(kt);
+    __syncthreads();
+    take(cl, scores, false);
+    dot(sum[3], cl);
+    read_values_of_keys();
+    dot(sum[1], dq);
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) row[i][t][r] = __builtin_fmaf(vecs[kGBeta * TC + 16 * t + l], cl[i][t][r], row[i][t][r]);
+    __syncthreads();  // the scores' place is the sums'
+  }
+#pragma unroll
+  for (int i = 0; i < KT; ++i) {
+    const int d0 = 16 * (wave * KT + i) + 4 * g;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
       const int token = 16 * t + l;
       if (token < all) {
         const bool in = token < n;
@@ -1312,36 +1433,41 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < TT; ++t) {
         sum[i][t] += __shfl_xor(sum[i][t], 16);
         sum[i][t] += __shfl_xor(sum[i][t], 32);
-        if (lane < 16) dots[(wave * 4 + i) * C + 16 * t + l] = sum[i][t];
+        if (lane < 16) dots[(wave * 4 + i) * TC + 16 * t + l] = sum[i][t];
       }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) inner += __shfl_xor(inner, d);
-    if (lane == 0) dots[4 * 4 * C + wave] = inner;
+    if (lane == 0) dots[WAVES * 4 * TC + wave] = inner;
   }
   __syncthreads();
-  if (threadIdx.x < C) {
+  if (threadIdx.x < TC) {
     const int t = threadIdx.x;
     float dbeta = 0.f;
     double dg = 0.;
     if (n > 0) {
-      float y[4];
+      float y[4], rs = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = (dots[i * C + t] + dots[(4 + i) * C + t]) + (dots[(8 + i) * C + t] + dots[(12 + i) * C + t]);
-      const float* const f = reinterpret_cast<const float*>(vecs);
-      dbeta = y[3];
-      dg = t < n ? ((double)y[1] + (double)y[2]) - (double)(f[kBeta * C + t] * dbeta) : 0.;
-      double behind = t < n ? (double)(f[kBeta * C + t] * y[0]) : 0.;
+      for (int i = 0; i < 4; ++i) {
+        y[i] = 0.f;
 #pragma unroll
-      for (int d = 1; d < C; d *= 2) {
-        behind += __shfl_xor(behind, d, C);
-        const double z = __shfl_down(dg, d, C);
-        if (t + d < C) dg += z;
+        for (int m = 0; m < WAVES; ++m) y[i] += dots[(m * 4 + i) * TC + t];
       }
-      const float* const in = dots + 4 * 4 * C;
-      dg += behind + (double)f[kUp * C + C - 1] * (double)((in[0] + in[1]) + (in[2] + in[3]));
+#pragma unroll
+      for (int m = 0; m < WAVES; ++m) rs += dots[WAVES * 4 * TC + m];
+      const float beta = vecs[kGBeta * TC + t];
+      dbeta = y[3];
+      dg = t < n ? ((double)y[1] + (double)y[2]) - (double)(beta * dbeta) : 0.;
+      double behind = t < n ? (double)(beta * y[0]) : 0.;
+#pragma unroll
+      for (int d = 1; d < TC; d *= 2) {
+        behind += __shfl_xor(behind, d, TC);
+        const double z = __shfl_down(dg, d, TC);
+        if (t + d < TC) dg += z;
+      }
+      dg += behind + (double)vecs[kGUp * TC + TC - 1] * (double)rs;
       if (t == 0 && c == 0 && a.s_in == nullptr) dg = 0.;  // nothing there to decay before the first token
     }
     if (t < all) {
@@ -1355,7 +1481,7 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(DeltaArgs a) {
 // -- launches of one element type ---------------------------------------------------------------------
 
 template <class K>
-hipError_t launch_kernel(K kernel, unsigned grid, int lds, const DeltaArgs& a, hipStream_t stream) {
+hipError_t launch_kernel(K kernel, unsigned grid, int lds, const DeltaArgs& a, hipStream_t stream, int threads = 256) {
   const void* fn = reinterpret_cast<const void*>(kernel);
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -1363,7 +1489,7 @@ hipError_t launch_kernel(K kernel, unsigned grid, int lds, const DeltaArgs& a, h
   }
   DeltaArgs args = a;
   void* list[] = {&args};
-  return hipLaunchKernel(fn, dim3(grid), dim3(256), list, (size_t)lds, stream);
+  return hipLaunchKernel(fn, dim3(grid), dim3(threads), list, (size_t)lds, stream);
 }
 
 template <class E, int DKP, bool VEC>
@@ -1387,7 +1513,7 @@ hipError_t launch_shape(const DeltaArgs& a, bool backward, hipStream_t stream) {
     if (e == hipSuccess && a.segments > 2) e = launch_kernel(delta_scan_kernel<DKP, true>, heads * columns, 0, a, stream);
   }
   if (e == hipSuccess) e = launch_kernel(delta_reverse_kernel<E, DKP, VEC, false>, pieces * a.tiles, kLds, a, stream);
-  if (e == hipSuccess && blocks > 0) e = launch_kernel(delta_grad_kernel<E, DKP, VEC>, blocks, GradShape<E, DKP>::kLds, a, stream);
+  if (e == hipSuccess && blocks > 0) e = launch_kernel(delta_grad_kernel<E, DKP, VEC>, (unsigned)(a.group_slots * a.H), GradShape<E, DKP>::kLds, a, stream, 64 * GradShape<E, DKP>::WAVES);
   return e;
 }
 

@@ -31,8 +31,9 @@ struct DeltaArgs {
   int qk_f32;  // dq and dk are fp32 whatever the element type
   // workspace, by chunk ("slot") and head
   char* blocks;
-  float *x, *w;   // backward: [slot][H][32][Dv]
-  float *S, *R;   // backward: [slot][H][Dk][Dv], the states that chunks start from and the gradients of those they end with
+  // ... backward, by group of chunks (see delta_grad_kernel) and head:
+  float *x, *w;   // [tokens][pitch]
+  float *S, *R;   // [Dk][pitch], the state that the group starts from and the gradient of the one it ends with
   // ... and by segment of a split sequence (first_segment()) and head
   float* ends;    // [Dk][pitch]: the state a segment leaves by itself, then the sequence's; backward then its gradient
   float* firsts;  // [Dk][pitch]: the state, or gradient, that the sequence's first, or last, segment starts from
@@ -40,13 +41,16 @@ struct DeltaArgs {
   // set by plan_delta
   int64_t slots;      // chunks in the workspace
   int chunks;         // of the longest sequence
+  int group, groups;  // chunks of a group; groups of the longest sequence
+  int64_t group_slots;  // groups in the workspace
   int64_t seg_slots;  // segments in the workspace, 0: no sequence is split
   int segments;       // of the longest sequence
   int seg_chunks;     // chunks of a segment
   int units;          // packed: workgroups' sequences and segments are found by number (unit_of), or 0
   int pitch, move_pitch;
   int dkp, tiles, move_tiles, vec;
-  uint32_t by_tiles, by_all_tiles, by_heads, by_chunks, by_segments, by_seg_chunks, by_seg_tokens;
+  uint32_t by_tiles, by_all_tiles, by_heads, by_chunks, by_segments, by_seg_chunks, by_seg_tokens, by_groups,
+      by_group_tokens;
 };
 
 // Packed sequences as find_unit() takes them: in pieces of seg_tokens.
