@@ -289,7 +289,8 @@ struct Rows {
   __device__ __forceinline__ void load(const void* p, int64_t t0, int n, uint32_t stride, int cols, bool reverse) {
     const __amdgpu_buffer_rsrc_t r = make_rsrc(
         static_cast<const char*>(p) + t0 * (int64_t)stride,
-        n > 0 ? (uint32_t)(n - 1) * stride + (uint32_t)cols * (uint32_t)sizeof(raw) : 0u);
+        // (in a scalar register, or the loads go round a loop over their lanes' buffers)
+        (uint32_t)__builtin_amdgcn_readfirstlane(n > 0 ? (uint32_t)(n - 1) * stride + (uint32_t)cols * (uint32_t)sizeof(raw) : 0u));
     if (VEC && n == C) {
       int at = (int)whole;
       keep(at);

@@ -2,6 +2,7 @@
 #include "delta_rule.h"
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <initializer_list>
@@ -187,17 +188,22 @@ void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward, int compute_un
   a->tiles = (a->Dv + 63) / 64;
   a->chunks = (int)(((int64_t)a->T + kDeltaChunk - 1) / kDeltaChunk);
   a->slots = a->T == 0 ? 0 : a->offsets != nullptr ? a->rows / kDeltaChunk + a->B : (int64_t)a->B * a->chunks;
-  a->group = 1;  // (group_chunks)
+  a->group = a->dkp == 128 && type != PRNN_DATA_FLOAT ? 2 : 1;  // (group_chunks)
   a->groups = (a->chunks + a->group - 1) / a->group;
   a->group_slots = a->T == 0 ? 0 : a->offsets != nullptr ? a->rows / (a->group * kDeltaChunk) + a->B : (int64_t)a->B * a->groups;
   a->pitch = (a->Dv + 3) / 4 * 4;
   a->move_pitch = (a->Dk + 3) / 4 * 4;
   a->move_tiles = (a->Dk + 63) / 64;
-  // Segments: as many as give each compute unit 2 workgroups, of at least 4 chunks,
-  // and no split in less than 3.
+  // Segments: as many as give each compute unit 2 workgroups, of at least 4 chunks, and
+  // no more than the root of the chunks (64 rows: twice that), since a step of the scan costs about
+  // as much as a chunk.  A split in 2 gains nothing.  Measured in 1 / 4 / 8 / 12 / 16
+  // segments: 32768 bf16 tokens of 32 heads of 128 2503 / 1303 / 1135 / 1121 / 1141 us,
+  // gradients of 3 x 1531 fp16 tokens of 6 heads of 96 x 80 339 / 234 / 218 / 214 / 238 (in
+  // 6 202), 4 x 256 fp32 tokens of 14 heads of 128 53 / 71 (in 4).
   const int64_t sequences = a->offsets != nullptr && a->T > 0 ? std::max<int64_t>(1, std::min<int64_t>(a->B, a->rows / a->T)) : a->B;
   const int64_t states = std::max<int64_t>(1, sequences * a->H * a->tiles);
-  int64_t segments = std::min<int64_t>(2 * compute_units / states, a->chunks / 4);
+  int64_t segments = std::min<int64_t>(2 * compute_units / states, (int64_t)(std::sqrt((double)a->chunks) * (a->dkp == 64 ? 2 : 1)));
+  segments = std::min<int64_t>(segments, a->chunks / 4);
   if (segments < 3) segments = 1;
   a->seg_chunks = std::max(1, (int)((a->chunks + segments - 1) / segments));
   a->segments = std::max(1, (a->chunks + a->seg_chunks - 1) / a->seg_chunks);

@@ -46,6 +46,8 @@
 // every gradient of its sequence and head NaN.)
 #pragma once
 
+#include <type_traits>
+
 #include "attention_chunk.h"
 #include "delta_rule.h"
 
@@ -53,6 +55,12 @@ namespace prnn {
 namespace delta {
 
 using namespace attn;
+
+// Element offset of token 0 of sequence b, head h, of an operand (all the same in every lane).
+__device__ __forceinline__ int64_t base_of(const AttnOperand& x, const DeltaArgs& a, const Span& s, int b, int h) {
+  const int head = __builtin_amdgcn_readfirstlane((int)divide((uint32_t)h, (uint32_t)x.group, x.inverse));
+  return (a.offsets != nullptr ? s.first * x.token : (int64_t)b * x.batch) + (int64_t)head * x.head;
+}
 
 constexpr int C = kDeltaChunk;
 
@@ -86,51 +94,55 @@ __device__ __forceinline__ void read_transposed(b16x8 (&x)[P], const char* m, in
   }
 }
 
-// 8 values of a row as an operand, zeros where the row or a column does not
-// exist.  row: its byte offset, or kOutside.
+// 8 values of a row, zeros where the row or a column does not exist, on their
+// way to an operand.  row: its byte offset, or kOutside.
 template <class E, bool VEC>
-__device__ __forceinline__ void load_operand(b16x8 (&f)[Parts<E>::kIn], __amdgpu_buffer_rsrc_t r, uint32_t row, int col, int cols) {
+struct RowPart {
   typedef typename E::raw raw;
-  constexpr int IN = Parts<E>::kIn;
+  static constexpr int IN = Parts<E>::kIn;
   uint32_t w[IN == 3 ? 8 : 4];
-  if constexpr (VEC) {
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, int col, int cols) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < (IN == 3 ? 2 : 1); ++i) {
-      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, col + 4 * i < cols ? row + (uint32_t)((col + 4 * i) * (int)sizeof(raw)) : kOutside, 0, kPlain);
+      for (int i = 0; i < (IN == 3 ? 2 : 1); ++i) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, col + 4 * i < cols ? row + (uint32_t)((col + 4 * i) * (int)sizeof(raw)) : kOutside, 0, kPlain);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[4 * i + e] = v[e];
-    }
-  } else {
-    uint32_t e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t at = col + i < cols ? row + (uint32_t)((col + i) * (int)sizeof(raw)) : kOutside;
-      e[i] = sizeof(raw) == 4 ? __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, kPlain)
-                              : (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, kPlain);
-    }
-#pragma unroll
-    for (int i = 0; i < (IN == 3 ? 8 : 4); ++i) w[i] = IN == 3 ? e[i % 8] : e[2 * i % 8] | e[(2 * i + 1) % 8] << 16;
-  }
-  if constexpr (IN == 1) {
-    f[0] = operand(w);
-  } else {
-    float x[8];
-    if constexpr (IN == 2) {
-      typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-      const u32x4 v = {w[0], w[1], w[2], w[3]};
-      const f16x8 h = __builtin_bit_cast(f16x8, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = (float)h[i];
+        for (int e = 0; e < 4; ++e) w[4 * i + e] = v[e];
+      }
     } else {
+      uint32_t e[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t at = col + i < cols ? row + (uint32_t)((col + i) * (int)sizeof(raw)) : kOutside;
+        e[i] = sizeof(raw) == 4 ? __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, kPlain)
+                                : (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, kPlain);
+      }
+#pragma unroll
+      for (int i = 0; i < (IN == 3 ? 8 : 4); ++i) w[i] = IN == 3 ? e[i % 8] : e[2 * i % 8] | e[(2 * i + 1) % 8] << 16;
     }
-    uint32_t words[IN][4];
-    split<IN, 8>(x, words);
-#pragma unroll
-    for (int p = 0; p < IN; ++p) f[p] = operand(words[p]);
   }
-}
+  __device__ __forceinline__ void take(b16x8 (&f)[IN]) const {
+    if constexpr (IN == 1) {
+      f[0] = operand(w);
+    } else {
+      float x[8];
+      if constexpr (IN == 2) {
+        typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+        const u32x4 v = {w[0], w[1], w[2], w[3]};
+        const f16x8 h = __builtin_bit_cast(f16x8, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (float)h[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+      }
+      uint32_t words[IN][4];
+      split<IN, 8>(x, words);
+#pragma unroll
+      for (int p = 0; p < IN; ++p) f[p] = operand(words[p]);
+    }
+  }
+};
 
 template <int P>
 __device__ __forceinline__ void split_operand(b16x8 (&f)[P], const float (&x)[8]) {
@@ -158,6 +170,10 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// A number that is the same in every lane, in a scalar register: the addresses and
+// buffers made of it are too (else every access goes round a loop over its lanes' buffers).
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // First chunk of a sequence in the workspace, and a chunk's sequence and number in it.
 __device__ __forceinline__ int64_t first_chunk(const DeltaArgs& a, const Span& s, int b) {
   return a.offsets != nullptr ? s.first / C + b : (int64_t)b * a.chunks;
@@ -165,9 +181,12 @@ __device__ __forceinline__ int64_t first_chunk(const DeltaArgs& a, const Span& s
 __device__ __forceinline__ bool chunk_of(const DeltaArgs& a, uint32_t slot, int& b, int& c) {
   if (a.offsets != nullptr) {
     const Pieces p = {a.offsets, a.rows, a.B, C, 0xffffffffu / C + 1};
-    return find_unit(p, slot, b, c);
+    const bool found = find_unit(p, slot, b, c);
+    b = scalar(b);
+    c = scalar(c);
+    return found;
   }
-  b = (int)divide(slot, a.chunks, a.by_chunks);
+  b = scalar((int)divide(slot, a.chunks, a.by_chunks));
   c = (int)slot - b * a.chunks;
   return true;
 }
@@ -176,7 +195,7 @@ __device__ __forceinline__ bool chunk_of(const DeltaArgs& a, uint32_t slot, int&
 // gradient of the last one) is kept: as many as LDS holds.
 template <class E, int DKP>
 __host__ __device__ constexpr int group_chunks() {
-  return 1;
+  return DKP == 128 && E::id != PRNN_DATA_FLOAT ? 2 : 1;
 }
 // First group of a sequence in the workspace, and a group's sequence and number in it.
 __device__ __forceinline__ int64_t first_group(const DeltaArgs& a, const Span& s, int b) {
@@ -185,9 +204,12 @@ __device__ __forceinline__ int64_t first_group(const DeltaArgs& a, const Span& s
 __device__ __forceinline__ bool group_of(const DeltaArgs& a, uint32_t slot, int& b, int& c) {
   if (a.offsets != nullptr) {
     const Pieces p = {a.offsets, a.rows, a.B, a.group * C, a.by_group_tokens};
-    return find_unit(p, slot, b, c);
+    const bool found = find_unit(p, slot, b, c);
+    b = scalar(b);
+    c = scalar(c);
+    return found;
   }
-  b = (int)divide(slot, a.groups, a.by_groups);
+  b = scalar((int)divide(slot, a.groups, a.by_groups));
   c = (int)slot - b * a.groups;
   return true;
 }
@@ -197,6 +219,19 @@ __device__ __forceinline__ bool group_of(const DeltaArgs& a, uint32_t slot, int&
 __device__ __forceinline__ uint32_t near(uint32_t id, uint32_t count) {
   const uint32_t whole = count / 8 * 8;
   return id < whole ? id % 8 * (whole / 8) + id / 8 : id;
+}
+
+// acc += x y for single accumulators.
+template <int NX, int NY>
+__device__ __forceinline__ void product(f32x4& acc, const b16x8 (&x)[NX], const b16x8 (&y)[NY]) {
+#pragma unroll
+  for (int s = kFull - 1; s >= 0; --s)  // small terms first
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int j = s - i;
+      if (j < 0 || j >= NY) continue;
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[j], acc, 0, 0, 0);
+    }
 }
 
 // -- what depends on no state ------------------------------------------------------------------
@@ -213,7 +248,7 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
   __shared__ float betas[4][C];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
   const uint32_t id = blockIdx.x * 4 + wave;
-  const uint32_t slot = divide(id, a.H, a.by_heads);
+  const uint32_t slot = scalar((int)divide(id, a.H, a.by_heads));
   const int h = (int)(id - slot * a.H);
   int b, c;
   if (slot >= (uint32_t)a.slots || !chunk_of(a, slot, b, c)) return;
@@ -224,14 +259,35 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
   char* const block = a.blocks + ((int64_t)slot * a.H + h) * kDeltaBlock;
   const int64_t t0 = (int64_t)c * C;
 
-  // the decays' sums, and the factors
+  // The rows of k and q, as much as registers hold of them at once before anything
+  // waits: where there are few chunks, a trip to memory is most of what this launch takes.
+  constexpr int kAhead = VEC ? (DKP / 32 < 4 ? DKP / 32 : 4) : 1;
+  const uint32_t ks = (uint32_t)a.k.token * (uint32_t)sizeof(raw), qs = (uint32_t)a.q.token * (uint32_t)sizeof(raw);
+  const __amdgpu_buffer_rsrc_t rk = make_rsrc(
+      static_cast<const raw*>(a.k.p) + base_of(a.k, a, s, b, h) + t0 * a.k.token, (uint32_t)scalar((n - 1) * (int)ks + a.Dk * (int)sizeof(raw)));
+  const __amdgpu_buffer_rsrc_t rq = make_rsrc(
+      static_cast<const raw*>(a.q.p) + base_of(a.q, a, s, b, h) + t0 * a.q.token, (uint32_t)scalar((n - 1) * (int)qs + a.Dk * (int)sizeof(raw)));
+  RowPart<E, VEC> pk[kAhead][2], pq[kAhead][2];
+  auto fetch = [&](int d) {
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int row = 16 * x + l;
+        pk[y][x].load(rk, row < n ? row * ks : kOutside, d + 32 * y + 8 * g, a.Dk);
+        if (PAIRS) pq[y][x].load(rq, row < n ? row * qs : kOutside, d + 32 * y + 8 * g, a.Dk);
+      }
+  };
+  float log_decay = 0.f, beta = 0.f;
   const int t = lane & 31;
-  double G = 0.;
-  float beta = 0.f;
   if (t < n) {
-    if (a.g.p != nullptr) G = summand(static_cast<const float*>(a.g.p)[base_of(a.g, a, s, b, h) + (t0 + t) * a.g.token]);
+    if (a.g.p != nullptr) log_decay = static_cast<const float*>(a.g.p)[base_of(a.g, a, s, b, h) + (t0 + t) * a.g.token];
     beta = static_cast<const float*>(a.beta.p)[base_of(a.beta, a, s, b, h) + (t0 + t) * a.beta.token];
   }
+  fetch(0);
+
+  // the decays' sums, and the factors
+  double G = summand(log_decay);
 #pragma unroll
   for (int d = 1; d < C; d *= 2) {
     const double y = __shfl_up(G, d, C);
@@ -257,36 +313,21 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
   f32x4 kk[3], qk[3];  // (ti, tj) = (0, 0), (1, 0), (1, 1)
 #pragma unroll
   for (int x = 0; x < 3; ++x) kk[x] = qk[x] = f32x4(0.f);
-  {
-    const uint32_t ks = (uint32_t)a.k.token * (uint32_t)sizeof(raw), qs = (uint32_t)a.q.token * (uint32_t)sizeof(raw);
-    const __amdgpu_buffer_rsrc_t rk = make_rsrc(
-        static_cast<const raw*>(a.k.p) + base_of(a.k, a, s, b, h) + t0 * a.k.token, (uint32_t)(n - 1) * ks + (uint32_t)(a.Dk * (int)sizeof(raw)));
-    const __amdgpu_buffer_rsrc_t rq = make_rsrc(
-        static_cast<const raw*>(a.q.p) + base_of(a.q, a, s, b, h) + t0 * a.q.token, (uint32_t)(n - 1) * qs + (uint32_t)(a.Dk * (int)sizeof(raw)));
-    for (int d = 0; d < a.Dk; d += 32) {
+  for (int d = 0; d < a.Dk; d += 32 * kAhead) {
+    if (d > 0) fetch(d);
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
       b16x8 K[2][IN], Q[2][IN];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int row = 16 * x + l;
-        load_operand<E, VEC>(K[x], rk, row < n ? row * ks : kOutside, d + 8 * g, a.Dk);
-        if (PAIRS) load_operand<E, VEC>(Q[x], rq, row < n ? row * qs : kOutside, d + 8 * g, a.Dk);
+        pk[y][x].take(K[x]);
+        if (PAIRS) pq[y][x].take(Q[x]);
       }
 #pragma unroll
       for (int x = 0; x < 3; ++x) {
         const int ti = (x + 1) / 2, tj = x / 2;
-        f32x4 y[1] = {kk[x]};
-        b16x8 Y[1][IN];
-#pragma unroll
-        for (int p = 0; p < IN; ++p) Y[0][p] = K[ti][p];
-        products<IN, IN, 1>(y, K[tj], Y);
-        kk[x] = y[0];
-        if (PAIRS) {
-          y[0] = qk[x];
-#pragma unroll
-          for (int p = 0; p < IN; ++p) Y[0][p] = Q[ti][p];
-          products<IN, IN, 1>(y, K[tj], Y);
-          qk[x] = y[0];
-        }
+        product(kk[x], K[tj], K[ti]);
+        if (PAIRS) product(qk[x], K[tj], Q[ti]);
       }
     }
   }
@@ -368,11 +409,12 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
 
 // -- the walk along a sequence --------------------------------------------------------------------
 
-template <class E, int DKP>
+// QUERIES: with q and P'.
+template <class E, int DKP, bool QUERIES>
 struct Shape {
   static constexpr int IN = Parts<E>::kIn, KT = DKP / 16, kTile = 2 * C * IN;  // bytes of a tile's column
-  static constexpr int kK = 0, kQ = kTile * DKP, kV = 2 * kTile * DKP, kM = kV + kTile * 64;
-  static constexpr int kVecs = kM + 2 * 3 * kPart, kLds = kVecs + 5 * 4 * C;
+  static constexpr int kK = 0, kQ = kTile * DKP, kV = kQ + (QUERIES ? kTile * DKP : 0), kM = kV + kTile * 64;
+  static constexpr int kVecs = kM + (QUERIES ? 2 : 1) * 3 * kPart, kLds = kVecs + 5 * 4 * C;
 };
 
 // What a workgroup works on: 64 columns of one head's state, or of what a segment
@@ -390,15 +432,17 @@ struct Where {
 // tiles: column tiles of a head; the launch has as many workgroups for every
 // head and segment.
 __device__ __forceinline__ bool where(const DeltaArgs& a, int tiles, uint32_t by_tiles, Where& w) {
-  const uint32_t id = near(blockIdx.x, gridDim.x), state = divide(id, tiles, by_tiles);
+  const uint32_t id = near(blockIdx.x, gridDim.x), state = scalar((int)divide(id, tiles, by_tiles));
   const int tile = (int)(id - state * tiles);
-  const uint32_t piece = divide(state, a.H, a.by_heads);
+  const uint32_t piece = scalar((int)divide(state, a.H, a.by_heads));
   w.h = (int)(state - piece * a.H);
   if (a.units > 0) {
     const Pieces p = {a.offsets, a.rows, a.B, a.seg_chunks * C, a.by_seg_tokens};
     if (!find_unit(p, piece, w.b, w.seg)) return false;
+    w.b = scalar(w.b);
+    w.seg = scalar(w.seg);
   } else {
-    w.b = (int)divide(piece, a.segments, a.by_segments);
+    w.b = scalar((int)divide(piece, a.segments, a.by_segments));
     w.seg = (int)piece - w.b * a.segments;
   }
   w.move = tile >= a.tiles;
@@ -406,7 +450,7 @@ __device__ __forceinline__ bool where(const DeltaArgs& a, int tiles, uint32_t by
   w.cols = min(64, (w.move ? a.Dk : a.Dv) - w.col0);
   w.s = span_of(a, w.b);
   w.chunks = (w.s.len + C - 1) / C;
-  w.segments = w.chunks > 0 ? (int)divide(w.chunks - 1, a.seg_chunks, a.by_seg_chunks) + 1 : 1;
+  w.segments = w.chunks > 0 ? scalar((int)divide(w.chunks - 1, a.seg_chunks, a.by_seg_chunks)) + 1 : 1;
   w.lo = w.seg * a.seg_chunks;
   w.hi = min(w.chunks, w.lo + a.seg_chunks);
   w.chunk = first_chunk(a, w.s, w.b);
@@ -453,18 +497,55 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[KT], float* p, int 
     for (int r = 0; r < 4; ++r) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[t][r]), x.rsrc, x.at(t, r), 0, kPlain);
 }
 
+// 4 x 4 values of 4 neighbouring lanes, transposed: lane i's value j becomes lane j's i.
+__device__ __forceinline__ f32x4 transposed(const f32x4& x, int lane) {
+  auto from = [](float v, auto way) { return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), decltype(way)::value, 0xF, 0xF, false)); };
+  const std::integral_constant<int, 0xB1> beside;   // lane ^ 1
+  const std::integral_constant<int, 0x4E> across;   // lane ^ 2
+  const bool odd = lane & 1, high = lane & 2;
+  // (every lane exchanges, then chooses)
+  const float b0 = from(x[0], beside), b1 = from(x[1], beside), b2 = from(x[2], beside), b3 = from(x[3], beside);
+  const float a0 = odd ? b1 : x[0], a1 = odd ? x[1] : b0, a2 = odd ? b3 : x[2], a3 = odd ? x[3] : b2;
+  const float c0 = from(a0, across), c1 = from(a1, across), c2 = from(a2, across), c3 = from(a3, across);
+  return f32x4{high ? c2 : a0, high ? c3 : a1, high ? a2 : c0, high ? a3 : c1};
+}
+
+// A state into the workspace, rows `pitch` (a multiple of 4) apart from `p` on, 16
+// bytes a lane: columns col0 + 16 wave .. + 15 of it.  Stored 4 bytes a lane it
+// takes four times the accesses, as many as the rest of a chunk's work takes time.
+template <int KT>
+__device__ __forceinline__ void keep_state(const f32x4 (&S)[KT], float* p, int Dk, int pitch, int col0, int lane) {
+  const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(p, (uint32_t)(Dk * pitch) * 4u);
+  const int col = col0 + (lane & 12), row = 8 * (lane >> 4) + (lane & 3);
+  const int rows = col < pitch ? Dk - row : 0, first = (row * pitch + col) * 4;
+#pragma unroll
+  for (int t = 0; t < KT; ++t) {
+    const int to = 32 * (t / 2) + 4 * (t % 2);
+    const f32x4 y = transposed(S[t], lane);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), rsrc, to < rows ? (uint32_t)(first + to * pitch * 4) : kOutside, 0, kPlain);
+  }
+}
+
 // The chunk's matrices and factors on their way from the workspace to LDS.
+// (PAIRS: P' too; T' alone leaves half of the last round's threads to the factors.)
+template <bool PAIRS>
 struct Block {
-  u32x4 m[3], f;
+  static constexpr int kUnits = (PAIRS ? 2 : 1) * 3 * kPart / 16, kWhole = kUnits / 256, kRest = kUnits % 256, kFactors = 5 * C / 4;
+  u32x4 m[kWhole], f;
   __device__ __forceinline__ void load(const char* p) {
 #pragma unroll
-    for (int i = 0; i < 3; ++i) m[i] = reinterpret_cast<const u32x4*>(p)[i * 256 + threadIdx.x];
-    if (threadIdx.x < 5 * C / 4) f = reinterpret_cast<const u32x4*>(p + kDeltaVec)[threadIdx.x];
+    for (int i = 0; i < kWhole; ++i) m[i] = reinterpret_cast<const u32x4*>(p)[i * 256 + threadIdx.x];
+    if ((int)threadIdx.x < kRest)
+      f = reinterpret_cast<const u32x4*>(p)[kWhole * 256 + threadIdx.x];
+    else if ((int)threadIdx.x < kRest + kFactors)
+      f = reinterpret_cast<const u32x4*>(p + kDeltaVec)[threadIdx.x - kRest];
   }
   __device__ __forceinline__ void store(char* matrices, char* vecs) const {
 #pragma unroll
-    for (int i = 0; i < 3; ++i) reinterpret_cast<u32x4*>(matrices)[i * 256 + threadIdx.x] = m[i];
-    if (threadIdx.x < 5 * C / 4) reinterpret_cast<u32x4*>(vecs)[threadIdx.x] = f;
+    for (int i = 0; i < kWhole; ++i) reinterpret_cast<u32x4*>(matrices)[i * 256 + threadIdx.x] = m[i];
+    // (the factors lie behind the matrices)
+    if ((int)threadIdx.x < kRest + kFactors) reinterpret_cast<u32x4*>(matrices)[kWhole * 256 + threadIdx.x] = f;
+    (void)vecs;
   }
 };
 
@@ -516,19 +597,6 @@ __device__ __forceinline__ void read_keys(b16x8 (&K)[Parts<E>::kIn], const char*
     const uint32_t words[4] = {half[0][0], half[0][1], half[1][0], half[1][1]};
     K[p] = operand(words);
   }
-}
-
-// acc += x y for single accumulators.
-template <int NX, int NY>
-__device__ __forceinline__ void product(f32x4& acc, const b16x8 (&x)[NX], const b16x8 (&y)[NY]) {
-#pragma unroll
-  for (int s = kFull - 1; s >= 0; --s)  // small terms first
-#pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      const int j = s - i;
-      if (j < 0 || j >= NY) continue;
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[j], acc, 0, 0, 0);
-    }
 }
 
 template <int P>
@@ -647,11 +715,11 @@ enum Walk { kOutputs, kKeep, kEnds };
 
 // Forward: grid tiles (kEnds: and move tiles) x H x segments.
 template <class E, int DKP, bool VEC, Walk WALK>
-__global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(DeltaArgs a) {
-  typedef Shape<E, DKP> Sh;
+__global__ void __launch_bounds__(256, DKP == 256 ? 1 : WALK == kOutputs && VEC && E::id != PRNN_DATA_FLOAT ? 3 : 2) delta_forward_kernel(DeltaArgs a) {
+  constexpr bool OUT = WALK == kOutputs;
+  typedef Shape<E, DKP, OUT> Sh;
   typedef typename E::raw raw;
   constexpr int IN = Sh::IN, KT = Sh::KT, GROUP = group_chunks<E, DKP>();
-  constexpr bool OUT = WALK == kOutputs;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char *const kt = lds + Sh::kK, *const qt = lds + Sh::kQ, *const vt = lds + Sh::kV, *const mt = lds + Sh::kM,
               *const vecs = lds + Sh::kVecs;
@@ -676,16 +744,22 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(
   const int vcols = w.move ? 0 : w.cols;  // (moves: values of zeros)
   Rows<E, C, DKP, 256, VEC> rq(qs, a.Dk, false), rk(ks, a.Dk, false);
   Rows<E, C, 64, 256, VEC> rv(vs, vcols, false);
-  Block block;
+  Block<OUT> block;
+  // (in two parts: all at once they fill the queue of the unit's loads, and the waves wait to issue them)
   auto fetch = [&](int c) {
     const int n = c < w.hi ? min(C, w.s.len - c * C) : 0;
     const int64_t t0 = n == 0 ? 0 : (int64_t)c * C;
     rk.load(k, t0, n, ks, a.Dk, false);
     if (OUT) rq.load(q, t0, n, qs, a.Dk, false);
+  };
+  auto fetch_rest = [&](int c) {
+    const int n = c < w.hi ? min(C, w.s.len - c * C) : 0;
+    const int64_t t0 = n == 0 ? 0 : (int64_t)c * C;
     rv.load(v, t0, n, vs, vcols, false);
     if (n > 0) block.load(a.blocks + ((w.chunk + c) * a.H + w.h) * kDeltaBlock);
   };
   fetch(w.lo);
+  fetch_rest(w.lo);
   const size_t head = (size_t)w.b * a.H + w.h;
   const int64_t matrix = (int64_t)a.Dk * a.pitch;
   const bool split = w.segments > 1;
@@ -710,9 +784,9 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(
   };
   f32x4 S[KT];
   start(S);
-  const bool kept = w.col0 + col < a.pitch;  // (columns of padding hold zeros)
+  const bool kept = w.col0 + col < a.pitch;
   if (WALK == kEnds && w.seg == 0 && a.s_in != nullptr)
-    store_state<KT>(S, a.firsts + (w.part * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
+    keep_state<KT>(S, a.firsts + (w.part * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + 16 * wave, lane);
   bool broken = false;
 
   for (int c = w.lo; c < w.hi; ++c) {
@@ -723,9 +797,12 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(
     block.store(mt, vecs);
     __syncthreads();
     fetch(c + 1);
-    const float whole = *reinterpret_cast<const float*>(vecs + 4 * (kUp * C + C - 1));
-    if constexpr (WALK == kKeep)
+    if constexpr (WALK == kKeep) {
+      // (the stores behind all loads: what waits for a load waits for the stores before it)
+      fetch_rest(c + 1);
       if (c % GROUP == 0) store_state<KT>(S, a.S + ((w.group + c / GROUP) * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
+    }
+    const float whole = *reinterpret_cast<const float*>(vecs + 4 * (kUp * C + C - 1));
 
     // K S and (Q S)^T
     const int rows = row_at<DKP>(l) ^ (g << 4);  // row l of a tile of 16, unit g
@@ -745,6 +822,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(
       state_operand<kFull>(A, S[2 * s], S[2 * s + 1]);
       state_products<IN, OUT>(x, O, K, Q, A);
     }
+    if (WALK != kKeep) fetch_rest(c + 1);
     // x = T' (v - up K S)
     float y[8], f[8];
     {
@@ -825,9 +903,9 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_forward_kernel(
   } else if constexpr (WALK == kEnds) {
     const int64_t part = (w.part + w.seg) * a.H + w.h;
     if (w.move)
-      store_state<KT>(S, a.moves + part * a.Dk * a.move_pitch, a.Dk, a.move_pitch, w.col0 + col, w.col0 + col < a.move_pitch, lane);
+      keep_state<KT>(S, a.moves + part * a.Dk * a.move_pitch, a.Dk, a.move_pitch, w.col0 + 16 * wave, lane);
     else
-      store_state<KT>(S, a.ends + part * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
+      keep_state<KT>(S, a.ends + part * matrix, a.Dk, a.pitch, w.col0 + 16 * wave, lane);
   }
 }
 
@@ -843,7 +921,7 @@ __global__ void __launch_bounds__(256) delta_scan_kernel(DeltaArgs a) {
   constexpr bool kAhead = DKP <= 128;  // (registers)
   __shared__ __attribute__((aligned(16))) float lds[16][kRow];
   const uint32_t tiles = (uint32_t)(a.pitch + 15) / 16u, state = blockIdx.x / tiles;
-  const uint32_t b = divide(state, a.H, a.by_heads);
+  const uint32_t b = scalar((int)divide(state, a.H, a.by_heads));
   const int h = (int)(state - b * a.H), col0 = 16 * (int)(blockIdx.x - state * tiles);
   const Span s = span_of(a, (int)b);
   const int segments = (s.len + a.seg_chunks * C - 1) / (a.seg_chunks * C);
@@ -941,7 +1019,7 @@ __global__ void __launch_bounds__(256) delta_scan_kernel(DeltaArgs a) {
 // start from, by themselves.  Grid tiles x H x segments.
 template <class E, int DKP, bool VEC, bool ENDS>
 __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(DeltaArgs a) {
-  typedef Shape<E, DKP> Sh;
+  typedef Shape<E, DKP, true> Sh;
   typedef typename E::raw raw;
   constexpr int IN = Sh::IN, KT = Sh::KT, GROUP = group_chunks<E, DKP>();
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -958,16 +1036,21 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
   const raw* const o = static_cast<const raw*>(a.o.p) + base_of(a.o, a, w.s, w.b, w.h) + w.col0;
   Rows<E, C, DKP, 256, VEC> rq(qs, a.Dk, false), rk(ks, a.Dk, false);
   Rows<E, C, 64, 256, VEC> ro(os, w.cols, false);
-  Block block;
+  Block<true> block;
   auto fetch = [&](int c) {
     const int n = c < w.lo ? 0 : min(C, w.s.len - c * C);
     const int64_t t0 = n <= 0 ? 0 : (int64_t)c * C;
     rk.load(k, t0, n, ks, a.Dk, false);
     rq.load(q, t0, n, qs, a.Dk, false);
+  };
+  auto fetch_rest = [&](int c) {
+    const int n = c < w.lo ? 0 : min(C, w.s.len - c * C);
+    const int64_t t0 = n <= 0 ? 0 : (int64_t)c * C;
     ro.load(o, t0, n, os, w.cols, false);
     if (n > 0) block.load(a.blocks + ((w.chunk + c) * a.H + w.h) * kDeltaBlock);
   };
   fetch(w.hi - 1);
+  fetch_rest(w.hi - 1);
   const size_t head = (size_t)w.b * a.H + w.h;
   const int64_t matrix = (int64_t)a.Dk * a.pitch;
   const bool kept = w.col0 + col < a.pitch, last = w.seg + 1 == w.segments;
@@ -981,7 +1064,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
   else
     load_state<KT>(R, a.ds_in != nullptr ? a.ds_in + head * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
   if (ENDS && last && a.ds_in != nullptr)
-    store_state<KT>(R, a.firsts + (w.part * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
+    keep_state<KT>(R, a.firsts + (w.part * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + 16 * wave, lane);
 
   for (int c = w.hi - 1; c >= w.lo; --c) {
     rk.store(kt);
@@ -990,9 +1073,12 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
     block.store(mt, vecs);
     __syncthreads();
     fetch(c - 1);
+    if (!ENDS) {
+      fetch_rest(c - 1);
+      if (c % GROUP == GROUP - 1 || c + 1 == w.chunks)
+        store_state<KT>(R, a.R + ((w.group + c / GROUP) * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
+    }
     const float whole = *reinterpret_cast<const float*>(vecs + 4 * (kUp * C + C - 1));
-    if (!ENDS && (c % GROUP == GROUP - 1 || c + 1 == w.chunks))
-      store_state<KT>(R, a.R + ((w.group + c / GROUP) * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
 
     // K R
     const int rows = row_at<DKP>(l) ^ (g << 4);
@@ -1009,6 +1095,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
       state_operand<kFull>(A, R[2 * s], R[2 * s + 1]);
       state_products<IN, false>(x, u, K, K, A);
     }
+    if (ENDS) fetch_rest(c - 1);
     // w = T'^T (P'^T dO + down beta K R)
     float y[8], f[8];
     b16x8 D[IN];
@@ -1062,7 +1149,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
     __syncthreads();
   }
   if (ENDS)
-    store_state<KT>(R, a.ends + ((w.part + w.seg - 1) * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + col, kept, lane);
+    keep_state<KT>(R, a.ends + ((w.part + w.seg - 1) * a.H + w.h) * matrix, a.Dk, a.pitch, w.col0 + 16 * wave, lane);
   else if (a.ds_out != nullptr && w.seg == 0)
     store_state<KT>(R, a.ds_out + head * a.Dk * a.Dv, a.Dk, a.Dv, w.col0 + col, col < w.cols, lane);
 }
@@ -1076,7 +1163,7 @@ __device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
 template <int DKP>
 constexpr int grad_waves() {
-  return DKP <= 128 ? 4 : 8;
+  return DKP == 64 ? 4 : 8;
 }
 template <class E, int DKP>
 struct GradShape {
@@ -1099,7 +1186,7 @@ __global__ void __launch_bounds__(64 * grad_waves<DKP>(), 2) delta_grad_kernel(D
   typedef typename E::raw raw;
   constexpr int IN = Sh::IN, KT = Sh::KT, TC = Sh::TC, TT = Sh::TT, WAVES = Sh::WAVES, THREADS = 64 * WAVES;
   // tiles (i, j) of the scores: those with j <= i, then those above the diagonal that the products read
-  constexpr bool kAhead = false;
+  constexpr bool kAhead = TC > C;  // one workgroup on a unit: its loads early
   constexpr int kTiles = TT * (TT + 1) / 2, kJobs = kTiles + TT / 2, kOwn = (kJobs + WAVES - 1) / WAVES;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char *const kt = lds + Sh::kK, *const ot = lds + Sh::kO, *const xt = lds + Sh::kX, *const wt = lds + Sh::kW,
@@ -1107,7 +1194,7 @@ __global__ void __launch_bounds__(64 * grad_waves<DKP>(), 2) delta_grad_kernel(D
   float* const vecs = reinterpret_cast<float*>(lds + Sh::kVecs);
   double* const sums = reinterpret_cast<double*>(lds + Sh::kSums);
   float* const dots = reinterpret_cast<float*>(lds + Sh::kA);  // [waves][4][TC], then <R, S> of each wave
-  const uint32_t id = near(blockIdx.x, gridDim.x), slot = divide(id, a.H, a.by_heads);
+  const uint32_t id = near(blockIdx.x, gridDim.x), slot = scalar((int)divide(id, a.H, a.by_heads));
   const int h = (int)(id - slot * a.H);
   int b, c;
   if (!group_of(a, slot, b, c)) return;
@@ -1209,6 +1296,7 @@ __global__ void __launch_bounds__(64 * grad_waves<DKP>(), 2) delta_grad_kernel(D
         }
     };
     fetch_states(0);
+    if (kAhead) rq.load(static_cast<const raw*>(a.q.p) + base_of(a.q, a, s, b, h), t0, n, qs, a.Dk, false);
     for (int col = 0; col < a.Dv; col += 64) {
       ro.store(ot);
       rx.store(xt);
@@ -1228,37 +1316,49 @@ __global__ void __launch_bounds__(64 * grad_waves<DKP>(), 2) delta_grad_kernel(D
         const int unit = row_at<64>(l) ^ (g << 4) ^ (64 * st);
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
-          b16x8 A[kFull], B[kFull];
-          {
-            float x[8], y[8];
+          b16x8 A[kFull];
+          float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              x[e] = __uint_as_float(fs[i][e / 4][e % 4]);
-              y[e] = __uint_as_float(fr[i][e / 4][e % 4]);
-              inner = __builtin_fmaf(x[e], y[e], inner);
-            }
-            split_operand<kFull>(A, x);
-            split_operand<kFull>(B, y);
+          for (int e = 0; e < 8; ++e) {
+            x[e] = __uint_as_float(fs[i][e / 4][e % 4]);
+            inner = __builtin_fmaf(x[e], __uint_as_float(fr[i][e / 4][e % 4]), inner);
           }
-          if (i == KT - 1) fetch_states(col + 32 * st + 32);
+          split_operand<kFull>(A, x);
+          hold();
 #pragma unroll
           for (int t = 0; t < TT; ++t) {
-            b16x8 O[IN], X[kFull], W[kFull];
+            b16x8 O[IN], W[kFull];
 #pragma unroll
             for (int p = 0; p < IN; ++p) O[p] = read_row(ot, unit + p * Sh::kPart + t * (16 * 128));
 #pragma unroll
-            for (int p = 0; p < kFull; ++p) {
-              X[p] = read_row(xt, unit + p * Sh::kPart + t * (16 * 128));
-              W[p] = read_row(wt, unit + p * Sh::kPart + t * (16 * 128));
-            }
+            for (int p = 0; p < kFull; ++p) W[p] = read_row(wt, unit + p * Sh::kPart + t * (16 * 128));
 #pragma unroll
             for (int z = kFull - 1; z >= 0; --z)
 #pragma unroll
               for (int y = 0; y <= z; ++y) {
                 row[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[z - y], W[y], row[i][t], 0, 0, 0);
-                cl[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B[z - y], X[y], cl[i][t], 0, 0, 0);
                 if (y < IN) dq[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[z - y], O[y < IN ? y : 0], dq[i][t], 0, 0, 0);
               }
+            hold();
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(fr[i][e / 4][e % 4]);
+          split_operand<kFull>(A, x);
+          if (i == KT - 1) fetch_states(col + 32 * st + 32);
+          hold();
+#pragma unroll
+          for (int t = 0; t < TT; t += 2) {
+            b16x8 X[2][kFull];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int p = 0; p < kFull; ++p) X[u][p] = read_row(xt, unit + p * Sh::kPart + (t + u) * (16 * 128));
+#pragma unroll
+            for (int z = kFull - 1; z >= 0; --z)
+#pragma unroll
+              for (int y = 0; y <= z; ++y)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) cl[i][t + u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[z - y], X[u][y], cl[i][t + u], 0, 0, 0);
             hold();
           }
         }
@@ -1281,7 +1381,7 @@ __global__ void __launch_bounds__(64 * grad_waves<DKP>(), 2) delta_grad_kernel(D
       __syncthreads();
       if (!kAhead) fetch(col + 64);
     }
-    rq.load(static_cast<const raw*>(a.q.p) + base_of(a.q, a, s, b, h), t0, n, qs, a.Dk, false);
+    if (!kAhead) rq.load(static_cast<const raw*>(a.q.p) + base_of(a.q, a, s, b, h), t0, n, qs, a.Dk, false);
 
     // The scores as matrices in parts: rows of tokens i, each with its factor of j (`by_rows`), or
     // rows of tokens j.  Which: Y, or -Z.
@@ -1317,6 +1417,7 @@ __global__ void __launch_bounds__(64 * grad_waves<DKP>(), 2) delta_grad_kernel(D
             *reinterpret_cast<u32x2*>(to + p * (128 * TC) + (row_at<64>(j) ^ ((i0 >> 3) << 4)) + 2 * (i0 & 7)) = u32x2{words[p][0], words[p][1]};
           }
         }
+        hold();
       }
     };
     // acc[i][t] += keys^T scores for the wave's rows of the state; LOWER: scores by rows i (tokens j <= i), else by rows j.
@@ -1375,8 +1476,10 @@ __global__ void __launch_bounds__(64 * grad_waves<DKP>(), 2) delta_grad_kernel(D
         for (int t = 0; t < TT; ++t)
 #pragma unroll
           for (int r = 0; r < 4; ++r) to[t] = __builtin_fmaf(keys[i][t][r], acc[i][t][r], to[t]);
+      hold();
     };
     read_values_of_keys();
+    hold();
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       const float* const f = vecs + 16 * t + l;
@@ -1386,6 +1489,7 @@ __global__ void __launch_bounds__(64 * grad_waves<DKP>(), 2) delta_grad_kernel(D
         row[i][t] *= -f[kGUp * TC];
         cl[i][t] *= f[kGDown * TC];
       }
+      hold();
     }
     dot(sum[0], cl);
     put_scores(scores, so, false, true);
@@ -1497,17 +1601,17 @@ hipError_t launch_shape(const DeltaArgs& a, bool backward, hipStream_t stream) {
   const unsigned blocks = (unsigned)(a.slots * a.H), heads = (unsigned)((int64_t)a.B * a.H),
                  pieces = (unsigned)(a.units > 0 ? (int64_t)a.units * a.H : (int64_t)heads * a.segments);
   const unsigned columns = (unsigned)(a.pitch + 15) / 16;  // (tiles of the scan)
-  constexpr int kLds = Shape<E, DKP>::kLds;
+  constexpr int kLds = Shape<E, DKP, true>::kLds, kLdsNarrow = Shape<E, DKP, false>::kLds;
   const bool split = a.seg_slots > 0;
   hipError_t e = hipSuccess;
   if (blocks > 0) e = launch_kernel(delta_prepare_kernel<E, DKP, VEC, true>, (blocks + 3) / 4, 0, a, stream);
   if (e == hipSuccess && split) {
-    e = launch_kernel(delta_forward_kernel<E, DKP, VEC, kEnds>, pieces * (a.tiles + a.move_tiles), kLds, a, stream);
+    e = launch_kernel(delta_forward_kernel<E, DKP, VEC, kEnds>, pieces * (a.tiles + a.move_tiles), kLdsNarrow, a, stream);
     if (e == hipSuccess && a.segments > 2) e = launch_kernel(delta_scan_kernel<DKP, false>, heads * columns, 0, a, stream);
   }
   if (e != hipSuccess) return e;
   if (!backward) return launch_kernel(delta_forward_kernel<E, DKP, VEC, kOutputs>, pieces * a.tiles, kLds, a, stream);
-  if (blocks > 0) e = launch_kernel(delta_forward_kernel<E, DKP, VEC, kKeep>, pieces * a.tiles, kLds, a, stream);
+  if (blocks > 0) e = launch_kernel(delta_forward_kernel<E, DKP, VEC, kKeep>, pieces * a.tiles, kLdsNarrow, a, stream);
   if (e == hipSuccess && split) {
     e = launch_kernel(delta_reverse_kernel<E, DKP, VEC, true>, pieces * a.tiles, kLds, a, stream);
     if (e == hipSuccess && a.segments > 2) e = launch_kernel(delta_scan_kernel<DKP, true>, heads * columns, 0, a, stream);
