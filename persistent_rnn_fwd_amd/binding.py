@@ -88,6 +88,10 @@ SEQUENCE_TYPES = {torch.float32: DATA_FLOAT, torch.float16: DATA_HALF, torch.bfl
 _ATTENTION = struct.Struct("@7if3Pq")
 _DELTA_RULE = struct.Struct("@7if2Pq")
 _SEQUENCE = struct.Struct("@P3q")
+_DELTA_FORWARD = struct.Struct("@7if2Pq" + 6 * "P3q")
+_DELTA_BACKWARD = struct.Struct("@7if2Pq" + 11 * "P3q")
+_NO_SEQUENCE = (0, 0, 0, 0)
+ABSENT = object()  # in a stream's place: an output that is not made
 RMS_GROUP = 128  # columns that share a scale of rms_norm_e4m3's groups
 
 
@@ -651,10 +655,12 @@ class Handle:
         return out
 
     # -- the gated delta rule -----------------------------------------------
-    def _delta_rule(self, q, k, v, log_decay, beta, scale, offsets, lengths, max_len, step, more):
+    def _delta_rule(self, q, k, v, log_decay, beta, scale, offsets, lengths, max_len, step, outs):
         """As _attention: writes the descriptors of the rule, of q, k, v, log_decay
-        and beta and of the sequences in `more`, and returns those tensors, the
-        shape of the states and whether there is a log_decay."""
+        and beta and of the sequences in `outs` (heads as q's or v's, head size or
+        None for one fp32 value a head, tensor or None for a new one, name, stream, or
+        ABSENT), and returns those tensors, the shape of the states and whether
+        there is a log_decay."""
         lead = 1 if step or offsets is not None else 2
         for t, name in ((q, "q"), (k, "k"), (v, "v")):
             if not isinstance(t, torch.Tensor) or t.dim() != lead + 2:
@@ -665,58 +671,71 @@ class Handle:
         code = SEQUENCE_TYPES.get(dtype)
         if code is None:
             raise TypeError(f"q must have dtype in {tuple(SEQUENCE_TYPES)}, got {dtype}")
-        *rows, Hk, Dk = q.shape
-        H, Dv = v.shape[-2:]
-        rows = tuple(rows)
-        total, at_lengths, at_offsets = 0, None, None
+        q_shape, v_shape = q.shape, v.shape
+        Hk, Dk = q_shape[-2:]
+        H, Dv = v_shape[-2:]
+        n = q_shape[0]
+        rows = q_shape[:-2]
+        total, at_lengths, at_offsets = 0, 0, 0
         if step:
-            B, T, axes = rows[0], 1, (None, 0)
+            B, T, token, batch = n, 1, -1, 0
         elif offsets is not None:
             if lengths is not None:
                 raise ValueError("give offsets (packed sequences) or lengths, not both")
             if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
                 raise ValueError("offsets must be [B + 1]")
-            B, total, axes = offsets.shape[0] - 1, rows[0], (0, None)
+            B, total, token, batch = offsets.shape[0] - 1, n, 0, -1
             T = total if max_len is None else max(-1, min(int(max_len), total))  # (longer than the rows: as long)
             at_offsets = self._dense(offsets, "offsets", torch.int32, (B + 1,))
         else:
-            (T, B), axes = rows, (0, 1)
+            T, B, token, batch = n, q_shape[1], 0, 1
             if lengths is not None:
                 at_lengths = self._dense(lengths, "lengths", torch.int32, (B,))
-        _DELTA_RULE.pack_into(self._desc, 0, B, min(T, 0x7fffffff), H, Hk, Dk, Dv, code, Dk ** -0.5 if scale is None else scale,
-                              at_lengths or 0, at_offsets or 0, total)
-        at = _DELTA_RULE.size
-        outs = []
-        token, batch = axes
-        shapes = {"H": H, "Hk": Hk, "Dk": Dk, "Dv": Dv}
-        for t, name, heads, size, stream in (
-                (q, "q", "Hk", "Dk", 0), (k, "k", "Hk", "Dk", 0), (v, "v", "H", "Dv", 0),
-                (log_decay, "log_decay", "H", None, -1), (beta, "beta", "H", None, 0), *more):
-            scalar = size is None
-            shape = (*rows, shapes[heads]) if scalar else (*rows, shapes[heads], shapes[size])
-            if t is None and stream == -1:  # (absent)
-                outs.append(None)
-                at += _SEQUENCE.size
-                continue
-            if t is None:
-                t = _empty(q, shape, torch.float32 if scalar else dtype, stream)
-                strides = t.stride()
-            elif scalar:
-                # (one value a token and head: any strides)
-                if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != shape
-                        or t.get_device() != self._index):
-                    _need_strided(t, name, self.device, (torch.float32,), shape)
-                strides = t.stride()
+        rule = [B, min(T, 0x7fffffff), H, Hk, Dk, Dv, code, Dk ** -0.5 if scale is None else scale, at_lengths, at_offsets, total]
+        wide, per_head = (*rows, H, Dv), (*rows, H)
+        more_tokens, more_batch = token >= 0 and rows[token] > 1, batch >= 0 and rows[batch] > 1
+        index, made = self._index, []
+
+        def vectors(t, name, shape, heads):
+            if (t.dtype != dtype or t.shape != shape or t.get_device() != index or (t.stride(-1) != 1 and shape[-1] > 1)):
+                _need_strided(t, name, self.device, (dtype,), shape)
+            s = t.stride()
+            rule.extend((t.data_ptr(), s[token] if more_tokens else 0, s[batch] if more_batch else 0, s[-2] if heads > 1 else 0))
+
+        def values(t, name):  # (one a token and head, at any strides)
+            if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != per_head
+                    or t.get_device() != index):
+                _need_strided(t, name, self.device, (torch.float32,), per_head)
+            s = t.stride()
+            rule.extend((t.data_ptr(), s[token] if more_tokens else 0, s[batch] if more_batch else 0, s[-1] if H > 1 else 0))
+
+        vectors(q, "q", q_shape, Hk)
+        vectors(k, "k", q_shape, Hk)
+        vectors(v, "v", wide, H)
+        if log_decay is None:
+            rule.extend(_NO_SEQUENCE)
+        else:
+            values(log_decay, "log_decay")
+        values(beta, "beta")
+        for kind, t, name, stream in outs:
+            if kind == "values":
+                if t is None:
+                    if stream is ABSENT:
+                        rule.extend(_NO_SEQUENCE)
+                        made.append(None)
+                        continue
+                    t = _empty(q, per_head, torch.float32, stream)
+                values(t, name)
             else:
-                strides = self._strided(t, name, dtype, shape)
-            heads_at = -1 if scalar else -2
-            _SEQUENCE.pack_into(self._desc, at, t.data_ptr(),
-                                strides[token] if token is not None and shape[token] > 1 else 0,
-                                strides[batch] if batch is not None and shape[batch] > 1 else 0,
-                                strides[heads_at] if shape[heads_at] > 1 else 0)
-            at += _SEQUENCE.size
-            outs.append(t)
-        return outs[5:], (B, H, Dk, Dv), log_decay is not None
+                shape = q_shape if kind == "keys" else wide
+                if t is None:
+                    t = _empty(q, shape, dtype, stream)
+                elif not isinstance(t, torch.Tensor):
+                    raise TypeError(f"{name} must be a torch tensor")
+                vectors(t, name, shape, shape[-2])
+            made.append(t)
+        (_DELTA_FORWARD if len(made) == 1 else _DELTA_BACKWARD).pack_into(self._desc, 0, *rule)
+        return made, (B, H, Dk, Dv), log_decay is not None
 
     def gated_delta_rule(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: Optional[torch.Tensor],
                          beta: torch.Tensor, *, scale: Optional[float] = None,
@@ -732,7 +751,7 @@ class Handle:
         -0.5.  Sequences of unequal length (offsets, lengths, max_len) and states
         fp32 [B, H, Dk, Dv] as in linear_attention."""
         (out,), state, decays = self._delta_rule(q, k, v, log_decay, beta, scale, offsets, lengths, max_len, False,
-                                                 ((out, "out", "H", "Dv", stream),))
+                                                 (("rows", out, "out", stream),))
         a = self._desc_at
         s = a + _DELTA_RULE.size
         _check("prnn_gated_delta_rule", self._lib.prnn_gated_delta_rule(
@@ -759,10 +778,10 @@ class Handle:
             raise TypeError("grad_out must be a torch tensor")
         (_, *grads), state, decays = self._delta_rule(
             q, k, v, log_decay, beta, scale, offsets, lengths, max_len, False,
-            ((grad_out, "grad_out", "H", "Dv", None), (grad_q, "grad_q", "Hk", "Dk", stream),
-             (grad_k, "grad_k", "Hk", "Dk", stream), (grad_v, "grad_v", "H", "Dv", stream),
-             (grad_log_decay, "grad_log_decay", "H", None, stream if log_decay is not None else -1),
-             (grad_beta, "grad_beta", "H", None, stream)))
+            (("rows", grad_out, "grad_out", None), ("keys", grad_q, "grad_q", stream), ("keys", grad_k, "grad_k", stream),
+             ("rows", grad_v, "grad_v", stream),
+             ("values", grad_log_decay, "grad_log_decay", ABSENT if log_decay is None else stream),
+             ("values", grad_beta, "grad_beta", stream)))
         a = self._desc_at
         s = a + _DELTA_RULE.size
         _check("prnn_gated_delta_rule_backward", self._lib.prnn_gated_delta_rule_backward(
@@ -782,7 +801,7 @@ class Handle:
         Dk, Dv] is updated in place, or left as it is and the new one written
         to new_state."""
         (out,), shape, decays = self._delta_rule(q, k, v, log_decay, beta, scale, None, None, None, True,
-                                                 ((out, "out", "H", "Dv", stream),))
+                                                 (("rows", out, "out", stream),))
         a = self._desc_at
         s = a + _DELTA_RULE.size
         s0 = self._dense(state, "state", torch.float32, shape)

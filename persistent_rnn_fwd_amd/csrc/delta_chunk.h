@@ -152,12 +152,12 @@ __device__ __forceinline__ void split_operand(b16x8 (&f)[P], const float (&x)[8]
   for (int p = 0; p < P; ++p) f[p] = operand(words[p]);
 }
 
-// exp of a difference of sums, its rounding to fp32 made good to first order.
+// exp of a difference of sums: 2 to the power of its fp32 part, what that leaves made good
+// to first order.
 __device__ __forceinline__ float exp_sum(double d) {
-  const float x = (float)d;
-  if (x < -104.f) return 0.f;
-  const float e = expf(x);
-  return x > 89.f ? e : __builtin_fmaf(e, (float)(d - (double)x), e);
+  const double y = d * 1.4426950408889634;
+  const float x = (float)y, e = __builtin_amdgcn_exp2f(x);
+  return x > 127.f ? e : __builtin_fmaf(e, (float)(y - (double)x) * 0.69314718f, e);
 }
 
 // A token's log decay as it is summed: minus infinity (and what else exp makes
@@ -236,7 +236,8 @@ __device__ __forceinline__ void product(f32x4& acc, const b16x8 (&x)[NX], const 
 
 // -- what depends on no state ------------------------------------------------------------------
 
-// A wave for each chunk and head.  T' is inverted in fp32: its two diagonal blocks of 16 by
+// A wave for each chunk and head, alone in its workgroup where that spreads them over
+// more units.  T' is inverted in fp32: its two diagonal blocks of 16 by
 // substitution, a column a lane, then T'_21 = -T'_22 A'_21 T'_11 on the matrix
 // cores.
 template <class E, int DKP, bool VEC, bool PAIRS>
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
   __shared__ double sums[4][C];
   __shared__ float betas[4][C];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
-  const uint32_t id = blockIdx.x * 4 + wave;
+  const uint32_t id = blockIdx.x * (blockDim.x / 64) + wave;
   const uint32_t slot = scalar((int)divide(id, a.H, a.by_heads));
   const int h = (int)(id - slot * a.H);
   int b, c;
@@ -349,11 +350,17 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
     const int o = 16 * (g & 1);
     float x[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float y = i == l ? 1.f : 0.f;
+    for (int i = 0; i < 16; ++i) x[i] = i == l ? 1.f : 0.f;
+    // four columns of the block at a time, each as soon as it is done into all rows below
 #pragma unroll
-      for (int j = 0; j < i; ++j) y = __builtin_fmaf(-A[o + i][o + j], x[j], y);
-      x[i] = y;
+    for (int j0 = 0; j0 < 16; j0 += 4) {
+#pragma unroll
+      for (int i = j0 + 1; i < 16; ++i) {
+        const f32x4 row = *reinterpret_cast<const f32x4*>(&A[o + i][o + j0]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j0 + j < i) x[i] = __builtin_fmaf(-row[j], x[j0 + j], x[i]);
+      }
     }
     if (g < 2) {
 #pragma unroll
@@ -1604,7 +1611,11 @@ hipError_t launch_shape(const DeltaArgs& a, bool backward, hipStream_t stream) {
   constexpr int kLds = Shape<E, DKP, true>::kLds, kLdsNarrow = Shape<E, DKP, false>::kLds;
   const bool split = a.seg_slots > 0;
   hipError_t e = hipSuccess;
-  if (blocks > 0) e = launch_kernel(delta_prepare_kernel<E, DKP, VEC, true>, (blocks + 3) / 4, 0, a, stream);
+  // (448 chunks and heads of 128, fp32: 12.5 us in fours, 10 alone)
+  if (blocks > 0) {
+    const bool alone = blocks <= 1024;
+    e = launch_kernel(delta_prepare_kernel<E, DKP, VEC, true>, alone ? blocks : (blocks + 3) / 4, 0, a, stream, alone ? 64 : 256);
+  }
   if (e == hipSuccess && split) {
     e = launch_kernel(delta_forward_kernel<E, DKP, VEC, kEnds>, pieces * (a.tiles + a.move_tiles), kLdsNarrow, a, stream);
     if (e == hipSuccess && a.segments > 2) e = launch_kernel(delta_scan_kernel<DKP, false>, heads * columns, 0, a, stream);
