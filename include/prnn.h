@@ -680,8 +680,10 @@ prnnStatus_t prnn_layer_norm_backward(prnnHandle_t handle, int64_t M, int N, prn
  * log_decay and beta are fp32 values for every token and head (log_decay may be
  * absent: no decay; minus infinity forgets everything before the token).  Head
  * h of v, o, log_decay, beta and the state uses head h / (H / Hk) of q and k.
- * Keys of unit length and 0 <= beta <= 2 keep the state bounded; any values are
- * taken as they are.  States are fp32 and dense, [B][H][Dk][Dv]; sums, states
+ * Keys of unit length and 0 <= beta <= 2 keep the state bounded; other values are
+ * taken as they are, but where the products of the tokens' transitions overflow
+ * fp32, a long sequence may end in NaN although its states happen to be zeros
+ * there.  States are fp32 and dense, [B][H][Dk][Dv]; sums, states
  * and all that lies between the products are fp32 for every type.  A row of o
  * depends on no later token, whatever that holds (infinities and NaN included);
  * from a value that is not finite on, the columns of the state that it reaches
@@ -721,8 +723,8 @@ prnnStatus_t prnn_gated_delta_rule(prnnHandle_t handle, const prnnDeltaRule_t* r
  * shared head's group, added in fp32 in a fixed order), dv [..][H][Dv],
  * dlog_decay (or NULL) and dbeta [..][H] and, unless NULL, dS0 (which may be
  * dS1).  Without S0 the first token's decay acts on nothing: its gradient is 0.
- * The workspace also holds the states of every chunk and their gradients (8 Dk
- * Dv bytes for 32 tokens of a head), x and w (8 Dv bytes a token and head) and,
+ * The workspace also holds states and their gradients (8 Dk Dv bytes for 32
+ * tokens of a head, for 64 where Dk is 65 .. 128 and the type has 16 bits), x and w (8 Dv bytes a token and head) and,
  * for shared heads, every head's dq and dk in fp32.  A value that is not finite
  * may make every gradient of its sequence and head NaN.  Errors as
  * prnn_gated_delta_rule. */

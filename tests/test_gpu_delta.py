@@ -543,3 +543,155 @@ def test_refusals(handle):
     with pytest.raises(ValueError):
         handle.gated_delta_rule(**p, initial_state=x["S0"][:, :, :, :8])
     handle.synchronize()
+
+
+# -- sequences long enough to be split into segments, and groups of chunks ----------
+
+SPLIT = [(530, 2, 3, 1, 96, 80), (600, 1, 2, 2, 128, 128), (420, 1, 1, 1, 256, 40), (401, 3, 2, 1, 33, 5), (777, 1, 1, 1, 100, 256),
+         (384, 1, 4, 2, 64, 64)]
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("shape", SPLIT, ids=str)
+def test_split_sequences(handle, type, shape):
+    """The states are in place: other workgroups may end before the first segment starts."""
+    p, x = problem(31 + sum(shape), type, *shape)
+    S = x["S0"].clone()
+    o = handle.gated_delta_rule(**p, scale=0.3, initial_state=S, final_state=S)
+    check_forward(o, S, p, 0.3, x["S0"])
+    o = handle.gated_delta_rule(**p, scale=0.3)
+    check_forward(o, None, p, 0.3)
+    dS = x["dS1"].clone()
+    grads = handle.gated_delta_rule_backward(**p, grad_out=x["do"], scale=0.3, initial_state=x["S0"],
+                                             grad_final_state=dS, grad_initial_state=dS)
+    check_backward(grads, dS, p, x["do"], 0.3, x["S0"], x["dS1"])
+    grads = handle.gated_delta_rule_backward(**p, grad_out=x["do"], scale=0.3)
+    check_backward(grads, None, p, x["do"], 0.3)
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("Dk", [48, 112])
+def test_split_lengths(handle, type, Dk):
+    """A padded batch of sequences in none, one and several segments."""
+    used = [0, 1, 530, 400, 129, 31, 256]
+    p, x = problem(41, type, 530, len(used), 1, 1, Dk, 72)
+    clean, clean_do = {m: t.clone() for m, t in p.items()}, x["do"].clone()
+    for b, n in enumerate(used):
+        for t in (*p.values(), x["do"]):
+            t[n:, b] = float("nan")
+    S, dS0 = torch.empty_like(x["S0"]), torch.empty_like(x["S0"])
+    n = torch.tensor(used, dtype=torch.int32, device="cuda")
+    o = handle.gated_delta_rule(**p, scale=0.2, initial_state=x["S0"], final_state=S, lengths=n)
+    grads = handle.gated_delta_rule_backward(**p, grad_out=x["do"], scale=0.2, initial_state=x["S0"],
+                                             grad_final_state=x["dS1"], grad_initial_state=dS0, lengths=n)
+    check_forward(o, S, clean, 0.2, x["S0"], used)
+    check_backward(grads, dS0, clean, clean_do, 0.2, x["S0"], x["dS1"], used)
+    for b, m in enumerate(used):
+        for t in (o, *grads):
+            assert not t[m:, b].any()
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("max_len", [None, 450])
+@pytest.mark.parametrize("Dk", [64, 100])
+def test_split_packed(handle, type, max_len, Dk):
+    """Long packed sequences between more short and empty ones than a wave looks at
+    at once; segments of one begin inside what would be another's."""
+    lens = [3, 450, 0, 0, 131, 1, 389] + [i % 4 for i in range(70)] + [300, 0]
+    offsets = np.cumsum([1] + lens)
+    rows = int(offsets[-1]) + 5
+    B, H, Hk = len(lens), 2, 1
+    p, x = problem(43, type, rows, 1, H, Hk, Dk, 24)
+    S0 = torch.randn((B, H, Dk, 24), device="cuda")
+    packed = {m: t[:, 0].contiguous() for m, t in p.items()}
+    S, dS0 = torch.empty_like(S0), torch.empty_like(S0)
+    out = torch.full((rows, H, 24), 7.0, dtype=TYPES[type], device="cuda")
+    seq = {"scale": 0.2, "offsets": torch.tensor(offsets, dtype=torch.int32, device="cuda"), "max_len": max_len, "initial_state": S0}
+    handle.gated_delta_rule(**packed, final_state=S, out=out, **seq)
+    given = {f"grad_{m}": torch.full_like(t, 7.0) for m, t in packed.items()}
+    grads = handle.gated_delta_rule_backward(**packed, grad_out=x["do"][:, 0].contiguous(), grad_final_state=S0 + 1,
+                                             grad_initial_state=dS0, **given, **seq)
+    for b in [0, 1, 2, 4, 5, 6, 8, 10, 40, 75, 76, 77, 78]:
+        lo, hi = offsets[b:b + 2]
+        one = {m: t[lo:hi] for m, t in p.items()}
+        check_forward(out[lo:hi, None], S[b:b + 1], one, 0.2, S0[b:b + 1])
+        check_backward([g[lo:hi, None] for g in grads], dS0[b:b + 1], one, x["do"][lo:hi], 0.2, S0[b:b + 1], S0[b:b + 1] + 1)
+    for t in (out, *grads):
+        assert (t[:1] == 7).all() and (t[-5:] == 7).all()
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("T", [32, 63, 64, 65, 96, 97, 128, 129])
+def test_groups_of_chunks(handle, type, T):
+    """Gradients where the last group of chunks is whole, of one chunk, of one token."""
+    p, x = problem(50 + T, type, T, 2, 2, 1, 112, 72)
+    dS0 = torch.empty_like(x["S0"])
+    grads = handle.gated_delta_rule_backward(**p, grad_out=x["do"], scale=0.3, initial_state=x["S0"],
+                                             grad_final_state=x["dS1"], grad_initial_state=dS0)
+    check_backward(grads, dS0, p, x["do"], 0.3, x["S0"], x["dS1"])
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+@pytest.mark.parametrize("where", ["q", "k", "v", "log_decay", "beta"])
+def test_later_tokens_of_a_split_sequence(handle, type, where):
+    """As test_later_tokens_reach_no_earlier_row, from a token in a middle segment on."""
+    T, t = 520, 300
+    p, x = problem(60, type, T, 2, 2, 2, 64, 64, decay=[-0.01, -0.5])
+    if where in ("log_decay", "beta"):
+        p[where][t, 0, 0] = float("nan")
+    else:
+        p[where][t, 0, 0, 5] = float("nan")
+    S = torch.empty_like(x["S0"])
+    o = handle.gated_delta_rule(**p, scale=0.2, initial_state=x["S0"], final_state=S)
+    check_forward(o[:t], None, {m: y[:t] for m, y in p.items()}, 0.2, x["S0"])
+    check_forward(o[:, 1:], S[1:], {m: y[:, 1:] for m, y in p.items()}, 0.2, x["S0"][1:])
+    with np.errstate(all="ignore"):
+        ref, refS, _ = oracle.gated_delta_rule(**{m: host(y) for m, y in p.items()}, scale=0.2, S0=host(x["S0"]))
+    for got, want in ((host(o), ref), (host(S), refS)):
+        assert np.array_equal(np.isfinite(got), np.isfinite(want))
+
+
+@pytest.mark.parametrize("type", sorted(TYPES))
+def test_decays_to_nothing_in_a_split_sequence(handle, type):
+    """log_decay of minus infinity forgets what was before, in the middle of a segment and
+    at its first token; beta of 0 and keys of zeros change nothing."""
+    p, x = problem(61, type, 500, 1, 2, 1, 64, 64)
+    p["log_decay"][[200, 256, 384, 385], :, 0] = float("-inf")
+    p["beta"][300:340] = 0
+    p["k"][400:420] = 0
+    S = torch.empty_like(x["S0"])
+    o = handle.gated_delta_rule(**p, scale=0.2, initial_state=x["S0"], final_state=S)
+    check_forward(o, S, p, 0.2, x["S0"])
+    q = {m: y.clone() for m, y in p.items()}
+    q["log_decay"].clamp_(min=-200.0)  # exp is 0 all the same, and the oracle's sums of it are finite
+    grads = handle.gated_delta_rule_backward(**p, grad_out=x["do"], scale=0.2, initial_state=x["S0"])
+    check_backward(grads, None, q, x["do"], 0.2, x["S0"])
+
+
+def test_two_graphs_share_the_workspace(gpu):
+    """Graphs of two calls of one handle, one split, replayed in turn on one stream."""
+    with Handle() as h:
+        a, ax = problem(62, "bf16", 700, 1, 2, 1, 64, 64)
+        b, bx = problem(63, "f16", 200, 3, 4, 4, 96, 40)
+        calls = [lambda: h.gated_delta_rule_backward(**a, grad_out=ax["do"], initial_state=ax["S0"]),
+                 lambda: (h.gated_delta_rule(**b), h.gated_delta_rule_backward(**b, grad_out=bx["do"])[4])]
+        want = [[t.clone() for t in call()] for call in calls]
+        for call in calls:
+            call()
+        torch.cuda.synchronize()
+        side, graphs, outs = torch.cuda.Stream(), [], []
+        with torch.cuda.stream(side):
+            for call in calls:
+                graphs.append(torch.cuda.CUDAGraph())
+                with torch.cuda.graph(graphs[-1], stream=side):
+                    outs.append(call())
+        torch.cuda.synchronize()
+        for i in (0, 1, 1, 0, 0, 1):
+            for t in outs[i]:
+                t.zero_()
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                graphs[i].replay()
+                graphs[1 - i].replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for got, ref in zip(outs, want) for x, y in zip(got, ref)), i
