@@ -5,7 +5,8 @@
 //   8 bits: scale = max(max |y| / 448, 2^-126) over a row or 128 columns, y / scale as e4m3
 //   dx = rstd (g - n mean(g n)) + dsum,  dw = sum_m dy n,  with n = s rstd and g = dy w
 //
-// Built like layer norm (layer_norm.hip): bound by memory, a row is read once into
+// Built like layer norm (layer_norm.hip): bound by memory (measured: see the launch; gradients of
+// 16384 x 5760 bf16 148 us, 5.1 TB/s, a large copy reaches 4.8), a row is read once into
 // the registers of TPR threads, 16 bytes at a time, with the next row's loads in
 // flight; the sum s stays in fp32 between its addition and the norm and is
 // rounded once where it is stored, as y is.  The scale of 128 columns is a
@@ -449,7 +450,10 @@ hipError_t launch_rms_norm(const RmsArgs& a, prnnDataType_t type, prnnDataType_t
     const bool fits = for_shape<V, 32>(s, [&](auto c) {
       typedef decltype(c) K;
       const int64_t sets = (a.M + K::block / K::tpr - 1) / (K::block / K::tpr);
-      const int64_t most = 4ll * a.compute_units;
+      // Workgroups with a row or two each: those at work then are on neighbouring rows.  With 4 /
+      // 16 / 64 a unit: 16384 x 5760 bf16 in 8 bits 132 / 124 / 117 us, 8192 x 8192 fp32 205 /
+      // 203 / 193, 100000 x 513 bf16 90 / 86 / 80; 40000 x 1153 fp16 in 8 bits 66 / 67 / 72.
+      const int64_t most = 64ll * a.compute_units;
       const unsigned grid = (unsigned)(sets < most ? sets : most);
       if (eight)
         rms_kernel<E, P, K::v, K::odd, K::tpr, K::nv, K::block, true><<<grid, K::block, 0, stream>>>(a);
