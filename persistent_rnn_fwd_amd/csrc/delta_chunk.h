@@ -716,6 +716,22 @@ __device__ __forceinline__ void state_products(f32x4 (&acc)[2], f32x4 (&other)[2
     }
 }
 
+// The priority of a wave by the chunks it has done.  Of two workgroups on a unit
+// the older one's waves issue first: it ends after 345 us, the other after 450 (128 chunks of 128 x 64
+// bf16 each).  A step lower every two chunks, the one that is behind mostly comes first.  Taken by
+// the walks of split sequences, whose workgroups are all there from the start: 32768 tokens of 32 bf16
+// heads of 128 1123 us without, 1097 with; 4 x 8192 of 16 592 and 568.  (In the walks of 8 x 1024 tokens of
+// 64 heads, which follow one another on a unit, 335 and 343; in those of the gradients, 18 fp32 heads of
+// 64, 74.7 and 76.1.)
+__device__ __forceinline__ void urge(int done) {
+  switch (done >> 1 & 3) {
+    case 0: __builtin_amdgcn_s_setprio(3); break;
+    case 1: __builtin_amdgcn_s_setprio(2); break;
+    case 2: __builtin_amdgcn_s_setprio(1); break;
+    default: __builtin_amdgcn_s_setprio(0);
+  }
+}
+
 // What the walk does: the outputs and the final state; x and the chunks' first
 // states for the gradients; or the segments' ends and moves.
 enum Walk { kOutputs, kKeep, kEnds };
@@ -798,6 +814,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : WALK == kOutputs && VEC 
 
   for (int c = w.lo; c < w.hi; ++c) {
     const int n = min(C, w.s.len - c * C);
+    if (WALK != kKeep && split) urge(c - w.lo);
     rk.store(kt);
     if (OUT) rq.store(qt);
     rv.store(vt);
