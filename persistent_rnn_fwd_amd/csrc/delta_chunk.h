@@ -30,10 +30,24 @@
 // 16) is that of an operand whose rows are dealt to suit, so K S, x, o^T and the
 // state's update follow each other without a shuffle: two tiles of 16 tokens are
 // the operand whose element e of lane group g is token 16 (e / 4) + 4 g + e % 4, and
-// T' and P' are stored with their columns in that order.  The backward pass walks
-// forward for x and the states that chunks start from (kept in the workspace),
-// backwards for w and the gradients of those they end with, and a last launch, a
-// workgroup for each chunk and head, takes the gradients from these.
+// T' and P' are stored with their columns in that order.  Long sequences of few heads
+// are split (plan_delta): a walk from zeros, and one from the identity without
+// values, leave what each segment adds to the state and makes of it,
+// delta_scan_kernel joins them, and the walk starts each segment from its own
+// state.  The backward pass walks forward for x and the states that groups of chunks
+// (group_chunks) start from, kept in the workspace, backwards for w and the gradients
+// of the states they end with (delta_reverse_kernel; split the same way, with the
+// moves transposed), and a last launch, a workgroup for each group and head, takes
+// the gradients from these (delta_grad_kernel).
+//
+// What bounds it.  The walk: a chunk's chain of products (96 for each wave, bf16 and
+// 128 rows, 1540 cycles), splitting of the state and of x (the most of 1700 cycles of vector
+// instructions) and LDS between them, 5600 cycles alone on a unit, of which a second
+// workgroup hides nearly half.  32768 tokens of 32 bf16 heads of 128: 1080 us, of them the first
+// launch 166 (5.8 TB/s), ends and moves 550, the scan 27, the walk 500.  The gradients: what
+// goes through memory, 8 x 2048 tokens of 16 bf16 heads of 128 782 us, of them the first launch
+// 60, the walks 155 and 205, the gradients' own launch 390 (1 GB read, one workgroup on a
+// unit).  Small calls: launches and first loads.
 //
 // Precision.  As linear attention's: operands in bf16 parts, exact (one for bf16,
 // two for fp16, three for fp32), what is fp32 between the products in three, sums
