@@ -214,6 +214,7 @@ void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward, int compute_un
     a->seg_slots = a->offsets != nullptr ? a->rows / tokens + 1 : (int64_t)a->B * a->segments;
     if (a->offsets != nullptr) a->units = (int)(a->rows / tokens + a->B);
   }
+  a->pieces = a->units > 0 ? a->units : a->B * a->segments;
   a->by_tiles = inverse_of(a->tiles);
   a->by_all_tiles = inverse_of(a->tiles + a->move_tiles);
   a->by_heads = inverse_of(a->H);
@@ -223,6 +224,7 @@ void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward, int compute_un
   a->by_segments = inverse_of(a->segments);
   a->by_seg_chunks = inverse_of(a->seg_chunks);
   a->by_seg_tokens = inverse_of((int)tokens);
+  a->by_pieces = inverse_of(a->pieces);
 }
 
 }  // namespace prnn

@@ -46,11 +46,12 @@ struct DeltaArgs {
   int64_t seg_slots;  // segments in the workspace, 0: no sequence is split
   int segments;       // of the longest sequence
   int seg_chunks;     // chunks of a segment
+  int pieces;         // segments of all sequences, as a launch has workgroups for them
   int units;          // packed: workgroups' sequences and segments are found by number (unit_of), or 0
   int pitch, move_pitch;
   int dkp, tiles, move_tiles, vec;
   uint32_t by_tiles, by_all_tiles, by_heads, by_chunks, by_segments, by_seg_chunks, by_seg_tokens, by_groups,
-      by_group_tokens;
+      by_group_tokens, by_pieces;
 };
 
 // Packed sequences as find_unit() takes them: in pieces of seg_tokens.
