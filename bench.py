@@ -47,7 +47,9 @@ KERNEL_SOURCES = ["device_common.h", "kernels.h", "dense_kernel.h", "sparse_kern
                   "dense_f16.hip", "dense_f32.hip", "sparse_f16.hip", "sparse_f32.hip", "team_f16.hip", "team_f32.hip",
                   "team_half.hip", "team_split.hip", "team_rows.hip", "team_pinned.h", "project_tile.h", "project.hip",
                   "stack.hip", "noalloc.hip", "host_internal.h", "sequence.h", "linear_attention.hip", "layer_norm.hip",
-                  "attention_chunk.h", "attention_f32.hip", "attention_f16.hip", "attention_bf16.hip"]
+                  "attention_chunk.h", "attention_f32.hip", "attention_f16.hip", "attention_bf16.hip", "regions.h", "norm_rows.h",
+                  "delta_rule.h", "delta_chunk.h", "delta_rule.hip", "delta_f32.hip", "delta_f16.hip", "delta_bf16.hip",
+                  "rms_norm.h", "rms_norm.hip"]
 
 
 def code_only(text: str) -> str:

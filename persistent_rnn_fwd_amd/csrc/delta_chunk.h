@@ -973,7 +973,7 @@ __global__ void __launch_bounds__(256) delta_scan_kernel(DeltaArgs a) {
   const uint32_t b = scalar((int)divide(state, a.H, a.by_heads));
   const int h = (int)(state - b * a.H), col0 = 16 * (int)(blockIdx.x - state * tiles);
   const Span s = span_of(a, (int)b);
-  const int segments = (s.len + a.seg_chunks * C - 1) / (a.seg_chunks * C);
+  const int segments = (s.len - 1) / (a.seg_chunks * C) + 1;
   if (segments <= 2) return;
   const int64_t part = a.offsets != nullptr ? s.first / (a.seg_chunks * C) : (int64_t)b * a.segments;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l = lane & 15;
