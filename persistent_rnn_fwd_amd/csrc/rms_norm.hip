@@ -10,9 +10,9 @@
 // the registers of TPR threads, 16 bytes at a time, with the next row's loads in
 // flight; the sum s stays in fp32 between its addition and the norm and is
 // rounded once where it is stored, as y is.  The scale of 128 columns is a
-// maximum over the 16 or 32 lanes that hold them; y times the scale's reciprocal
-// is off by a rounding or two of fp32 before it is rounded to e4m3 (nearest, ties to
-// even) and cannot pass 448 by as much as its last step, so nothing is clamped.
+// maximum over the 16 or 32 lanes that hold them; y / scale is rounded once in fp32
+// before it is rounded to e4m3 (nearest, ties to even) and cannot pass 448 by as much as its
+// last step, so nothing is clamped.
 #include "norm_rows.h"
 #include "rms_norm.h"
 
@@ -49,13 +49,25 @@ __device__ __forceinline__ float row_max(float x, float* slot) {
 
 __device__ __forceinline__ float scale_of(float most) { return fmaxf(most / 448.f, 0x1p-126f); }
 
+// A group's scale as y is divided by it: y / scale is y times the reciprocal and one step
+// of its residual, rounded once.  (An infinite scale is that of a row with an infinity:
+// what is finite there becomes 0.)
+struct Scale {
+  float finite, inverse;
+  __device__ __forceinline__ explicit Scale(float scale) : finite(fminf(scale, 0x1.fffffep127f)), inverse(1.f / scale) {}
+  __device__ __forceinline__ float under(float y) const {
+    const float q = y * inverse;
+    return __builtin_fmaf(__builtin_fmaf(-q, finite, y), inverse, q);
+  }
+};
+
 // V values in 8 bits.
 template <int V>
-__device__ __forceinline__ void eights(const float (&y)[V], float inverse, uint32_t (&out)[V / 4]) {
+__device__ __forceinline__ void eights(const float (&y)[V], const Scale& s, uint32_t (&out)[V / 4]) {
 #pragma unroll
   for (int i = 0; i < V; i += 4) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[i] * inverse, y[i + 1] * inverse, 0, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(y[i + 2] * inverse, y[i + 3] * inverse, w, true);
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(s.under(y[i]), s.under(y[i + 1]), 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(s.under(y[i + 2]), s.under(y[i + 3]), w, true);
     out[i / 4] = (uint32_t)w;
   }
 }
@@ -165,7 +177,7 @@ __global__ void __launch_bounds__(BLOCK) rms_kernel(RmsArgs a) {
           if (!c.in) continue;
           const float scale = scale_of(most[j]);
           uint32_t out[V / 4];
-          eights<V>(x[j], 1.f / scale, out);
+          eights<V>(x[j], Scale(scale), out);
           if (groups == 1 ? k == 0 : k % kLanes == 0) a.scales[m * groups + k / kLanes] = scale;
           if (ODD && c.again > 0) {  // the columns before may be another scale's
 #pragma unroll
@@ -217,17 +229,17 @@ __global__ void __launch_bounds__(1024) rms_wide_kernel(RmsArgs a) {
     } else {
       uint8_t* y = static_cast<uint8_t*>(a.y) + m * a.ldy;
       const int groups = a.group > 0 ? (a.N + kRmsGroup - 1) / kRmsGroup : 1;
-      auto put = [&](int n, float inverse) {
+      auto put = [&](int n, const Scale& s8) {
         const float f = normed(n), t = value(n);
         if (a.sum != nullptr) static_cast<raw*>(a.sum)[m * a.lds + n] = E::put(t);
-        y[n] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(f * inverse, 0.f, 0, false);
+        y[n] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(s8.under(f), 0.f, 0, false);
       };
       if (a.group == 0) {
         float most = 0.f;
         for (int n = threadIdx.x; n < a.N; n += 1024) most = fmaxf(most, fabsf(normed(n)));
         const float scale = scale_of(row_max<1024>(most, slots));
         if (threadIdx.x == 0) a.scales[m] = scale;
-        for (int n = threadIdx.x; n < a.N; n += 1024) put(n, 1.f / scale);
+        for (int n = threadIdx.x; n < a.N; n += 1024) put(n, Scale(scale));
       } else {
         const int lane = threadIdx.x & 63;
         for (int q = threadIdx.x >> 6; q < groups; q += 16) {
@@ -239,8 +251,8 @@ __global__ void __launch_bounds__(1024) rms_wide_kernel(RmsArgs a) {
           for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
           const float scale = scale_of(most);
           if (lane == 0) a.scales[m * groups + q] = scale;
-          if (n0 < a.N) put(n0, 1.f / scale);
-          if (n1 < a.N) put(n1, 1.f / scale);
+          if (n0 < a.N) put(n0, Scale(scale));
+          if (n1 < a.N) put(n1, Scale(scale));
         }
       }
     }

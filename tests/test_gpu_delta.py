@@ -695,3 +695,26 @@ def test_two_graphs_share_the_workspace(gpu):
                 graphs[1 - i].replay()
             torch.cuda.synchronize()
             assert all(torch.equal(x, y) for got, ref in zip(outs, want) for x, y in zip(got, ref)), i
+
+
+def test_two_handles_on_two_streams(gpu):
+    """Each handle has its own workspace: calls that run at once leave each other's results alone."""
+    problems = [problem(64, "bf16", 900, 1, 2, 1, 64, 64), problem(65, "f32", 300, 2, 4, 4, 96, 40)]
+    with Handle() as a, Handle() as b:
+        def call(h, p, x, stream=None):
+            S = torch.empty_like(x["S0"])
+            return (h.gated_delta_rule(**p, initial_state=x["S0"], final_state=S, stream=stream), S,
+                    *h.gated_delta_rule_backward(**p, grad_out=x["do"], initial_state=x["S0"], stream=stream))
+
+        want = [call(h, *p) for h, p in zip((a, b), problems)]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        got = [[], []]
+        for _ in range(5):
+            for i, h in enumerate((a, b)):
+                with torch.cuda.stream(streams[i]):
+                    got[i].append(call(h, *problems[i]))
+        torch.cuda.synchronize()
+        for i in range(2):
+            for run in got[i]:
+                assert all(torch.equal(x, y) for x, y in zip(run, want[i])), i
