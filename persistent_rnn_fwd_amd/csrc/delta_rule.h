@@ -34,7 +34,7 @@ struct DeltaArgs {
   // ... backward, by group of chunks (see delta_grad_kernel) and head:
   float *x, *w;   // [tokens][pitch]
   float *S, *R;   // [Dk][pitch], the state that the group starts from and the gradient of the one it ends with
-  // ... and by segment of a split sequence (first_segment()) and head
+  // ... and by segment of a split sequence (Where::part) and head
   float* ends;    // [Dk][pitch]: the state a segment leaves by itself, then the sequence's; backward then its gradient
   float* firsts;  // [Dk][pitch]: the state, or gradient, that the sequence's first, or last, segment starts from
   float* moves;   // [Dk][Dk], rows `move_pitch` apart: what a segment makes of the identity, without values
@@ -47,7 +47,7 @@ struct DeltaArgs {
   int segments;       // of the longest sequence
   int seg_chunks;     // chunks of a segment
   int pieces;         // segments of all sequences, as a launch has workgroups for them
-  int units;          // packed: workgroups' sequences and segments are found by number (unit_of), or 0
+  int units;          // packed: workgroups' sequences and segments are found by number (find_unit), or 0
   int pitch, move_pitch;
   int dkp, tiles, move_tiles, vec;
   uint32_t by_tiles, by_all_tiles, by_heads, by_chunks, by_segments, by_seg_chunks, by_seg_tokens, by_groups,
