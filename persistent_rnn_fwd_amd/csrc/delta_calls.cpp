@@ -137,10 +137,12 @@ DeltaArgs base_args(const Problem& p, const prnnSequence_t* q, const prnnSequenc
 }
 
 // Whether the launches' workgroups fit a grid (prepare: a wave for each chunk
-// and head; the gradients: a workgroup).
+// and head; the gradients: a workgroup for each group of chunks and head, which may have more
+// than the 256 threads that kMaxWorkgroups counts).
 bool grids_fit(const DeltaArgs& a, bool backward) {
   if ((double)a.slots * a.H > 4. * kMaxWorkgroups) return false;
   const int64_t blocks = a.slots * a.H;
+  if (backward && a.group_slots * a.H * delta_grad_waves(a.dkp) > 4 * kMaxWorkgroups) return false;
   const double pieces = a.units > 0 ? (double)a.units * a.H : (double)a.B * a.H * a.segments;
   return (backward ? blocks : (blocks + 3) / 4) <= kMaxWorkgroups &&
          pieces * (a.tiles + (a.segments > 1 ? a.move_tiles : 0)) <= kMaxWorkgroups && (a.segments < 3 || (double)a.B * a.H * ((a.pitch + 15) / 16) <= kMaxWorkgroups);

@@ -1210,14 +1210,10 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
 // Nothing is moved across: reads of operands ahead would take the registers of the sums.
 __device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
-template <int DKP>
-constexpr int grad_waves() {
-  return DKP == 64 ? 4 : 8;
-}
 template <class E, int DKP>
 struct GradShape {
   static constexpr int IN = Parts<E>::kIn, TC = group_chunks<E, DKP>() * C, TT = TC / 16;
-  static constexpr int WAVES = grad_waves<DKP>(), KT = DKP / 16 / WAVES;  // tiles of 16 rows of the state a wave
+  static constexpr int WAVES = delta_grad_waves(DKP), KT = DKP / 16 / WAVES;  // tiles of 16 rows of the state a wave
   static constexpr int kPart = 2 * TC * 64;         // a part of 64 columns of TC rows
   // k, then q; dO, x and w of 64 columns, then two matrices of scores, then the sums of the waves
   static constexpr int kK = 0, kA = 2 * TC * IN * DKP, kO = kA, kX = kO + IN * kPart, kW = kX + 3 * kPart,
@@ -1230,7 +1226,7 @@ enum GradVec { kGUp, kGScaledUp, kGDown, kGBeta };
 // Grid groups x H.  The columns of the state are taken 64 at a time; a wave has KT
 // tiles of 16 of its rows.
 template <class E, int DKP, bool VEC>
-__global__ void __launch_bounds__(64 * grad_waves<DKP>(), 2) delta_grad_kernel(DeltaArgs a) {
+__global__ void __launch_bounds__(64 * delta_grad_waves(DKP), 2) delta_grad_kernel(DeltaArgs a) {
   typedef GradShape<E, DKP> Sh;
   typedef typename E::raw raw;
   constexpr int IN = Sh::IN, KT = Sh::KT, TC = Sh::TC, TT = Sh::TT, WAVES = Sh::WAVES, THREADS = 64 * WAVES;

@@ -15,6 +15,9 @@ enum DeltaVec { kUp, kScaledUp, kInto, kDown, kBeta };  // 32 floats each
 constexpr int kDeltaSums = kDeltaVec + 5 * 128;         // 32 doubles: the decays' sums
 constexpr int kDeltaBlock = 13 * 1024;
 
+// Waves of a workgroup of the gradients' launch, by the rows its instance holds (dkp).
+constexpr int delta_grad_waves(int dkp) { return dkp == 64 ? 4 : 8; }
+
 struct DeltaArgs {
   AttnOperand q, k, v, o;  // o: the output, or its gradient
   AttnOperand g, beta;     // fp32, one value a token and head; g.p null: no decay
