@@ -722,7 +722,10 @@ prnnStatus_t prnn_gated_delta_rule(prnnHandle_t handle, const prnnDeltaRule_t* r
  * NULL), the inputs as they were; writes dq and dk [..][Hk][Dk] (sums over a
  * shared head's group, added in fp32 in a fixed order), dv [..][H][Dv],
  * dlog_decay (or NULL) and dbeta [..][H] and, unless NULL, dS0 (which may be
- * dS1).  Without S0 the first token's decay acts on nothing: its gradient is 0.
+ * dS1).  Without S0 the first token's decay acts on nothing: its gradient is 0, and
+ * so is that of a log decay whose exp is 0 (below -104, minus infinity among them).
+ * Others come from sums over the tokens behind, whose rounding is relative to the
+ * states' and their gradients' norms, however small the decay itself is.
  * The workspace also holds states and their gradients (8 Dk Dv bytes for 32
  * tokens of a head, for 64 where Dk is 65 .. 128 and the type has 16 bits), x and w (8 Dv bytes a token and head) and,
  * for shared heads, every head's dq and dk in fp32.  A value that is not finite

@@ -20,7 +20,7 @@
 //   dq = scale up o (dO S^T) + (Y beta) K,   row = -up o (w S^T) - (Z beta) K
 //   col = down o (x R^T) + Y^T Q - Z^T K,    dk = row + beta o col
 //   dbeta_i = k_i.col_i,   dG_i = q_i.dq_i + k_i.row_i - beta_i dbeta_i
-//   dg_t = up_C <R, S> + sum_j beta_j k_j.(down o x R^T)_j + sum_{i >= t} dG_i
+//   dg_t = up_C <R, S> + sum_j beta_j k_j.(down o x R^T)_j + sum_{i >= t} dG_i   (0 where exp(g_t) is)
 //
 // Launches.  T', P' and the factors depend on no state: a first launch, a wave
 // for each chunk and head, leaves them in the workspace (delta_prepare_kernel).
@@ -1618,6 +1618,9 @@ __global__ void __launch_bounds__(64 * delta_grad_waves(DKP), 2) delta_grad_kern
       }
       dg += behind + (double)vecs[kGUp * TC + TC - 1] * (double)rs;
       if (t == 0 && c == 0 && a.s_in == nullptr) dg = 0.;  // nothing there to decay before the first token
+      // What a decay of 0 leaves does not depend on its logarithm.  (From sums that cancel, the
+      // difference would be their rounding.  exp is 0 in fp32 below -103.98; NaN stays.)
+      if (sums[t] - (t > 0 ? sums[t - 1] : 0.) < -104.) dg *= 0.;
     }
     if (t < all) {
       static_cast<float*>(const_cast<void*>(a.dbeta.p))[base_of(a.dbeta, a, s, b, h) + (t0 + t) * a.dbeta.token] = t < n ? dbeta : 0.f;
