@@ -254,7 +254,7 @@ __device__ __forceinline__ void product(f32x4& acc, const b16x8 (&x)[NX], const 
 // more units.  T' is inverted in fp32: its two diagonal blocks of 16 by
 // substitution, a column a lane, then T'_21 = -T'_22 A'_21 T'_11 on the matrix
 // cores.
-template <class E, int DKP, bool VEC, bool PAIRS>
+template <class E, int DKP, bool VEC>
 __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
   typedef typename E::raw raw;
   constexpr int IN = Parts<E>::kIn, kRow = 36;
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
       for (int x = 0; x < 2; ++x) {
         const int row = 16 * x + l;
         pk[y][x].load(rk, row < n ? row * ks : kOutside, d + 32 * y + 8 * g, a.Dk);
-        if (PAIRS) pq[y][x].load(rq, row < n ? row * qs : kOutside, d + 32 * y + 8 * g, a.Dk);
+        pq[y][x].load(rq, row < n ? row * qs : kOutside, d + 32 * y + 8 * g, a.Dk);
       }
   };
   float log_decay = 0.f, beta = 0.f;
@@ -336,13 +336,13 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         pk[y][x].take(K[x]);
-        if (PAIRS) pq[y][x].take(Q[x]);
+        pq[y][x].take(Q[x]);
       }
 #pragma unroll
       for (int x = 0; x < 3; ++x) {
         const int ti = (x + 1) / 2, tj = x / 2;
         product(kk[x], K[tj], K[ti]);
-        if (PAIRS) product(qk[x], K[tj], Q[ti]);
+        product(qk[x], K[tj], Q[ti]);
       }
     }
   }
@@ -416,16 +416,14 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaArgs a) {
     }
   };
   put(T, kDeltaT);
-  if constexpr (PAIRS) {
 #pragma unroll
-    for (int x = 0; x < 3; ++x) {
-      const int ti = (x + 1) / 2, tj = x / 2;
-      *reinterpret_cast<f32x4*>(&A[16 * ti + l][16 * tj + 4 * g]) = qk[x];
-    }
-    *reinterpret_cast<f32x4*>(&A[l][16 + 4 * g]) = f32x4(0.f);
-    wave_sync();
-    put(A, kDeltaP);
+  for (int x = 0; x < 3; ++x) {
+    const int ti = (x + 1) / 2, tj = x / 2;
+    *reinterpret_cast<f32x4*>(&A[16 * ti + l][16 * tj + 4 * g]) = qk[x];
   }
+  *reinterpret_cast<f32x4*>(&A[l][16 + 4 * g]) = f32x4(0.f);
+  wave_sync();
+  put(A, kDeltaP);
 }
 
 // -- the walk along a sequence --------------------------------------------------------------------
@@ -572,12 +570,11 @@ struct Block {
     else if ((int)threadIdx.x < kRest + kFactors)
       f = reinterpret_cast<const u32x4*>(p + kDeltaVec)[threadIdx.x - kRest];
   }
-  __device__ __forceinline__ void store(char* matrices, char* vecs) const {
+  // (the factors lie behind the matrices: see Shape)
+  __device__ __forceinline__ void store(char* matrices) const {
 #pragma unroll
     for (int i = 0; i < kWhole; ++i) reinterpret_cast<u32x4*>(matrices)[i * 256 + threadIdx.x] = m[i];
-    // (the factors lie behind the matrices)
     if ((int)threadIdx.x < kRest + kFactors) reinterpret_cast<u32x4*>(matrices)[kWhole * 256 + threadIdx.x] = f;
-    (void)vecs;
   }
 };
 
@@ -793,6 +790,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : WALK == kOutputs && VEC 
   Rows<E, C, DKP, 256, VEC> rq(qs, a.Dk, false), rk(ks, a.Dk, false);
   Rows<E, C, 64, 256, VEC> rv(vs, vcols, false);
   Block<OUT> block;
+  static_assert(Sh::kVecs == Sh::kM + 16 * Block<OUT>::kUnits, "factors behind the matrices");
   // (in two parts: all at once they fill the queue of the unit's loads, and the waves wait to issue them)
   auto fetch = [&](int c) {
     const int n = c < w.hi ? min(C, w.s.len - c * C) : 0;
@@ -843,7 +841,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : WALK == kOutputs && VEC 
     rk.store(kt);
     if (OUT) rq.store(qt);
     rv.store(vt);
-    block.store(mt, vecs);
+    block.store(mt);
     __syncthreads();
     fetch(c + 1);
     if constexpr (WALK == kKeep) {
@@ -1086,6 +1084,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
   Rows<E, C, DKP, 256, VEC> rq(qs, a.Dk, false), rk(ks, a.Dk, false);
   Rows<E, C, 64, 256, VEC> ro(os, w.cols, false);
   Block<true> block;
+  static_assert(Sh::kVecs == Sh::kM + 16 * Block<true>::kUnits, "factors behind the matrices");
   auto fetch = [&](int c) {
     const int n = c < w.lo ? 0 : min(C, w.s.len - c * C);
     const int64_t t0 = n <= 0 ? 0 : (int64_t)c * C;
@@ -1119,7 +1118,7 @@ __global__ void __launch_bounds__(256, DKP == 256 ? 1 : 2) delta_reverse_kernel(
     rk.store(kt);
     rq.store(qt);
     ro.store(vt);
-    block.store(mt, vecs);
+    block.store(mt);
     __syncthreads();
     fetch(c - 1);
     if (!ENDS) {
@@ -1655,7 +1654,7 @@ hipError_t launch_shape(const DeltaArgs& a, bool backward, hipStream_t stream) {
   // (448 chunks and heads of 128, fp32: 12.5 us in fours, 10 alone)
   if (blocks > 0) {
     const bool alone = blocks <= 1024;
-    e = launch_kernel(delta_prepare_kernel<E, DKP, VEC, true>, alone ? blocks : (blocks + 3) / 4, 0, a, stream, alone ? 64 : 256);
+    e = launch_kernel(delta_prepare_kernel<E, DKP, VEC>, alone ? blocks : (blocks + 3) / 4, 0, a, stream, alone ? 64 : 256);
   }
   if (e == hipSuccess && split) {
     e = launch_kernel(delta_forward_kernel<E, DKP, VEC, kEnds>, pieces * (a.tiles + a.move_tiles), kLdsNarrow, a, stream);
