@@ -21,8 +21,8 @@ namespace {
 
 using namespace norm;
 
-// Maximum over rows of 16 lanes, the same in each of them.
-__device__ __forceinline__ float dpp_row_max(float x) {
+// Maximum over rows of 16 lanes, the same in each of them (by exchanges through LDS's network).
+__device__ __forceinline__ float max16(float x) {
 #pragma unroll
   for (int m = 1; m < 16; m *= 2) x = fmaxf(x, __shfl_xor(x, m));
   return x;
@@ -31,7 +31,7 @@ __device__ __forceinline__ float dpp_row_max(float x) {
 // ... over the TPR threads of a row (see row_sums).
 template <int TPR>
 __device__ __forceinline__ float row_max(float x, float* slot) {
-  x = dpp_row_max(x);
+  x = max16(x);
   if constexpr (TPR >= 64) {
     x = fmaxf(x, __shfl_xor(x, 16));
     x = fmaxf(x, __shfl_xor(x, 32));
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(BLOCK) rms_kernel(RmsArgs a) {
       } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          most[j] = dpp_row_max(most[j]);
+          most[j] = max16(most[j]);
           if (kLanes == 32) most[j] = fmaxf(most[j], __shfl_xor(most[j], 16));
         }
       }
