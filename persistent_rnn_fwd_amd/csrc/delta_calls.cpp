@@ -198,10 +198,11 @@ void plan_delta(DeltaArgs* a, prnnDataType_t type, bool backward, int compute_un
   a->move_tiles = (a->Dk + 63) / 64;
   // Segments: as many as give each compute unit 2 workgroups, of at least 4 chunks, and
   // no more than the root of the chunks (64 rows: twice that), since a step of the scan costs about
-  // as much as a chunk.  A split in 2 gains nothing.  Measured in 1 / 4 / 8 / 12 / 16
-  // segments: 32768 bf16 tokens of 32 heads of 128 2503 / 1303 / 1135 / 1121 / 1141 us,
-  // gradients of 3 x 1531 fp16 tokens of 6 heads of 96 x 80 339 / 234 / 218 / 214 / 238 (in
-  // 6 202), 4 x 256 fp32 tokens of 14 heads of 128 53 / 71 (in 4).
+  // as much as a chunk.  A split in 2 gains nothing.  Measured in 1 / 4 / 6 / 8 / 10 / 12 / 16
+  // segments: 32768 bf16 tokens of 32 heads of 128 (the rule: 8) 2481 / 1250 / 1126 / 1059 / 1134 /
+  // 1088 / 1142 us; gradients of 3 x 1531 fp16 tokens of 6 heads of 96 x 80 (the rule: 6) 342 / 238 / 204 /
+  // 218 / - / 210 / 243; 3001 packed fp16 rows of 16 heads of 64, the longest sequence 1463 (the rule:
+  // 10) 123 / 81 / 73 / 71 / 68; 4 x 256 fp32 tokens of 14 heads of 128 (the rule: 1) 48 / 64.
   const int64_t sequences = a->offsets != nullptr && a->T > 0 ? std::max<int64_t>(1, std::min<int64_t>(a->B, a->rows / a->T)) : a->B;
   const int64_t states = std::max<int64_t>(1, sequences * a->H * a->tiles);
   int64_t segments = std::min<int64_t>(2 * compute_units / states, (int64_t)(std::sqrt((double)a->chunks) * (a->dkp == 64 ? 2 : 1)));

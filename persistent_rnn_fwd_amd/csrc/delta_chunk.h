@@ -43,8 +43,9 @@
 // What bounds it.  The walk: a chunk's chain of products (96 for each wave, bf16 and
 // 128 rows, 1540 cycles), splitting of the state and of x (the most of 1700 cycles of vector
 // instructions) and LDS between them, 5600 cycles alone on a unit, of which a second
-// workgroup hides nearly half.  32768 tokens of 32 bf16 heads of 128: 1073 to 1089 us, of them the first
-// launch 166 (4.8 TB/s), ends and moves 530, the scan 27, the walk 490.  The gradients: what
+// workgroup hides nearly half.  32768 tokens of 32 bf16 heads of 128: 1059 to 1135 us, on one card or
+// another (traced one by one, at lower clocks: the first launch 166, 4.8 TB/s, ends and moves 530, the scan
+// 27, the walk 490).  The gradients: what
 // goes through memory, 8 x 2048 tokens of 16 bf16 heads of 128 782 to 824 us, of them the first launch
 // 60, the walks 155 and 205, the gradients' own launch 390 (1 GB read, one workgroup on a
 // unit).  Small calls: launches and first loads.

@@ -196,9 +196,11 @@ __global__ void __launch_bounds__(BLOCK) rms_kernel(RmsArgs a) {
   }
 }
 
-// Rows wider than the registers of a workgroup, or narrower than a vector: read
-// twice (8 bits: three times), the later times from the caches, element by
-// element.  A wave takes the groups that have a scale in turn.
+// Rows wider than the registers of a workgroup (16384 columns of 16 bits, 12288 of fp32), or
+// narrower than a vector: read twice (8 bits: three times), the later times from the
+// caches, element by element.  A wave takes the groups that have a scale in turn.  Simple,
+// not fast: 4096 x 20480 bf16 with a residual 275 us (2.4 TB/s; 16384 columns, by vectors, 104
+// us, 5.2 TB/s), in 8 bits 408, with a scale for 128 columns 459; 65536 x 4 bf16 180 us.
 template <class E, class P, bool EIGHT>
 __global__ void __launch_bounds__(1024) rms_wide_kernel(RmsArgs a) {
   typedef typename E::raw raw;
@@ -362,7 +364,9 @@ __global__ void __launch_bounds__(BLOCK) rms_backward_kernel(RmsArgs a) {
   }
 }
 
-// dx of rows wider than the registers of a workgroup, or narrower than a vector.
+// dx of rows wider than the registers of a workgroup (12288 columns), or narrower than a
+// vector.  With the weight's sums, which read x and dy once more: 4096 x 16384 bf16 with
+// the sum's gradient 259 us (2.1 TB/s; 12288 columns, by vectors, 83 us, 4.9 TB/s).
 template <class E, class P>
 __global__ void __launch_bounds__(1024) rms_backward_wide_kernel(RmsArgs a) {
   typedef typename E::raw raw;
@@ -463,8 +467,9 @@ hipError_t launch_rms_norm(const RmsArgs& a, prnnDataType_t type, prnnDataType_t
       typedef decltype(c) K;
       const int64_t sets = (a.M + K::block / K::tpr - 1) / (K::block / K::tpr);
       // Workgroups with a row or two each: those at work then are on neighbouring rows.  With 4 /
-      // 16 / 64 a unit: 16384 x 5760 bf16 in 8 bits 132 / 124 / 117 us, 8192 x 8192 fp32 205 /
-      // 203 / 193, 100000 x 513 bf16 90 / 86 / 80; 40000 x 1153 fp16 in 8 bits 66 / 67 / 72.
+      // 16 / 64 a unit: 16384 x 5760 bf16 with a residual, in 8 bits with a scale a row, 133 / 124 / 116
+      // us; 8192 x 8192 fp32 with a residual 199 / 199 / 189; 100000 x 513 bf16 45 / 42 / 44; 40000 x 1153
+      // fp16 in 8 bits with a scale for 128 columns 52 / 50 / 58 (1152 columns: 41 / 36 / 37).
       const int64_t most = 64ll * a.compute_units;
       const unsigned grid = (unsigned)(sets < most ? sets : most);
       if (eight)
